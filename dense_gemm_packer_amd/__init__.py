@@ -28,6 +28,8 @@ LDS_POISON_LIB_PATH = os.path.join(_HERE, "libdgp_lds_poison.so")
 BF16 = 0
 FP8_E4M3 = 1
 FP4_E2M1 = 2
+F16 = 3      # inputs of the quantising operators only
+F32 = 4
 SCALE_NONE = 0
 SCALE_TENSOR = 1
 SCALE_BLOCK128 = 2
@@ -58,7 +60,9 @@ class Config(ctypes.Structure):
 
 # Every symbol include/dgp.h and include/dgp_diag.h declare.
 EXPORTS = ("dgp_preshuffle_b", "dgp_unshuffle_b", "dgp_gemm_preshuffle", "dgp_splitk_workspace_bytes",
-           "dgp_gemm_preshuffle_splitk", "dgp_gemm_preshuffle_splitk_noalloc", "dgp_check_arch", "dgp_status_string", "dgp_last_error",
+           "dgp_gemm_preshuffle_splitk", "dgp_gemm_preshuffle_splitk_noalloc",
+           "dgp_quantize_workspace_bytes", "dgp_quantize", "dgp_quantize_b", "dgp_rmsnorm_quantize",
+           "dgp_swiglu_quantize", "dgp_check_arch", "dgp_status_string", "dgp_last_error",
            "dgp_tile_of_workgroup", "dgp_tile_map", "dgp_kernel_count", "dgp_kernel_info", "dgp_select_kernel",
            "dgp_probe_mfma_layout", "dgp_probe_mfma_scaled", "dgp_probe_lds_dma", "dgp_probe_lds_dma_narrow", "dgp_probe_copy",
            "dgp_probe_stream_read", "dgp_probe_mfma_peak", "dgp_lds_poison")
@@ -115,6 +119,11 @@ def _load(path: str) -> ctypes.CDLL:
                                        _sz, _vp, _vp],
         "dgp_gemm_preshuffle_splitk_noalloc": [_vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _int,
                                                _vp, _vp],
+        "dgp_quantize": [_vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _int, _vp, _sz, _vp],
+        "dgp_quantize_b": [_vp, _int, _vp, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp],
+        "dgp_rmsnorm_quantize": [_vp, _i64, _vp, _i64, _int, _vp, _int, ctypes.c_float, _vp, _vp, _vp, _vp, _i64,
+                                 _i64, _int, _vp],
+        "dgp_swiglu_quantize": [_vp, _i64, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _int, _vp],
         "dgp_check_arch": [ctypes.c_char_p],
         "dgp_tile_of_workgroup": [_i64, _i64, _i64, _i64, _int, _int, ctypes.POINTER(_i64)],
         "dgp_tile_map": [_i64, _i64, _i64, _int, _int, _vp, _i64],
@@ -136,6 +145,8 @@ def _load(path: str) -> ctypes.CDLL:
         f.restype = _int
     L.dgp_splitk_workspace_bytes.argtypes = [_i64, _i64, _int]
     L.dgp_splitk_workspace_bytes.restype = _sz
+    L.dgp_quantize_workspace_bytes.argtypes = [_i64, _int]
+    L.dgp_quantize_workspace_bytes.restype = _sz
     L.dgp_status_string.argtypes = [_int]
     L.dgp_status_string.restype = ctypes.c_char_p
     L.dgp_last_error.argtypes = []
@@ -394,6 +405,201 @@ def gemm_preshuffle_splitk_noalloc(A: torch.Tensor, Bs: torch.Tensor, split_k: i
                                                     _ptr(sA), _ptr(sB), split_k, _config(config),
                                                     _stream_handle(stream)))
     return out
+
+
+# ------------------------------------------- operators that write an operand
+
+_INPUT = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+_CODES = {SCALE_NONE: torch.bfloat16, SCALE_TENSOR: torch.float8_e4m3fn, SCALE_BLOCK128: torch.float8_e4m3fn,
+          SCALE_MX128: torch.float8_e4m3fn, SCALE_MX32: torch.float4_e2m1fn_x2}
+_SCALES = {SCALE_TENSOR: torch.float32, SCALE_BLOCK128: torch.float32, SCALE_MX128: torch.uint8,
+           SCALE_MX32: torch.uint8}
+
+
+def input_code(t: torch.Tensor) -> int:
+    code = _INPUT.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported input type {t.dtype} (bfloat16, float16 or float32)")
+    return code
+
+
+def _rows(t: torch.Tensor, what: str, shape=None, like: torch.Tensor | None = None) -> int:
+    """Checks a strided [M][K] input on the device; returns its row stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D (got {t.dim()}-D)")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must be {tuple(shape)} (got {tuple(t.shape)})")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what} is {t.dtype} on {t.device}, X {like.dtype} on {like.device}")
+    M, K = t.shape
+    if K > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    if M <= 1:
+        return K
+    ld = t.stride(0)
+    if ld < K:
+        raise ValueError(f"{what}: rows overlap (stride {ld}, {K} elements)")
+    return ld
+
+
+def _dense(t: torch.Tensor, dtype, shape, X: torch.Tensor, what: str) -> None:
+    _dev(t, what)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be a {tuple(shape)} {dtype} tensor (got {tuple(t.shape)} {t.dtype})")
+    if t.device != X.device:
+        raise ValueError(f"{what} is on {t.device}, the input on {X.device}")
+
+
+def _mode(scale_mode: int, allow_none: bool) -> None:
+    if scale_mode not in _CODES or (scale_mode == SCALE_NONE and not allow_none):
+        raise DgpError(5, f"scale mode {scale_mode} is not one this operator writes")
+
+
+def _operand_out(X, M, K, mode, scale, out, scales, stream):
+    """Checks or allocates the codes and scales of an [M][K] operand; returns
+    (Q, S) (S: the given scale, or None without scales)."""
+    block = {SCALE_BLOCK128: 128, SCALE_MX128: 128, SCALE_MX32: 32}.get(mode)
+    qshape = (M, K // 2) if mode == SCALE_MX32 else (M, K)
+    sshape = (1,) if block is None else (M, K // block)
+    if scale is not None:
+        if mode != SCALE_TENSOR:
+            raise DgpError(5, "a given scale goes with SCALE_TENSOR only")
+        if scales is not None:
+            raise ValueError("scale is given: there are no scales to write")
+        if scale.numel() != 1:
+            raise ValueError(f"scale must hold one value (got {scale.numel()})")
+        _dense(scale, torch.float32, scale.shape, X, "scale")
+    if out is not None:
+        _dense(out, _CODES[mode], qshape, X, "out")
+    if scales is not None:
+        if mode == SCALE_NONE:
+            raise ValueError("SCALE_NONE writes no scales")
+        _dense(scales, _SCALES[mode], sshape, X, "scales")
+    if out is None or (scales is None and scale is None and mode != SCALE_NONE):
+        with _alloc_stream(stream):
+            if out is None:
+                out = torch.empty(qshape, dtype=_CODES[mode], device=X.device)
+            if scales is None and scale is None and mode != SCALE_NONE:
+                scales = torch.empty(sshape, dtype=_SCALES[mode], device=X.device)
+    return out, scale if scale is not None else scales
+
+
+def _enqueue(X: torch.Tensor, stream, fn, *args) -> None:
+    """fn(*args, stream) with X's device current: on the given stream, or on
+    the current stream of that device."""
+    index = X.device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _enqueue(X, stream, fn, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    elif stream.device != X.device:
+        raise ValueError(f"stream is on {stream.device}, the input on {X.device}")
+    _check(fn(*args, stream.cuda_stream))
+
+
+def quantize(X: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+             scales: torch.Tensor | None = None, stream=None):
+    """(Q, S): the rows of X ([M][K] bfloat16, float16 or float32; the row
+    stride is free) as the A operand of a quantised product (dgp_quantize).
+    SCALE_TENSOR measures the scale, or takes the given one (then S is it)."""
+    ld = _rows(X, "X")
+    _mode(scale_mode, False)
+    M, K = X.shape
+    Q, S = _operand_out(X, M, K, scale_mode, scale, out, scales, stream)
+    ws = None
+    if scale_mode == SCALE_TENSOR and scale is None:
+        with _alloc_stream(stream):
+            ws = torch.empty(lib().dgp_quantize_workspace_bytes(1, scale_mode) // 4, dtype=torch.float32,
+                             device=X.device)
+    _enqueue(X, stream, lib().dgp_quantize, X.data_ptr(), ld, input_code(X), Q.data_ptr(),
+             None if scale is not None else S.data_ptr(), _ptr(scale), M, K, scale_mode, _ptr(ws),
+             0 if ws is None else ws.numel() * 4)
+    return Q, S
+
+
+def quantize_b(B: torch.Tensor, scale_mode: int, out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+               stream=None):
+    """(Bs, sB): a weight [N][K], or a stack [E][N][K], quantised and
+    preshuffled in one pass (dgp_quantize_b): Bs as preshuffle_b of the codes,
+    sB as the product reads it ([E][...] for a stack; SCALE_TENSOR: one value
+    per weight, BLOCK128: 128 x 128 blocks)."""
+    _dev(B, "B")
+    if B.dim() not in (2, 3):
+        raise ValueError(f"B must be 2-D or 3-D (got {B.dim()}-D)")
+    _mode(scale_mode, False)
+    lead = tuple(B.shape[:-2])
+    E = B.shape[0] if lead else 1
+    N, K = B.shape[-2:]
+    code = input_code(B)
+    qshape = lead + ((N, K // 2) if scale_mode == SCALE_MX32 else (N, K))
+    sshape = {SCALE_TENSOR: lead or (1,), SCALE_BLOCK128: lead + (N // 128, K // 128),
+              SCALE_MX128: lead + (N, K // 128), SCALE_MX32: lead + (N, K // 32)}[scale_mode]
+    if out is not None:
+        _dense(out, _CODES[scale_mode], qshape, B, "out")
+    if scales is not None:
+        _dense(scales, _SCALES[scale_mode], sshape, B, "scales")
+    need = lib().dgp_quantize_workspace_bytes(E, scale_mode)
+    with _alloc_stream(stream):
+        if out is None:
+            out = torch.empty(qshape, dtype=_CODES[scale_mode], device=B.device)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=_SCALES[scale_mode], device=B.device)
+        ws = torch.empty(need // 4, dtype=torch.float32, device=B.device) if need else None
+    _enqueue(B, stream, lib().dgp_quantize_b, B.data_ptr(), code, out.data_ptr(), scales.data_ptr(), E, N, K,
+             scale_mode, _ptr(ws), need)
+    return out, scales
+
+
+def rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, scale_mode: int, residual: torch.Tensor | None = None,
+                     eps: float = 1e-6, scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     scales: torch.Tensor | None = None, residual_out: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of h = X (+ residual) over each row, times weight,
+    written as a product's A operand (dgp_rmsnorm_quantize).  Returns (Q, S),
+    or (Q, S, H) with a residual: H = h in X's type, the residual stream's new
+    value (residual_out may be the residual itself).  SCALE_NONE: Q is
+    bfloat16 and S None; SCALE_TENSOR takes a given scale."""
+    ldx = _rows(X, "X")
+    _mode(scale_mode, True)
+    M, K = X.shape
+    code = input_code(X)
+    ldr = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", X.shape, X)
+    _dev(weight, "weight")
+    if weight.dim() != 1 or weight.shape[0] != K or weight.dtype not in (X.dtype, torch.float32):
+        raise ValueError(f"weight must hold {K} values of {X.dtype} or float32 (got {tuple(weight.shape)} {weight.dtype})")
+    _same_device(X, (weight, "weight"))
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        _dense(residual_out, X.dtype, X.shape, X, "residual_out")
+    Q, S = _operand_out(X, M, K, scale_mode, scale, out, scales, stream)
+    if residual is not None and residual_out is None:
+        with _alloc_stream(stream):
+            residual_out = torch.empty((M, K), dtype=X.dtype, device=X.device)
+    _enqueue(X, stream, lib().dgp_rmsnorm_quantize, X.data_ptr(), ldx, _ptr(residual), ldr, code, weight.data_ptr(),
+             input_code(weight), eps, Q.data_ptr(), None if scale is not None else _ptr(S), _ptr(scale),
+             _ptr(residual_out), M, K, scale_mode)
+    return (Q, S) if residual is None else (Q, S, residual_out)
+
+
+def swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """(Q, S): gate / (1 + exp(-gate)) * up written as a product's A operand
+    (dgp_swiglu_quantize).  gate and up are [M][K] with free row strides: the
+    two halves of one product's columns are C[:, :K] and C[:, K:].  SCALE_NONE:
+    Q is bfloat16 and S None; SCALE_TENSOR takes a given scale."""
+    ldg = _rows(gate, "gate")
+    ldu = _rows(up, "up", gate.shape, gate)
+    _mode(scale_mode, True)
+    M, K = gate.shape
+    Q, S = _operand_out(gate, M, K, scale_mode, scale, out, scales, stream)
+    _enqueue(gate, stream, lib().dgp_swiglu_quantize, gate.data_ptr(), ldg, up.data_ptr(), ldu, input_code(gate),
+             Q.data_ptr(), None if scale is not None else _ptr(S), _ptr(scale), M, K, scale_mode)
+    return Q, S
 
 
 def check_arch(name: str) -> bool:

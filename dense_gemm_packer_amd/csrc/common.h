@@ -24,6 +24,8 @@ constexpr int kNumXcd = 8;          // gfx950: 8 XCDs, workgroups dealt round-ro
 constexpr int kDtypeBf16 = 0;
 constexpr int kDtypeFp8 = 1;
 constexpr int kDtypeFp4 = 2;         // OCP E2M1, two per byte
+constexpr int kTypeF16 = 3;          // inputs of the quantising operators only
+constexpr int kTypeF32 = 4;
 constexpr int kScaleNone = 0;
 constexpr int kScaleTensor = 1;
 constexpr int kScaleBlock = 2;

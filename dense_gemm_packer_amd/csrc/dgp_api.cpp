@@ -579,6 +579,88 @@ dgp_status shuffle(const void *src, void *dst, int64_t N, int64_t K, int dtype, 
     return hip_status(launch_preshuffle(src, dst, N, Kb, inverse, (hipStream_t)stream), "preshuffle launch");
 }
 
+// ------------------------------------------------- quantising operators
+
+// Rules shared by the operators that write a GEMM operand of `M` rows and `K`
+// elements from rows of type x_type: types, sizes, the operand's own K rule.
+int input_size(int x_type) { return x_type == DGP_F32 ? 4 : (x_type == DGP_BF16 || x_type == DGP_F16) ? 2 : 0; }
+
+dgp_status check_operand(int x_type, int64_t M, int64_t K, int scale_mode, bool allow_none)
+{
+    if (!input_size(x_type))
+        return fail(DGP_ERR_DTYPE, "input type %d is not DGP_BF16, DGP_F16 or DGP_F32", x_type);
+    if (scale_mode < (allow_none ? DGP_SCALE_NONE : DGP_SCALE_TENSOR) || scale_mode > DGP_SCALE_MX32)
+        return fail(DGP_ERR_SCALE_MODE, "scale mode %d is not one this operator writes", scale_mode);
+    if (M < 0 || K < 0)
+        return fail(DGP_ERR_SHAPE, "negative size M=%lld K=%lld", (long long)M, (long long)K);
+    const int dtype = scale_mode == DGP_SCALE_NONE ? DGP_BF16 : scale_mode == DGP_SCALE_MX32 ? DGP_FP4_E2M1 : DGP_FP8_E4M3;
+    if (K % 2 != 0 || row_bytes(dtype, K) % 128 != 0)
+        return fail(DGP_ERR_SHAPE, "K=%lld: the operand's rows are not a multiple of 128 bytes", (long long)K);
+    if (row_bytes(dtype, K) > kMaxRowBytes)
+        return fail(DGP_ERR_SHAPE, "operand rows of %lld bytes exceed %lld", (long long)row_bytes(dtype, K),
+                    (long long)kMaxRowBytes);
+    if (M > INT32_MAX / 2)
+        return fail(DGP_ERR_SHAPE, "M too large");
+    return DGP_OK;
+}
+
+// A strided input: rows ld elements apart, every row 16-byte aligned.
+dgp_status check_rows(const void *p, int64_t ld, int64_t K, int x_type, const char *what)
+{
+    if (!p)
+        return fail(DGP_ERR_NULL, "%s is NULL", what);
+    if (ld < K)
+        return fail(DGP_ERR_SHAPE, "%s: row stride %lld below K=%lld", what, (long long)ld, (long long)K);
+    if (!aligned16(p) || (ld * input_size(x_type)) % 16 != 0)
+        return fail(DGP_ERR_ALIGN, "%s: rows must be 16-byte aligned", what);
+    return DGP_OK;
+}
+
+// Codes and scales: Q 16-byte aligned; S present where the mode writes block
+// scales, 4-byte aligned where they are fp32.
+dgp_status check_codes(const void *Q, const void *S, const float *scale, int scale_mode)
+{
+    if (!Q)
+        return fail(DGP_ERR_NULL, "Q is NULL");
+    if (!aligned16(Q))
+        return fail(DGP_ERR_ALIGN, "Q is not 16-byte aligned");
+    const bool writes = scale_mode != DGP_SCALE_NONE && !(scale_mode == DGP_SCALE_TENSOR && scale);
+    if (writes && !S)
+        return fail(DGP_ERR_NULL, "S is NULL");
+    if (scale && scale_mode != DGP_SCALE_TENSOR)
+        return fail(DGP_ERR_SCALE_MODE, "a given scale goes with DGP_SCALE_TENSOR only");
+    if ((scale_mode == DGP_SCALE_TENSOR || scale_mode == DGP_SCALE_BLOCK128) && (((uintptr_t)S | (uintptr_t)scale) & 3u))
+        return fail(DGP_ERR_ALIGN, "fp32 scales must be 4-byte aligned");
+    return DGP_OK;
+}
+
+dgp_status check_amax_workspace(int64_t groups, const float *ws, size_t ws_bytes)
+{
+    const size_t need = dgp_quantize_workspace_bytes(groups, DGP_SCALE_TENSOR);
+    if (!ws)
+        return fail(DGP_ERR_WORKSPACE, "DGP_SCALE_TENSOR without a given scale needs a workspace");
+    if ((uintptr_t)ws & 3u)
+        return fail(DGP_ERR_ALIGN, "workspace is not 4-byte aligned");
+    if (ws_bytes < need)
+        return fail(DGP_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+    return DGP_OK;
+}
+
+// Workgroups per matrix for the largest-magnitude pass: four 2 KiB (fp32: 4
+// KiB) pieces each, at most kAmaxParts.
+int amax_parts(int64_t M, int64_t K)
+{
+    const int64_t n = (M * K / 8 + 1023) / 1024;
+    return (int)(n < 1 ? 1 : n > kAmaxParts ? kAmaxParts : n);
+}
+
+#define DGP_TRY(expr)                                                                          \
+    do {                                                                                       \
+        const dgp_status st_ = (expr);                                                         \
+        if (st_ != DGP_OK)                                                                     \
+            return st_;                                                                        \
+    } while (0)
+
 }  // namespace
 
 // ====================================================================== ABI
@@ -626,6 +708,114 @@ dgp_status dgp_gemm_preshuffle_splitk_noalloc(const void *A, const void *Bs, voi
     GemmCall c{A, Bs, C, M, N, K, dtype, scale_mode, sA, sB, split_k, nullptr, 0, cfg};
     c.lib_scratch = true;
     return run_gemm(c, (hipStream_t)stream);
+}
+
+size_t dgp_quantize_workspace_bytes(int64_t E, int scale_mode)
+{
+    return scale_mode == DGP_SCALE_TENSOR && E > 0 ? (size_t)E * kAmaxParts * sizeof(uint32_t) : 0;
+}
+
+dgp_status dgp_quantize(const void *X, int64_t ldx, int x_type, void *Q, void *S, const float *scale, int64_t M,
+                        int64_t K, int scale_mode, float *ws, size_t ws_bytes, void *stream)
+{
+    DGP_TRY(check_operand(x_type, M, K, scale_mode, false));
+    if (M == 0 || K == 0)
+        return ok();
+    DGP_TRY(check_rows(X, ldx, K, x_type, "X"));
+    DGP_TRY(check_codes(Q, S, scale, scale_mode));
+    const bool measure = scale_mode == DGP_SCALE_TENSOR && !scale;
+    if (measure)
+        DGP_TRY(check_amax_workspace(1, ws, ws_bytes));
+    DGP_TRY(check_device_arch());
+    RowQuantArgs a{};
+    a.X = X, a.Q = Q, a.S = S, a.scale = scale;
+    a.ldx = a.ldu = ldx, a.M = M, a.K = K;
+    if (measure) {
+        a.nparts = amax_parts(M, K);
+        a.parts = (const uint32_t *)ws;
+        DGP_TRY(hip_status(launch_amax(X, ldx, x_type, 1, M, K, a.nparts, (uint32_t *)ws, (hipStream_t)stream),
+                           "largest-magnitude launch"));
+    }
+    return hip_status(launch_row_quant(a, x_type, scale_mode, false, (hipStream_t)stream), "quantisation launch");
+}
+
+dgp_status dgp_quantize_b(const void *B, int x_type, void *Bs, void *sB, int64_t E, int64_t N, int64_t K,
+                          int scale_mode, float *ws, size_t ws_bytes, void *stream)
+{
+    DGP_TRY(check_operand(x_type, 0, K, scale_mode, false));
+    if (E < 0 || N < 0 || E > 65535 || N > INT32_MAX / 2 || E * N > INT32_MAX / 2)
+        return fail(DGP_ERR_SHAPE, "E=%lld matrices of N=%lld rows", (long long)E, (long long)N);
+    if (N % 16 != 0)
+        return fail(DGP_ERR_SHAPE, "N=%lld is not a multiple of 16 (preshuffle block rows)", (long long)N);
+    if (scale_mode == DGP_SCALE_BLOCK128 && N % 128 != 0)
+        return fail(DGP_ERR_SHAPE, "blockscale needs N %% 128 == 0 (N=%lld)", (long long)N);
+    if (E * N / 16 * (K / 128) > INT32_MAX)
+        return fail(DGP_ERR_SHAPE, "too many operand blocks");
+    if (E == 0 || N == 0 || K == 0)
+        return ok();
+    DGP_TRY(check_rows(B, K, K, x_type, "B"));
+    DGP_TRY(check_codes(Bs, sB, nullptr, scale_mode));
+    const bool measure = scale_mode == DGP_SCALE_TENSOR;
+    if (measure)
+        DGP_TRY(check_amax_workspace(E, ws, ws_bytes));
+    DGP_TRY(check_device_arch());
+    WeightQuantArgs a{};
+    a.B = B, a.Q = Bs, a.S = sB;
+    a.rows = E * N, a.N = N, a.K = K;
+    if (measure) {
+        a.nparts = amax_parts(N, K);
+        a.parts = (const uint32_t *)ws;
+        DGP_TRY(hip_status(launch_amax(B, K, x_type, E, N, K, a.nparts, (uint32_t *)ws, (hipStream_t)stream),
+                           "largest-magnitude launch"));
+    }
+    return hip_status(launch_quantize_b(a, x_type, scale_mode, (hipStream_t)stream), "weight quantisation launch");
+}
+
+dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64_t ldr, int x_type, const void *W,
+                                int w_type, float eps, void *Q, void *S, const float *scale, void *H, int64_t M,
+                                int64_t K, int scale_mode, void *stream)
+{
+    DGP_TRY(check_operand(x_type, M, K, scale_mode, true));
+    if (w_type != x_type && w_type != DGP_F32)
+        return fail(DGP_ERR_DTYPE, "weight type %d is neither X's type nor DGP_F32", w_type);
+    if (!(eps >= 0.0f) || !(eps <= 3.0e38f))
+        return fail(DGP_ERR_SHAPE, "eps must be finite and not negative");
+    if (M == 0 || K == 0)
+        return ok();
+    DGP_TRY(check_rows(X, ldx, K, x_type, "X"));
+    if (R)
+        DGP_TRY(check_rows(R, ldr, K, x_type, "residual"));
+    if (!W)
+        return fail(DGP_ERR_NULL, "weight is NULL");
+    if (!aligned16(W) || !aligned16(H))
+        return fail(DGP_ERR_ALIGN, "weight and residual output must be 16-byte aligned");
+    if (scale_mode == DGP_SCALE_TENSOR && !scale)
+        return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
+    DGP_TRY(check_codes(Q, S, scale, scale_mode));
+    DGP_TRY(check_device_arch());
+    NormArgs a{};
+    a.X = X, a.R = R, a.W = W, a.Q = Q, a.S = S, a.H = H, a.scale = scale;
+    a.ldx = ldx, a.ldr = ldr, a.M = M, a.K = K;
+    a.eps = eps, a.wt = w_type;
+    return hip_status(launch_rmsnorm(a, x_type, scale_mode, (hipStream_t)stream), "norm launch");
+}
+
+dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_t ldu, int x_type, void *Q, void *S,
+                               const float *scale, int64_t M, int64_t K, int scale_mode, void *stream)
+{
+    DGP_TRY(check_operand(x_type, M, K, scale_mode, true));
+    if (M == 0 || K == 0)
+        return ok();
+    DGP_TRY(check_rows(G, ldg, K, x_type, "gate"));
+    DGP_TRY(check_rows(U, ldu, K, x_type, "up"));
+    if (scale_mode == DGP_SCALE_TENSOR && !scale)
+        return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
+    DGP_TRY(check_codes(Q, S, scale, scale_mode));
+    DGP_TRY(check_device_arch());
+    RowQuantArgs a{};
+    a.X = G, a.U = U, a.Q = Q, a.S = S, a.scale = scale;
+    a.ldx = ldg, a.ldu = ldu, a.M = M, a.K = K;
+    return hip_status(launch_row_quant(a, x_type, scale_mode, true, (hipStream_t)stream), "gated activation launch");
 }
 
 dgp_status dgp_check_arch(const char *name)

@@ -82,6 +82,41 @@ hipError_t launch_preshuffle(const void *src, void *dst, int64_t N, int64_t Kb, 
 hipError_t launch_splitk_reduce(const float *ws, void *C, int64_t M, int64_t N, int splits,
                                 hipStream_t stream);
 
+// Operators that write a GEMM operand (quantize.hip).  Input types are
+// kDtypeBf16, kTypeF16 or kTypeF32; strides are in elements.
+struct RowQuantArgs {
+    const void *X;          // [M][K] rows ldx apart (the gated activation: the gate)
+    const void *U;          // the gated activation's second factor, rows ldu apart
+    void *Q;                // [M][K] codes (bf16 without scales)
+    void *S;                // scales, row-major
+    const float *scale;     // per tensor: the given scale, where parts is NULL
+    const uint32_t *parts;  // per tensor: nparts <= 256 partial maxima (bits of |x|)
+    int64_t ldx, ldu, M, K;
+    int nparts;
+};
+struct WeightQuantArgs {
+    const void *B;          // [rows][K], rows = a stack of matrices of N rows
+    void *Q;                // preshuffled codes
+    void *S;                // scales, row-major
+    const uint32_t *parts;  // per tensor: nparts partial maxima per matrix
+    int64_t rows, N, K;
+    int nparts;
+};
+struct NormArgs {
+    const void *X, *R, *W;  // R: residual or NULL, rows ldr apart
+    void *Q, *S, *H;        // H: the residual stream's new value ([M][K]) or NULL
+    const float *scale;
+    int64_t ldx, ldr, M, K;
+    float eps;
+    int wt;                 // W's type: X's or kTypeF32
+};
+constexpr int kAmaxParts = 256;   // most partial maxima per matrix
+hipError_t launch_row_quant(const RowQuantArgs &a, int x_type, int mode, bool gated, hipStream_t s);
+hipError_t launch_amax(const void *X, int64_t ldx, int x_type, int64_t groups, int64_t M, int64_t K, int parts_per_group,
+                       uint32_t *parts, hipStream_t s);
+hipError_t launch_quantize_b(const WeightQuantArgs &a, int x_type, int mode, hipStream_t s);
+hipError_t launch_rmsnorm(const NormArgs &a, int x_type, int mode, hipStream_t s);
+
 // Probes (probe.hip).
 hipError_t launch_probe_mfma(int which, const void *a, const void *b, float *out, hipStream_t s);
 hipError_t launch_probe_lds_dma(const void *src, const int32_t *perm, void *dst, hipStream_t s);

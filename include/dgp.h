@@ -67,8 +67,10 @@ typedef enum dgp_status {
 } dgp_status;
 
 /* Element types.  K always counts elements; a row of DGP_FP4_E2M1 (OCP E2M1,
- * two per byte, element 2j in the low nibble of byte j) is K/2 bytes. */
-typedef enum dgp_dtype { DGP_BF16 = 0, DGP_FP8_E4M3 = 1, DGP_FP4_E2M1 = 2 } dgp_dtype;
+ * two per byte, element 2j in the low nibble of byte j) is K/2 bytes.
+ * DGP_F16 and DGP_F32 (IEEE binary16 and binary32) are input types of the
+ * quantising operators only. */
+typedef enum dgp_dtype { DGP_BF16 = 0, DGP_FP8_E4M3 = 1, DGP_FP4_E2M1 = 2, DGP_F16 = 3, DGP_F32 = 4 } dgp_dtype;
 
 /* DGP_SCALE_NONE: bf16 only; sA, sB unused.  DGP_SCALE_TENSOR: fp8 only; sA,
  * sB each point to one fp32 and C = bf16(acc * (sA*sB)).  DGP_SCALE_BLOCK128:
@@ -288,6 +290,66 @@ dgp_status dgp_gemm_preshuffle_splitk_noalloc(const void *A, const void *Bs, voi
                                               int64_t K, int dtype, int scale_mode, const void *sA,
                                               const void *sB, int split_k, const dgp_config *cfg,
                                               void *stream);
+
+/*
+ * Operators that write an operand of the product
+ *
+ * Each makes one operand A (dgp_quantize_b: a weight) in the form that a scale
+ * mode takes, from rows of `x_type` (DGP_BF16, DGP_F16 or DGP_F32), in fp32,
+ * with one rounding to nearest even at the end:
+ *   DGP_SCALE_NONE      Q is bf16 [M][K]; S unused.  (Not dgp_quantize.)
+ *   DGP_SCALE_TENSOR    Q is e4m3, one fp32 scale s: Q = e4m3(x * (1/s)).
+ *   DGP_SCALE_BLOCK128  Q is e4m3, S fp32 [M][K/128].
+ *   DGP_SCALE_MX128     Q is e4m3, S E8M0 [M][K/128].
+ *   DGP_SCALE_MX32      Q is E2M1 [M][K/2 bytes], S E8M0 [M][K/32].
+ * With amax the largest magnitude of a block: an fp32 scale is max(amax / 448,
+ * 2^-126); an E8M0 scale of e4m3 is the smallest power of two with amax <= 448
+ * scales; an E8M0 scale of E2M1 is 2^(floor(log2 amax) - 2), values beyond 6
+ * saturating (OCP MX 1.0); the exponent is never below 2^-127, which an
+ * all-zero block gets.  A block that holds a NaN or an infinity gets a NaN
+ * scale (E8M0 255), and its codes are NaN (E2M1: 0).  With a given per-tensor
+ * scale, values beyond 448 scales saturate, infinities included, and a NaN
+ * becomes the NaN code; a scale that is zero, negative or not finite is the
+ * caller's to avoid.
+ *
+ * Inputs are rows ld* elements apart (ld* >= K), each 16-byte aligned; Q, S
+ * and H are dense.  K as the product takes it: rows of Q a multiple of 128
+ * bytes, at most 2^23.  M = 0 or K = 0 is a no-op (no scale is written: such
+ * a product reads none).
+ */
+
+/* Bytes of workspace that dgp_quantize (E = 1) and dgp_quantize_b need: 1 KiB
+ * per matrix for DGP_SCALE_TENSOR, 0 for the other modes. */
+size_t dgp_quantize_workspace_bytes(int64_t E, int scale_mode);
+
+/* dgp_quantize -- X [M][K] -> codes Q and scales S.  DGP_SCALE_TENSOR: with
+ * `scale` NULL the scale is measured (a pass over X of its own, through ws)
+ * and written to S; else `scale` points to it and S is not written. */
+dgp_status dgp_quantize(const void *X, int64_t ldx, int x_type, void *Q, void *S, const float *scale, int64_t M,
+                        int64_t K, int scale_mode, float *ws, size_t ws_bytes, void *stream);
+
+/* dgp_quantize_b -- E weights [N][K] (dense, E = 1 for one) -> Bs, each weight
+ * in the layout of dgp_preshuffle_b (it is not to be shuffled again), and sB
+ * as the product reads it: one fp32 per weight, fp32 [E][N/128][K/128] over
+ * 128 x 128 blocks, or E8M0 [E][N][K/128] or [E][N][K/32].  N % 16 == 0
+ * (blockscale: N % 128 == 0). */
+dgp_status dgp_quantize_b(const void *B, int x_type, void *Bs, void *sB, int64_t E, int64_t N, int64_t K,
+                          int scale_mode, float *ws, size_t ws_bytes, void *stream);
+
+/* dgp_rmsnorm_quantize -- h = x + r (r: the residual's rows, or R NULL: h = x),
+ * y = h / sqrt(mean(h^2) + eps) * w over each row; Q, S from y.  H, where not
+ * NULL, receives h rounded to x_type ([M][K]; y comes from the unrounded sum);
+ * it may be X or R itself where their rows are dense (an update in place).
+ * w has K values of x_type or DGP_F32.  DGP_SCALE_TENSOR takes a given scale. */
+dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64_t ldr, int x_type, const void *W,
+                                int w_type, float eps, void *Q, void *S, const float *scale, void *H, int64_t M,
+                                int64_t K, int scale_mode, void *stream);
+
+/* dgp_swiglu_quantize -- y = g / (1 + exp(-g)) * u elementwise; Q, S from y.
+ * The two halves of one product's columns are g and u with ldg = ldu = 2 K.
+ * DGP_SCALE_TENSOR takes a given scale. */
+dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_t ldu, int x_type, void *Q, void *S,
+                               const float *scale, int64_t M, int64_t K, int scale_mode, void *stream);
 
 /* dgp_check_arch -- DGP_OK if `gcn_arch_name` (as reported by the HIP device
  * properties, e.g. "gfx950:sramecc+:xnack-") names gfx950, else DGP_ERR_ARCH.
