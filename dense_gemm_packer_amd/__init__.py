@@ -62,7 +62,7 @@ class Config(ctypes.Structure):
 EXPORTS = ("dgp_preshuffle_b", "dgp_unshuffle_b", "dgp_gemm_preshuffle", "dgp_splitk_workspace_bytes",
            "dgp_gemm_preshuffle_splitk", "dgp_gemm_preshuffle_splitk_noalloc",
            "dgp_quantize_workspace_bytes", "dgp_quantize", "dgp_quantize_b", "dgp_rmsnorm_quantize",
-           "dgp_swiglu_quantize", "dgp_check_arch", "dgp_status_string", "dgp_last_error",
+           "dgp_swiglu_quantize", "dgp_gemm_preshuffle_grouped", "dgp_check_arch", "dgp_status_string", "dgp_last_error",
            "dgp_tile_of_workgroup", "dgp_tile_map", "dgp_kernel_count", "dgp_kernel_info", "dgp_select_kernel",
            "dgp_probe_mfma_layout", "dgp_probe_mfma_scaled", "dgp_probe_lds_dma", "dgp_probe_lds_dma_narrow", "dgp_probe_copy",
            "dgp_probe_stream_read", "dgp_probe_mfma_peak", "dgp_lds_poison")
@@ -119,6 +119,8 @@ def _load(path: str) -> ctypes.CDLL:
                                        _sz, _vp, _vp],
         "dgp_gemm_preshuffle_splitk_noalloc": [_vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _int,
                                                _vp, _vp],
+        "dgp_gemm_preshuffle_grouped": [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _int, _int, _vp, _vp,
+                                        _vp, _vp],
         "dgp_quantize": [_vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _int, _vp, _sz, _vp],
         "dgp_quantize_b": [_vp, _int, _vp, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp],
         "dgp_rmsnorm_quantize": [_vp, _i64, _vp, _i64, _int, _vp, _int, ctypes.c_float, _vp, _vp, _vp, _vp, _i64,
@@ -379,6 +381,62 @@ def gemm_preshuffle_splitk(A: torch.Tensor, Bs: torch.Tensor, split_k: int,
     _check(lib().dgp_gemm_preshuffle_splitk(_ptr(A), _ptr(Bs), _ptr(out), M, N, K, dtype_code(A), mode,
                                             _ptr(sA), _ptr(sB), split_k, _ptr(workspace), ws_bytes,
                                             _config(config), _stream_handle(stream)))
+    return out
+
+
+def check_grouped_operands(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Tensor, sA, sB, mode: int, rows,
+                           out) -> None:
+    """The shape and dtype checks of a grouped product that the C ABI cannot
+    make.  Raises ValueError before any launch."""
+    if A.dim() != 2 or Bs.dim() != 3:
+        raise ValueError(f"A must be 2-D and Bs 3-D (got {A.dim()}-D and {Bs.dim()}-D)")
+    if Bs.dtype != A.dtype:
+        raise ValueError(f"Bs is {Bs.dtype}, A is {A.dtype}: both operands take one element type")
+    E, N = Bs.shape[:2]
+    K = k_elements(A)
+    if Bs.shape[2] != A.shape[1]:
+        raise ValueError(f"Bs holds {Bs.shape[2] * K // max(A.shape[1], 1)} elements per row, A {K}")
+    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,):
+        raise ValueError(f"offsets must be {E + 1} int32 values (got {tuple(offsets.shape)} {offsets.dtype})")
+    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1):
+        raise ValueError(f"rows must be a 1-D int32 tensor (got {tuple(rows.shape)} {rows.dtype})")
+    M = A.shape[0] if rows is None else rows.shape[0]
+    if out is not None and (out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N)):
+        raise ValueError(f"out must be a ({M}, {N}) bfloat16 tensor (got {tuple(out.shape)} {out.dtype})")
+    want = scale_shapes(mode, A.shape[0], N, K)
+    if want is None:
+        return
+    dt, na, nb = want
+    for t, n, what in ((sA, na, "sA"), (sB, E * nb, "sB")):
+        if t is not None and (t.dtype != dt or t.numel() != n):
+            raise ValueError(f"{what} must hold {n} {dt} values for this scale mode and shape "
+                             f"(got {t.numel()} {t.dtype})")
+
+
+def gemm_preshuffle_grouped(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Tensor, sA: torch.Tensor | None = None,
+                            sB: torch.Tensor | None = None, scale_mode: int | None = None,
+                            rows: torch.Tensor | None = None, out: torch.Tensor | None = None, config=None,
+                            stream=None) -> torch.Tensor:
+    """The product grouped by expert (dgp_gemm_preshuffle_grouped): rows
+    offsets[e]..offsets[e+1] of C are rows of A times weight e, transposed.  Bs
+    is [E][N][K] preshuffled (quantize_b of a stack, or preshuffle_b of each
+    weight: preshuffle_b(B.view(E * N, K)).view(E, N, K)), offsets int32 [E+1] on the device; rows (int32) names the row of A
+    for each row of C.  Rows of C that no expert owns keep what `out` holds
+    (unspecified without it)."""
+    for t, name in ((A, "A"), (Bs, "Bs"), (offsets, "offsets"), (sA, "sA"), (sB, "sB"), (rows, "rows"), (out, "out")):
+        if t is not None:
+            _dev(t, name)
+    _same_device(A, (Bs, "Bs"), (offsets, "offsets"), (sA, "sA"), (sB, "sB"), (rows, "rows"), (out, "out"))
+    mode = _scale_mode(A, sA, sB, scale_mode)
+    check_grouped_operands(A, Bs, offsets, sA, sB, mode, rows, out)
+    M = A.shape[0] if rows is None else rows.shape[0]
+    E, N = Bs.shape[:2]
+    if out is None:
+        with _alloc_stream(stream):
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+    _enqueue(A, stream, lib().dgp_gemm_preshuffle_grouped, A.data_ptr(), A.shape[0], Bs.data_ptr(), out.data_ptr(), M,
+             N, k_elements(A), E, offsets.data_ptr(), _ptr(rows), dtype_code(A), mode, _ptr(sA), _ptr(sB),
+             _config(config))
     return out
 
 

@@ -52,6 +52,20 @@ struct TileCoordT {
 };
 using TileCoord = TileCoordT<int64_t>;
 
+// Tile t of a tiles_m x tiles_n grid rastered over groups of group_m rows.
+template <typename I>
+__host__ __device__ inline void raster_tile(I t, I tiles_m, I tiles_n, int group_m, I &tm, I &tn)
+{
+    const I in_group = (I)group_m * tiles_n;
+    const I first_m = (t / in_group) * group_m;
+    I rows = tiles_m - first_m;
+    if (rows > group_m)
+        rows = group_m;
+    const I r = t % in_group;
+    tm = first_m + r % rows;
+    tn = r / rows;
+}
+
 // I = int in the kernels (grids are validated to fit), int64_t on the host.
 template <typename I>
 __host__ __device__ inline TileCoordT<I> tile_of_workgroup(I wg, I tiles_m, I tiles_n, I splits, int remap,
@@ -73,14 +87,7 @@ __host__ __device__ inline TileCoordT<I> tile_of_workgroup(I wg, I tiles_m, I ti
         c.tn = t % tiles_n;
         return c;
     }
-    const I in_group = (I)group_m * tiles_n;
-    const I first_m = (t / in_group) * group_m;
-    I rows = tiles_m - first_m;
-    if (rows > group_m)
-        rows = group_m;
-    const I r = t % in_group;
-    c.tm = first_m + r % rows;
-    c.tn = r / rows;
+    raster_tile<I>(t, tiles_m, tiles_n, group_m, c.tm, c.tn);
     return c;
 }
 

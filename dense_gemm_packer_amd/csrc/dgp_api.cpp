@@ -44,6 +44,23 @@ const KernelSpec *kernel_table(int *count)
     return all.data();
 }
 
+const KernelSpec *grouped_table(int *count)
+{
+    static const std::vector<KernelSpec> all = [] {
+        std::vector<KernelSpec> v;
+        int n = 0;
+        const KernelSpec *t = tiled_grouped_kernels(&n);
+        v.insert(v.end(), t, t + n);
+        t = w4_grouped_kernels(&n);
+        v.insert(v.end(), t, t + n);
+        t = stream_grouped_kernels(&n);
+        v.insert(v.end(), t, t + n);
+        return v;
+    }();
+    *count = (int)all.size();
+    return all.data();
+}
+
 }  // namespace dgp
 
 namespace {
@@ -58,6 +75,13 @@ dgp_status fail(dgp_status st, const char *fmt, ...)
     va_end(ap);
     return st;
 }
+
+#define DGP_TRY(expr)                                                                          \
+    do {                                                                                       \
+        const dgp_status st_ = (expr);                                                         \
+        if (st_ != DGP_OK)                                                                     \
+            return st_;                                                                        \
+    } while (0)
 
 dgp_status ok()
 {
@@ -128,10 +152,10 @@ struct Query {
     int kt = -1, wm = -1, depth = -1, pv = -1, pd = -1, sched = -1, lay = -1, copy = -1;
 };
 
-const KernelSpec *find_spec(const Query &q)
+const KernelSpec *find_spec(const Query &q, const KernelSpec *(*table)(int *) = kernel_table)
 {
     int n = 0;
-    const KernelSpec *t = kernel_table(&n);
+    const KernelSpec *t = table(&n);
     for (int i = 0; i < n; ++i) {
         const KernelSpec &k = t[i];
         const int wm = k.family == kTiled ? k.p0 : k.waves;
@@ -334,6 +358,58 @@ struct GemmCall {
     bool lib_scratch = false;   // split-K partials go to the library's fixed array (ws unused)
 };
 
+// The kernel of `table` that the call's configuration names.
+dgp_status configured_spec(const GemmCall &c, int64_t Ks, const KernelSpec *(*table)(int *), const KernelSpec **out_spec)
+{
+    const int fam = c.cfg->tile_m == 16 ? kStream : c.cfg->tile_m == 1 ? kWave : kTiled;
+    if (c.cfg->waves_m < 0 || c.cfg->prefetch < 0)
+        return fail(DGP_ERR_CONFIG, "waves_m and prefetch must be >= 0");
+    if (c.cfg->schedule < 0 || c.cfg->schedule > kSchedW4)
+        return fail(DGP_ERR_CONFIG, "schedule must be 0, 1, 2, 3 or 4 (got %d)", c.cfg->schedule);
+    if (c.cfg->a_layout < 0 || c.cfg->a_layout > 2)
+        return fail(DGP_ERR_CONFIG, "a_layout must be 0, 1 or 2 (got %d)", c.cfg->a_layout);
+    if (c.cfg->a_copy < 0 || c.cfg->a_copy > 2)
+        return fail(DGP_ERR_CONFIG, "a_copy must be 0, 1 or 2 (got %d)", c.cfg->a_copy);
+    Query q{fam, c.dtype, c.scale, c.split_k > 1 ? kOutPartial : kOutBf16, c.cfg->tile_m, c.cfg->tile_n};
+    if (fam == kTiled) {
+        q.kt = c.cfg->tile_k;
+        q.wm = c.cfg->waves_m > 0 ? c.cfg->waves_m : -1;
+        q.depth = c.cfg->prefetch > 0 ? c.cfg->prefetch : -1;
+        // (0, 0) = this tile's tuned default hints; any other pair must
+        // name a compiled kernel exactly.
+        if (c.cfg->preload_vmem != 0 || c.cfg->preload_dsrd != 0) {
+            q.pv = c.cfg->preload_vmem;
+            q.pd = c.cfg->preload_dsrd;
+        }
+        if (c.cfg->schedule > 0)
+            q.sched = c.cfg->schedule;
+        if (c.cfg->a_layout > 0)
+            q.lay = c.cfg->a_layout - 1;
+        q.copy = c.cfg->a_copy > 0 ? c.cfg->a_copy - 1 : kCopyAsync;
+    } else {
+        if (c.cfg->preload_vmem != 0 || c.cfg->preload_dsrd != 0)
+            return fail(DGP_ERR_CONFIG, "the 16-row and one-row kernels take no preload hints");
+        if (c.cfg->schedule != 0)
+            return fail(DGP_ERR_CONFIG, "the 16-row and one-row kernels have no schedule choice");
+        if (c.cfg->a_layout != 0 || c.cfg->a_copy != 0)
+            return fail(DGP_ERR_CONFIG, "the 16-row and one-row kernels have no A layout or copy choice");
+        q.wm = c.cfg->waves_m > 0 ? c.cfg->waves_m : -1;   // matched against waves per workgroup
+        q.depth = c.cfg->prefetch > 0 ? c.cfg->prefetch : -1;
+    }
+    const KernelSpec *spec = find_spec(q, table);
+    if (!spec)
+        return fail(DGP_ERR_CONFIG,
+                    "no compiled kernel for tile %dx%dx%d (waves_m %d, prefetch %d, preload %d,%d, schedule %d, "
+                    "a_layout %d, a_copy %d) with this dtype/scale", c.cfg->tile_m, c.cfg->tile_n, c.cfg->tile_k,
+                    c.cfg->waves_m, c.cfg->prefetch, c.cfg->preload_vmem, c.cfg->preload_dsrd, c.cfg->schedule,
+                    c.cfg->a_layout, c.cfg->a_copy);
+    if (!spec_fits(*spec, Ks))
+        return fail(DGP_ERR_CONFIG, "tile_k=%d does not divide the K range of a split (%lld bytes)",
+                    spec->kt, (long long)Ks);
+    *out_spec = spec;
+    return DGP_OK;
+}
+
 // Kernel choice for a validated call: the configured tile, or the built-in
 // per-shape table.
 dgp_status select_kernel(const GemmCall &c, int64_t Ks, Plan *plan)
@@ -341,51 +417,9 @@ dgp_status select_kernel(const GemmCall &c, int64_t Ks, Plan *plan)
     const int out = c.split_k > 1 ? kOutPartial : kOutBf16;
     const KernelSpec *spec = nullptr;
     if (c.cfg && c.cfg->tile_m > 0) {
-        const int fam = c.cfg->tile_m == 16 ? kStream : c.cfg->tile_m == 1 ? kWave : kTiled;
-        if (c.cfg->waves_m < 0 || c.cfg->prefetch < 0)
-            return fail(DGP_ERR_CONFIG, "waves_m and prefetch must be >= 0");
-        if (c.cfg->schedule < 0 || c.cfg->schedule > kSchedW4)
-            return fail(DGP_ERR_CONFIG, "schedule must be 0, 1, 2, 3 or 4 (got %d)", c.cfg->schedule);
-        if (c.cfg->a_layout < 0 || c.cfg->a_layout > 2)
-            return fail(DGP_ERR_CONFIG, "a_layout must be 0, 1 or 2 (got %d)", c.cfg->a_layout);
-        if (c.cfg->a_copy < 0 || c.cfg->a_copy > 2)
-            return fail(DGP_ERR_CONFIG, "a_copy must be 0, 1 or 2 (got %d)", c.cfg->a_copy);
-        Query q{fam, c.dtype, c.scale, out, c.cfg->tile_m, c.cfg->tile_n};
-        if (fam == kTiled) {
-            q.kt = c.cfg->tile_k;
-            q.wm = c.cfg->waves_m > 0 ? c.cfg->waves_m : -1;
-            q.depth = c.cfg->prefetch > 0 ? c.cfg->prefetch : -1;
-            // (0, 0) = this tile's tuned default hints; any other pair must
-            // name a compiled kernel exactly.
-            if (c.cfg->preload_vmem != 0 || c.cfg->preload_dsrd != 0) {
-                q.pv = c.cfg->preload_vmem;
-                q.pd = c.cfg->preload_dsrd;
-            }
-            if (c.cfg->schedule > 0)
-                q.sched = c.cfg->schedule;
-            if (c.cfg->a_layout > 0)
-                q.lay = c.cfg->a_layout - 1;
-            q.copy = c.cfg->a_copy > 0 ? c.cfg->a_copy - 1 : kCopyAsync;
-        } else {
-            if (c.cfg->preload_vmem != 0 || c.cfg->preload_dsrd != 0)
-                return fail(DGP_ERR_CONFIG, "the 16-row and one-row kernels take no preload hints");
-            if (c.cfg->schedule != 0)
-                return fail(DGP_ERR_CONFIG, "the 16-row and one-row kernels have no schedule choice");
-            if (c.cfg->a_layout != 0 || c.cfg->a_copy != 0)
-                return fail(DGP_ERR_CONFIG, "the 16-row and one-row kernels have no A layout or copy choice");
-            q.wm = c.cfg->waves_m > 0 ? c.cfg->waves_m : -1;   // matched against waves per workgroup
-            q.depth = c.cfg->prefetch > 0 ? c.cfg->prefetch : -1;
-        }
-        spec = find_spec(q);
-        if (!spec)
-            return fail(DGP_ERR_CONFIG,
-                        "no compiled kernel for tile %dx%dx%d (waves_m %d, prefetch %d, preload %d,%d, schedule %d, "
-                        "a_layout %d, a_copy %d) with this dtype/scale", c.cfg->tile_m, c.cfg->tile_n, c.cfg->tile_k,
-                        c.cfg->waves_m, c.cfg->prefetch, c.cfg->preload_vmem, c.cfg->preload_dsrd, c.cfg->schedule,
-                        c.cfg->a_layout, c.cfg->a_copy);
-        if (!spec_fits(*spec, Ks))
-            return fail(DGP_ERR_CONFIG, "tile_k=%d does not divide the K range of a split (%lld bytes)",
-                        spec->kt, (long long)Ks);
+        const dgp_status st = configured_spec(c, Ks, kernel_table, &spec);
+        if (st != DGP_OK)
+            return st;
     } else {
         spec = default_spec(c.dtype, c.scale, out, c.M, c.N, Ks, c.split_k);
         if (!spec)
@@ -407,7 +441,8 @@ dgp_status select_kernel(const GemmCall &c, int64_t Ks, Plan *plan)
     return ok();
 }
 
-dgp_status validate(const GemmCall &c, Plan *plan)
+// Types, sizes, scale mode and configuration of a call.
+dgp_status validate_shape(const GemmCall &c)
 {
     if (!known_dtype(c.dtype))
         return fail(DGP_ERR_DTYPE, "dtype %d is not DGP_BF16, DGP_FP8_E4M3 or DGP_FP4_E2M1", c.dtype);
@@ -456,7 +491,31 @@ dgp_status validate(const GemmCall &c, Plan *plan)
         return fail(DGP_ERR_SPLITK, "K range per split (%lld bytes) is not a multiple of 128", (long long)Ks);
     if ((c.scale == DGP_SCALE_BLOCK128 || c.scale == DGP_SCALE_MX128) && (c.K / c.split_k) % 128 != 0)
         return fail(DGP_ERR_SPLITK, "block scales need (K/split_k) %% 128 == 0");
+    return DGP_OK;
+}
 
+// Operands and scales of a call with K > 0.
+dgp_status validate_operands(const GemmCall &c)
+{
+    if (!c.A || !c.Bs)
+        return fail(DGP_ERR_NULL, "A or Bs is NULL");
+    if (!aligned16(c.A) || !aligned16(c.Bs))
+        return fail(DGP_ERR_ALIGN, "A and Bs must be 16-byte aligned");
+    if (c.scale != DGP_SCALE_NONE) {
+        if (!c.sA || !c.sB)
+            return fail(DGP_ERR_NULL, "scale mode needs sA and sB");
+        if (c.scale != DGP_SCALE_MX128 && (((uintptr_t)c.sA & 3u) || ((uintptr_t)c.sB & 3u)))
+            return fail(DGP_ERR_ALIGN, "fp32 scales sA and sB must be 4-byte aligned");
+    }
+    return DGP_OK;
+}
+
+dgp_status validate(const GemmCall &c, Plan *plan)
+{
+    dgp_status st = validate_shape(c);
+    if (st != DGP_OK)
+        return st;
+    const int64_t Ks = row_bytes(c.dtype, c.K) / c.split_k;
     if (c.M == 0 || c.N == 0 || (c.select_only && c.K == 0)) {
         plan->spec = nullptr;
         return ok();
@@ -471,16 +530,9 @@ dgp_status validate(const GemmCall &c, Plan *plan)
         plan->spec = nullptr;
         return ok();
     }
-    if (!c.A || !c.Bs)
-        return fail(DGP_ERR_NULL, "A or Bs is NULL");
-    if (!aligned16(c.A) || !aligned16(c.Bs))
-        return fail(DGP_ERR_ALIGN, "A and Bs must be 16-byte aligned");
-    if (c.scale != DGP_SCALE_NONE) {
-        if (!c.sA || !c.sB)
-            return fail(DGP_ERR_NULL, "scale mode needs sA and sB");
-        if (c.scale != DGP_SCALE_MX128 && (((uintptr_t)c.sA & 3u) || ((uintptr_t)c.sB & 3u)))
-            return fail(DGP_ERR_ALIGN, "fp32 scales sA and sB must be 4-byte aligned");
-    }
+    st = validate_operands(c);
+    if (st != DGP_OK)
+        return st;
     if (c.split_k > 1) {
         const size_t need = dgp_splitk_workspace_bytes(c.M, c.N, c.split_k);
         if (c.lib_scratch) {
@@ -545,6 +597,82 @@ dgp_status run_gemm(const GemmCall &c, hipStream_t stream)
     if (st != DGP_OK || c.split_k == 1)
         return st;
     return hip_status(launch_splitk_reduce(ws, c.C, c.M, c.N, c.split_k, stream), "split-K reduce launch");
+}
+
+// ------------------------------------------------- product by expert
+
+// Most row tiles of tm rows that M rows split over E experts can make.
+int64_t most_row_tiles(int64_t M, int64_t E, int64_t tm)
+{
+    const int64_t live = E < M ? E : M;   // experts that can have a row
+    return (M + live * (tm - 1)) / tm;
+}
+
+// Built-in choice for M rows over E experts.  Only the average row count is
+// known on the host.
+const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t N, int64_t E)
+{
+    const int64_t live = E < M ? E : M;
+    const int64_t per = (M + live - 1) / live;
+    Query q{kStream, dtype, scale, kOutBf16, 16, N >= 64 ? 64 : 16};
+    if (per > 48) {
+        q = Query{kTiled, dtype, scale, kOutBf16, per > 160 ? 256 : 128, per > 160 ? 256 : 128};
+    }
+    return find_spec(q, grouped_table);
+}
+
+struct Experts {
+    int64_t E, a_rows;
+    const int32_t *offsets, *rows;
+};
+
+dgp_status run_grouped(const GemmCall &c, const Experts &x, hipStream_t stream)
+{
+    DGP_TRY(validate_shape(c));
+    if (x.E < 0 || x.E > 65535 || x.a_rows < 0)
+        return fail(DGP_ERR_SHAPE, "E=%lld experts, %lld rows of A", (long long)x.E, (long long)x.a_rows);
+    if (c.K == 0)
+        return fail(DGP_ERR_SHAPE, "the grouped product needs K > 0");
+    if (c.M == 0 || c.N == 0 || x.E == 0)
+        return ok();
+    const int64_t Kb = row_bytes(c.dtype, c.K);
+    if (!x.offsets)
+        return fail(DGP_ERR_NULL, "offsets is NULL");
+    if (((uintptr_t)x.offsets | (uintptr_t)x.rows) & 3u)
+        return fail(DGP_ERR_ALIGN, "offsets and rows must be 4-byte aligned");
+    if (x.rows ? x.a_rows < 1 : x.a_rows < c.M)
+        return fail(DGP_ERR_SHAPE, "A has %lld rows, the product %lld", (long long)x.a_rows, (long long)c.M);
+    if (x.rows && (x.a_rows > INT32_MAX / 2 || x.a_rows * Kb > (int64_t)0xFF000000))
+        return fail(DGP_ERR_SHAPE, "with a row list A must be at most %lld bytes", (long long)0xFF000000);
+    if (!c.C)
+        return fail(DGP_ERR_NULL, "C is NULL");
+    if (!aligned16(c.C))
+        return fail(DGP_ERR_ALIGN, "C is not 16-byte aligned");
+    DGP_TRY(validate_operands(c));
+    const KernelSpec *spec = nullptr;
+    if (c.cfg && c.cfg->tile_m > 0)
+        DGP_TRY(configured_spec(c, Kb, grouped_table, &spec));
+    else
+        spec = default_grouped_spec(c.dtype, c.scale, c.M, c.N, x.E);
+    if (!spec)
+        return fail(DGP_ERR_CONFIG, "no compiled grouped kernel fits this shape");
+    const int64_t tiles_m = most_row_tiles(c.M, x.E, spec->tm), tiles_n = (c.N + spec->tn - 1) / spec->tn;
+    if (tiles_m * tiles_n > INT32_MAX)
+        return fail(DGP_ERR_SHAPE, "grid of %lld workgroups too large", (long long)(tiles_m * tiles_n));
+    DGP_TRY(check_device_arch());
+    GemmArgs a{};
+    a.A = (const uint8_t *)c.A, a.Bs = (const uint8_t *)c.Bs, a.C = c.C;
+    a.sA = c.sA, a.sB = c.sB;
+    a.M = (int)c.M, a.N = (int)c.N, a.K = (int)c.K;
+    a.Kb = a.Ks = (int)Kb;
+    a.tiles_m = (int)tiles_m, a.tiles_n = (int)tiles_n, a.splits = 1;
+    const bool configured = c.cfg && c.cfg->tile_m > 0;
+    a.remap = configured ? c.cfg->xcd_remap : 1;
+    a.group_m = configured && c.cfg->group_m > 0 ? c.cfg->group_m : 8;
+    a.offsets = x.offsets, a.rows = x.rows;
+    a.groups = (int)x.E, a.a_rows = (int)(x.rows ? x.a_rows : 0);
+    spec->launch(a, dim3((unsigned)(tiles_m * tiles_n)), stream);
+    return hip_status(hipGetLastError(), "grouped GEMM launch");
 }
 
 dgp_status shuffle(const void *src, void *dst, int64_t N, int64_t K, int dtype, void *stream, bool inverse)
@@ -653,13 +781,6 @@ int amax_parts(int64_t M, int64_t K)
     const int64_t n = (M * K / 8 + 1023) / 1024;
     return (int)(n < 1 ? 1 : n > kAmaxParts ? kAmaxParts : n);
 }
-
-#define DGP_TRY(expr)                                                                          \
-    do {                                                                                       \
-        const dgp_status st_ = (expr);                                                         \
-        if (st_ != DGP_OK)                                                                     \
-            return st_;                                                                        \
-    } while (0)
 
 }  // namespace
 
@@ -816,6 +937,15 @@ dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_
     a.X = G, a.U = U, a.Q = Q, a.S = S, a.scale = scale;
     a.ldx = ldg, a.ldu = ldu, a.M = M, a.K = K;
     return hip_status(launch_row_quant(a, x_type, scale_mode, true, (hipStream_t)stream), "gated activation launch");
+}
+
+dgp_status dgp_gemm_preshuffle_grouped(const void *A, int64_t a_rows, const void *Bs, void *C, int64_t M, int64_t N,
+                                       int64_t K, int64_t E, const int32_t *offsets, const int32_t *rows, int dtype,
+                                       int scale_mode, const void *sA, const void *sB, const dgp_config *cfg,
+                                       void *stream)
+{
+    GemmCall c{A, Bs, C, M, N, K, dtype, scale_mode, sA, sB, 1, nullptr, 0, cfg};
+    return run_grouped(c, Experts{E, a_rows, offsets, rows}, (hipStream_t)stream);
 }
 
 dgp_status dgp_check_arch(const char *name)

@@ -161,6 +161,148 @@ __device__ inline void lds_dma16(__amdgpu_buffer_rsrc_t r, uint8_t *lds_dst, uin
     lds_dma<16>(r, lds_dst, voff, soff);
 }
 
+// ------------------------------------------------- product by expert
+//
+// GR = 1 forms of the kernels multiply the rows [offsets[e], offsets[e+1]) of
+// the product with weight e.  The row counts are known on the device only, so
+// the grid is the most tiles any counts give, and every wave finds its tile
+// itself: a lane per expert takes its two offsets and its tile count, a DPP
+// scan adds them up, and the tile's expert is the first whose running count
+// passes it.  Tiles run expert by expert (an expert's weight is read by
+// neighbouring workgroups), regrouped over the XCDs by the number of tiles
+// there are, not by the grid; workgroups past it end at once.  The arguments
+// are then narrowed to the expert's rows and weight, and the kernel runs as
+// on one product.
+// Offsets are clamped to [0, M] and to their predecessor, so whatever they
+// hold no row outside the product is touched.
+
+// Inclusive sum over the wave's lanes.
+__device__ inline int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast 15 into rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast 31 into rows 2, 3
+    return v;
+}
+
+// Rows [lo, hi) of this lane's expert e (none past the last one).
+__device__ inline void expert_rows(const GemmArgs &p, int e, int &lo, int &hi)
+{
+    lo = hi = 0;
+    if (e < p.groups) {
+        lo = p.offsets[e];
+        hi = p.offsets[e + 1];
+        lo = lo < 0 ? 0 : lo > p.M ? p.M : lo;
+        hi = hi < lo ? lo : hi > p.M ? p.M : hi;
+    }
+}
+
+// This workgroup's tile; GR = 1: also narrows p to its expert.  False: none.
+template <int GR, int TM, int SCALE>
+__device__ inline bool locate_tile(GemmArgs &p, TileCoordT<int> &tc)
+{
+    if constexpr (GR == 0) {
+        tc = tile_of_workgroup<int>((int)blockIdx.x, p.tiles_m, p.tiles_n, p.splits, p.remap, p.group_m);
+        return true;
+    } else {
+        const int lane = threadIdx.x & 63;
+        int lo, hi;
+        expert_rows(p, lane, lo, hi);
+        int n = (hi - lo + TM - 1) / TM;
+        int incl = wave_scan(n);
+        int total = __builtin_amdgcn_readlane(incl, 63);
+        for (int e0 = 64; e0 < p.groups; e0 += 64) {
+            int l2, h2;
+            expert_rows(p, e0 + lane, l2, h2);
+            total += __builtin_amdgcn_readlane(wave_scan((h2 - l2 + TM - 1) / TM), 63);
+            total = total < p.tiles_m ? total : p.tiles_m;
+        }
+        total = total < p.tiles_m ? total : p.tiles_m;
+        const int wg = (int)blockIdx.x;
+        if (wg >= total * p.tiles_n)
+            return false;
+        int logical = wg;
+        if (p.remap) {
+            const int per = total * p.tiles_n / kNumXcd;
+            if (wg < per * kNumXcd)
+                logical = (wg % kNumXcd) * per + wg / kNumXcd;
+        }
+        const int rt = logical / p.tiles_n;          // row tile, counted over all experts
+        int before = 0, e0 = 0;                      // row tiles before expert e0
+        uint64_t past = __ballot(incl > rt);
+        while (past == 0) {                          // (rt < total: an expert is found)
+            before += __builtin_amdgcn_readlane(incl, 63);
+            e0 += 64;
+            expert_rows(p, e0 + lane, lo, hi);
+            n = (hi - lo + TM - 1) / TM;
+            incl = wave_scan(n);
+            past = __ballot(before + incl > rt);
+            if (e0 >= p.groups)
+                return false;
+        }
+        const int at = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
+        const int first = __builtin_amdgcn_readlane(lo, at), last = __builtin_amdgcn_readlane(hi, at);
+        const int tiles = __builtin_amdgcn_readlane(n, at);
+        before += __builtin_amdgcn_readlane(incl, at) - tiles;
+        raster_tile<int>(logical - before * p.tiles_n, tiles, p.tiles_n, p.group_m < 1 ? 1 : p.group_m, tc.tm, tc.tn);
+        tc.s = 0;
+        const int64_t e = e0 + at;
+        const int64_t kblk = SCALE == kScaleMx32 ? p.K / 32 : p.K / 128;
+        p.M = last - first;
+        p.Bs += e * p.N * (int64_t)p.Kb;
+        p.C = static_cast<uint8_t *>(p.C) + (int64_t)first * p.N * 2;
+        if constexpr (SCALE == kScaleTensor)
+            p.sB = static_cast<const float *>(p.sB) + e;
+        if constexpr (SCALE == kScaleBlock)
+            p.sB = static_cast<const float *>(p.sB) + e * (p.N / 128) * kblk;
+        if constexpr (SCALE == kScaleMx || SCALE == kScaleMx32)
+            p.sB = static_cast<const uint8_t *>(p.sB) + e * p.N * kblk;
+        if (p.rows) {
+            p.rows += first;
+        } else {
+            p.A += (int64_t)first * p.Kb;
+            if constexpr (SCALE == kScaleBlock)
+                p.sA = static_cast<const float *>(p.sA) + (int64_t)first * kblk;
+            if constexpr (SCALE == kScaleMx || SCALE == kScaleMx32)
+                p.sA = static_cast<const uint8_t *>(p.sA) + (int64_t)first * kblk;
+        }
+        return true;
+    }
+}
+
+// The buffer range of a tile's rows of A (or of A's scales), rows row_bytes
+// long, and the byte offset of the tile's row r in it.  Rows past M lie past
+// the range.  With a row list the range is all of A, and a row past M, or one
+// that A does not have, goes to an offset past every range (the host keeps A
+// below it, with room for the K offsets that are added).
+constexpr uint32_t kNoRow = 0xFF000000u;
+
+template <int GR>
+__device__ inline __amdgpu_buffer_rsrc_t row_rsrc(const GemmArgs &p, const void *base, int m0, int64_t row_bytes)
+{
+    if constexpr (GR != 0) {
+        if (p.rows)
+            return make_rsrc(base, clamp_bytes((int64_t)p.a_rows * row_bytes));
+    }
+    return make_rsrc(static_cast<const uint8_t *>(base) + (int64_t)m0 * row_bytes,
+                     clamp_bytes((int64_t)(p.M - m0) * row_bytes));
+}
+
+template <int GR>
+__device__ inline uint32_t row_offset(const GemmArgs &p, int m0, int r, uint32_t row_bytes)
+{
+    if constexpr (GR != 0) {
+        if (p.rows) {
+            const uint32_t i = m0 + r < p.M ? (uint32_t)p.rows[m0 + r] : 0xFFFFFFFFu;
+            return i < (uint32_t)p.a_rows ? i * row_bytes : kNoRow;
+        }
+    }
+    return (uint32_t)r * row_bytes;
+}
+
 // ------------------------------------------------------------ load ring
 //
 // ring_run<DEPTH>(n, load, consume) -- one wave's slice of n steps through a

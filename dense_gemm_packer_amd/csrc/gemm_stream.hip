@@ -319,9 +319,10 @@ gemm_stream_kernel(const GemmArgs p, int panel)
 // memory access: each workgroup reads only its half of every 1 KiB block
 // (8 rows x 4 contiguous 128-byte pieces), and its MFMAs compute zeros for
 // the other half's columns, which it does not store.
-template <int DT, int NW, int DEPTH, int SCALE, int OUT, int TN>
+// GR: 1 = the product grouped by expert (gemm_common.h).
+template <int DT, int NW, int DEPTH, int SCALE, int OUT, int TN, int GR>
 __global__ void __attribute__((amdgpu_flat_work_group_size(NW * 64, NW * 64)))
-gemm_ksplit_kernel(const GemmArgs p)
+gemm_ksplit_kernel(const GemmArgs args)
 {
     static_assert(TN == 8 || TN == 16 || TN == 32 || TN == 64, "half a strip, or 1, 2 or 4 strips");
     constexpr bool kHalf = TN == 8;
@@ -339,7 +340,10 @@ gemm_ksplit_kernel(const GemmArgs p)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    const auto tc = tile_of_workgroup<int>((int)blockIdx.x, p.tiles_m, p.tiles_n, p.splits, p.remap, p.group_m);
+    GemmArgs p = args;
+    TileCoordT<int> tc;
+    if (!locate_tile<GR, 16, SCALE>(p, tc))
+        return;
     const int m0 = (int)tc.tm * 16;
     const int strip0 = kHalf ? (int)tc.tn >> 1 : (int)tc.tn * SPW;
     const int half = kHalf ? (int)tc.tn & 1 : 0;
@@ -355,8 +359,8 @@ gemm_ksplit_kernel(const GemmArgs p)
     // 32-K block (mxfp4).
     const int kblocks_row = SCALE == kScaleMx32 ? p.K / 32 : p.K / 128;
 
-    const auto rA = make_rsrc(p.A + (int64_t)m0 * Kb, clamp_bytes((int64_t)(p.M - m0) * Kb));
-    const uint32_t a_voff = (uint32_t)(lane & 15) * Kb + (uint32_t)(lane >> 4) * 16u;
+    const auto rA = row_rsrc<GR>(p, p.A, m0, Kb);
+    const uint32_t a_voff = row_offset<GR>(p, m0, lane & 15, Kb) + (uint32_t)(lane >> 4) * 16u;
     // Half strips: the resource covers exactly the strip (16 rows, at most
     // 128 MiB), and the other half's lanes start at 2^31, so every offset
     // they form stays past the range and below 2^32.
@@ -375,12 +379,11 @@ gemm_ksplit_kernel(const GemmArgs p)
     // ring) or read where the step is multiplied (guarded loop).
     static_assert(SCALE != kScaleBlock || 128 % (16 * SPW) == 0, "a tile's strips in one 128-column block");
     constexpr bool kBs = SCALE == kScaleBlock;
-    [[maybe_unused]] const auto rSa = make_rsrc(kBs ? static_cast<const float *>(p.sA) + (int64_t)m0 * kblocks_row : nullptr,
-                                                kBs ? clamp_bytes((int64_t)(p.M - m0) * kblocks_row * 4) : 0);
+    [[maybe_unused]] const auto rSa = kBs ? row_rsrc<GR>(p, p.sA, m0, (int64_t)kblocks_row * 4) : make_rsrc(nullptr, 0);
     [[maybe_unused]] const auto rSb = make_rsrc(kBs ? static_cast<const float *>(p.sB) + (int64_t)(strip0 * 16 / 128) * kblocks_row
                                                     : nullptr,
                                                 kBs ? (uint32_t)kblocks_row * 4u : 0u);
-    [[maybe_unused]] const uint32_t sa_off = (uint32_t)(lane & 15) * (uint32_t)kblocks_row * 4u;
+    [[maybe_unused]] const uint32_t sa_off = row_offset<GR>(p, m0, lane & 15, (uint32_t)kblocks_row * 4u);
     // mxfp8: a step's E8M0 bytes (this lane's A row, its B column in each
     // strip) are loaded with the step's operands into the same ring slot, so
     // they arrive with them and waiting for them never drains the ring.  With
@@ -391,13 +394,12 @@ gemm_ksplit_kernel(const GemmArgs p)
     // resources cover rows m0.. < M and columns strip0*16.. < N: rows and
     // strips past the edge read zero (2^-127), which only scales zero data.
     constexpr bool kMx = SCALE == kScaleMx;
-    [[maybe_unused]] const auto rXa8 = make_rsrc(kMx ? static_cast<const uint8_t *>(p.sA) + (int64_t)m0 * kblocks_row
-                                                     : nullptr,
-                                                 kMx ? clamp_bytes((int64_t)(p.M - m0) * kblocks_row) : 0);
+    [[maybe_unused]] const auto rXa8 = kMx ? row_rsrc<GR>(p, p.sA, m0, kblocks_row) : make_rsrc(nullptr, 0);
     [[maybe_unused]] const auto rXb8 = make_rsrc(kMx ? static_cast<const uint8_t *>(p.sB) + (int64_t)strip0 * 16 * kblocks_row
                                                      : nullptr,
                                                  kMx ? clamp_bytes((int64_t)(p.N - strip0 * 16) * kblocks_row) : 0);
-    [[maybe_unused]] const uint32_t x8_off = (uint32_t)(lane & 15) * (uint32_t)kblocks_row;
+    [[maybe_unused]] const uint32_t x8_off = (uint32_t)(lane & 15) * (uint32_t)kblocks_row;   // a strip's column
+    [[maybe_unused]] const uint32_t xa_off = row_offset<GR>(p, m0, lane & 15, (uint32_t)kblocks_row);
     [[maybe_unused]] int xs[DEPTH][1 + SPW];   // [ring slot][A row, then each strip's column]
     static_assert(!kMx || kStepBytes == 128, "mxfp8: one 128-K scale block per MFMA step");
 
@@ -413,9 +415,7 @@ gemm_ksplit_kernel(const GemmArgs p)
     // only ever scales zero data.
     constexpr bool kXw = SCALE == kScaleMx32;
     static_assert(!kXw || (DEPTH == 4 && kStepBytes == 64), "mxfp4 scale words: 4 bytes per step, one 16-byte load per 4 steps");
-    [[maybe_unused]] const auto rXa = make_rsrc(kXw ? static_cast<const uint8_t *>(p.sA) + (int64_t)m0 * kblocks_row
-                                                    : nullptr,
-                                                kXw ? clamp_bytes((int64_t)(p.M - m0) * kblocks_row) : 0);
+    [[maybe_unused]] const auto rXa = kXw ? row_rsrc<GR>(p, p.sA, m0, kblocks_row) : make_rsrc(nullptr, 0);
     [[maybe_unused]] const auto rXb = make_rsrc(kXw ? static_cast<const uint8_t *>(p.sB) + (int64_t)strip0 * 16 * kblocks_row
                                                     : nullptr,
                                                 kXw ? clamp_bytes((int64_t)(p.N - strip0 * 16) * kblocks_row) : 0);
@@ -424,11 +424,11 @@ gemm_ksplit_kernel(const GemmArgs p)
         if constexpr (kXw) {
             constexpr int X = decltype(setc)::value;
             const uint32_t gb = kbase / 16u + 4u * (uint32_t)st;
-            const uint32_t oa = (uint32_t)(lane & 15) * (uint32_t)kblocks_row + gb;
-            xw[X][0] = load16<kAuxNone>(rXa, oa);
+            const uint32_t ob = x8_off + gb;
+            xw[X][0] = load16<kAuxNone>(rXa, xa_off + gb);
 #pragma unroll
             for (int sp = 0; sp < SPW; ++sp)
-                xw[X][1 + sp] = load16<kAuxNone>(rXb, oa + (uint32_t)(sp * 16) * (uint32_t)kblocks_row);
+                xw[X][1 + sp] = load16<kAuxNone>(rXb, ob + (uint32_t)(sp * 16) * (uint32_t)kblocks_row);
         }
     };
 
@@ -451,7 +451,7 @@ gemm_ksplit_kernel(const GemmArgs p)
         const uint32_t k = kbase + (uint32_t)st * kStepBytes;
         if constexpr (kMx) {
             const uint32_t kb = k / 128u;   // one E8M0 byte per 128-K step
-            xs[d][0] = __builtin_amdgcn_raw_buffer_load_b8(rXa8, x8_off + kb, 0, kAuxNone);
+            xs[d][0] = __builtin_amdgcn_raw_buffer_load_b8(rXa8, xa_off + kb, 0, kAuxNone);
             if constexpr (SPW >= 2) {   // one load for all strips: lane l takes column l % 16 of strip (l / 16) % SPW
                 xs[d][1] = __builtin_amdgcn_raw_buffer_load_b8(
                     rXb8, (uint32_t)(16 * ((lane >> 4) % SPW) + (lane & 15)) * (uint32_t)kblocks_row + kb, 0, kAuxNone);
@@ -616,10 +616,10 @@ void launch_stream(const GemmArgs &a, dim3 grid, hipStream_t s)
     gemm_stream_kernel<DT, NW, SPW, DEPTH, SCALE, OUT><<<grid, NW * 64, lds, s>>>(a, panel);
 }
 
-template <int DT, int NW, int DEPTH, int SCALE, int OUT, int TN>
+template <int DT, int NW, int DEPTH, int SCALE, int OUT, int TN, int GR = 0>
 void launch_ksplit(const GemmArgs &a, dim3 grid, hipStream_t s)
 {
-    gemm_ksplit_kernel<DT, NW, DEPTH, SCALE, OUT, TN><<<grid, NW * 64, 0, s>>>(a);
+    gemm_ksplit_kernel<DT, NW, DEPTH, SCALE, OUT, TN, GR><<<grid, NW * 64, 0, s>>>(a);
 }
 
 #define DGP_KSPLIT(DT, NW, DEPTH, SC, OUT, TN)                                                \
@@ -683,6 +683,25 @@ static const KernelSpec kStreamKernels[] = {
     DGP_KSPLIT_BOTH_OUT(kDtypeFp4, 16, 4, kScaleMx32, 16),
     DGP_KSPLIT_BOTH_OUT(kDtypeFp4, 16, 4, kScaleMx32, 32),
 };
+
+// Product grouped by expert: the 8-wave K-split tiles.
+#define DGP_KSPLITG(DT, DEPTH, SC, TN)                                                         \
+    {kStream, DT, SC, kOutBf16, 16, TN, 0, 8, (TN >= 16 ? TN / 16 : 1), DEPTH, 0, 0, DEPTH, 0,      \
+     &launch_ksplit<DT, 8, DEPTH, SC, kOutBf16, TN, 1>}
+#define DGP_KSPLITG_ALL(DT, DEPTH, DEPTH32, SC)                                                \
+    DGP_KSPLITG(DT, DEPTH, SC, 8), DGP_KSPLITG(DT, DEPTH, SC, 16), DGP_KSPLITG(DT, DEPTH32, SC, 32),  \
+        DGP_KSPLITG(DT, DEPTH, SC, 64)
+static const KernelSpec kStreamGrouped[] = {
+    DGP_KSPLITG_ALL(kDtypeBf16, 4, 4, kScaleNone), DGP_KSPLITG_ALL(kDtypeFp8, 4, 4, kScaleTensor),
+    DGP_KSPLITG_ALL(kDtypeFp8, 4, 4, kScaleBlock), DGP_KSPLITG_ALL(kDtypeFp8, 4, 3, kScaleMx),
+    DGP_KSPLITG_ALL(kDtypeFp4, 4, 4, kScaleMx32),
+};
+
+const KernelSpec *stream_grouped_kernels(int *count)
+{
+    *count = (int)(sizeof(kStreamGrouped) / sizeof(kStreamGrouped[0]));
+    return kStreamGrouped;
+}
 
 const KernelSpec *stream_kernels(int *count)
 {

@@ -26,10 +26,11 @@ namespace dgp {
 // ================================================================ tiled
 
 
-template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD>
+// GR: 1 = the product grouped by expert (gemm_common.h).
+template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD, int GR>
 __global__ void __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
                                amdgpu_waves_per_eu((WM * WN + 3) / 4, (WM * WN + 3) / 4)))
-gemm_tiled_kernel(const GemmArgs p)
+gemm_tiled_kernel(const GemmArgs args)
 {
     using S = TiledShape<DT, TM, TN, WM, WN, KT>;
     using Frag = typename Op<DT>::Frag;
@@ -68,7 +69,10 @@ gemm_tiled_kernel(const GemmArgs p)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
 
-    const auto tc = tile_of_workgroup<int>((int)blockIdx.x, p.tiles_m, p.tiles_n, p.splits, p.remap, p.group_m);
+    GemmArgs p = args;
+    TileCoordT<int> tc;
+    if (!locate_tile<GR, TM, SCALE>(p, tc))
+        return;
     const int m0 = (int)tc.tm * TM;
     const int n0 = (int)tc.tn * TN;
     const int split = (int)tc.s;
@@ -77,7 +81,7 @@ gemm_tiled_kernel(const GemmArgs p)
     const int ntiles = p.Ks / KT;
 
     // A: rows m0.. of A; rows >= M are past num_records and load as zero.
-    const auto rA = make_rsrc(p.A + (int64_t)m0 * Kb, clamp_bytes((int64_t)(p.M - m0) * Kb));
+    const auto rA = row_rsrc<GR>(p, p.A, m0, Kb);
     // Where the copy puts each lane's 16 bytes: instruction j of this wave
     // fills LDS block blk = j*waves + wave = (row group rg, 64-byte chunk ch),
     // lane l landing at byte 16*l with row 16*rg + l%16, K-bytes
@@ -87,7 +91,7 @@ gemm_tiled_kernel(const GemmArgs p)
     for (int j = 0; j < S::kDmaPerWave; ++j) {
         const int blk = j * S::kWaves + wave;
         const int rg = blk / S::kCH, ch = blk % S::kCH;
-        dma_voff[j] = (uint32_t)(rg * 16 + (lane & 15)) * Kb + (uint32_t)(ch * 64 + (lane >> 4) * 16);
+        dma_voff[j] = row_offset<GR>(p, m0, rg * 16 + (lane & 15), Kb) + (uint32_t)(ch * 64 + (lane >> 4) * 16);
     }
     // B: this wave's strips; strips >= N/16 are past num_records and load as zero.
     const int strip0 = (n0 + wn * (TN / WN)) / 16;
@@ -105,8 +109,7 @@ gemm_tiled_kernel(const GemmArgs p)
     [[maybe_unused]] uint32_t x_voff[kXDma > 0 ? kXDma : 1];
     if constexpr (kX4) {
         const uint32_t rowb = Kb / 16u;    // E8M0 bytes per row: one per 32 elements = 16 bytes
-        const auto rXA = make_rsrc((const uint8_t *)p.sA + (int64_t)m0 * rowb,
-                                   clamp_bytes((int64_t)(p.M - m0) * rowb));
+        const auto rXA = row_rsrc<GR>(p, p.sA, m0, rowb);
         const auto rXB = make_rsrc((const uint8_t *)p.sB + (int64_t)n0 * rowb,
                                    clamp_bytes((int64_t)(p.N - n0) * rowb));
 #pragma unroll
@@ -115,12 +118,11 @@ gemm_tiled_kernel(const GemmArgs p)
             const bool on_a = g * 64 < 2 * TM;
             const int d = (on_a ? g * 64 : g * 64 - 2 * TM) + lane;
             x_rsrc[j] = on_a ? rXA : rXB;
-            x_voff[j] = (uint32_t)(d >> 1) * rowb + 4u * (uint32_t)(d & 1);
+            x_voff[j] = (on_a ? row_offset<GR>(p, m0, d >> 1, rowb) : (uint32_t)(d >> 1) * rowb) + 4u * (uint32_t)(d & 1);
         }
     } else if constexpr (kXS) {
         const uint32_t kblk = Kb / 128u;   // 128-K blocks per row (fp8: one byte per element)
-        const auto rXA = make_rsrc((const uint8_t *)p.sA + (int64_t)m0 * kblk * kES,
-                                   clamp_bytes((int64_t)(p.M - m0) * kblk * kES));
+        const auto rXA = row_rsrc<GR>(p, p.sA, m0, (int64_t)kblk * kES);
         const int64_t bcol0 = SCALE == kScaleBlock ? n0 / 128 : n0;   // first sB row of the tile
         const int64_t brows = SCALE == kScaleBlock ? p.N / 128 : p.N;
         const auto rXB = make_rsrc((const uint8_t *)p.sB + bcol0 * kblk * kES,
@@ -132,7 +134,7 @@ gemm_tiled_kernel(const GemmArgs p)
                 const int d = g * 64 + lane;
                 const int row = (d % (TM / 16)) * 16 + d / (TM / 16);
                 x_rsrc[j] = rXA;
-                x_voff[j] = (uint32_t)row * kblk * kES;
+                x_voff[j] = row_offset<GR>(p, m0, row, kblk * kES);
             } else {
                 const int d = g * 64 - TM + lane;
                 const int col = (d % (TN / 16)) * 16 + d / (TN / 16);
@@ -689,10 +691,10 @@ gemm_pingpong_kernel(const GemmArgs p)
     }
 }
 
-template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD>
+template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD, int GR = 0>
 void launch_tiled(const GemmArgs &a, dim3 grid, hipStream_t s)
 {
-    gemm_tiled_kernel<DT, TM, TN, WM, WN, KT, DEPTH, SCALE, OUT, PV, PD><<<grid, WM * WN * 64, 0, s>>>(a);
+    gemm_tiled_kernel<DT, TM, TN, WM, WN, KT, DEPTH, SCALE, OUT, PV, PD, GR><<<grid, WM * WN * 64, 0, s>>>(a);
 }
 
 template <int DT, int SCALE, int OUT>
@@ -737,6 +739,23 @@ static const KernelSpec kTiledKernels[] = {
     DGP_TILED_BOTH_OUT(kDtypeFp4, 256, 256, 1, 8, 128, 2, kScaleMx32, 0, 8),
     DGP_TILED_BOTH_OUT(kDtypeFp4, 128, 128, 2, 2, 128, 2, kScaleMx32, 0, 4),
 };
+
+// Product grouped by expert: the tuned 128 x 128 tile of every mode, and
+// blockscale's 256 x 256 one (the other modes' larger tiles: gemm_w4.hip).
+#define DGP_TILEDG(DT, TM, TN, WM, WN, DEPTH, SC, PD)                                          \
+    {kTiled, DT, SC, kOutBf16, TM, TN, 128, WM * WN, WM, WN, 0, PD, DEPTH, kSchedInterleaved,   \
+     &launch_tiled<DT, TM, TN, WM, WN, 128, DEPTH, SC, kOutBf16, 0, PD, 1>}
+static const KernelSpec kTiledGrouped[] = {
+    DGP_TILEDG(kDtypeBf16, 128, 128, 2, 2, 2, kScaleNone, 4), DGP_TILEDG(kDtypeFp8, 128, 128, 2, 2, 2, kScaleTensor, 4),
+    DGP_TILEDG(kDtypeFp8, 128, 128, 2, 2, 2, kScaleBlock, 4), DGP_TILEDG(kDtypeFp8, 128, 128, 2, 2, 2, kScaleMx, 4),
+    DGP_TILEDG(kDtypeFp4, 128, 128, 2, 2, 2, kScaleMx32, 4),  DGP_TILEDG(kDtypeFp8, 256, 256, 1, 8, 2, kScaleBlock, 4),
+};
+
+const KernelSpec *tiled_grouped_kernels(int *count)
+{
+    *count = (int)(sizeof(kTiledGrouped) / sizeof(kTiledGrouped[0]));
+    return kTiledGrouped;
+}
 
 const KernelSpec *tiled_kernels(int *count)
 {

@@ -166,9 +166,11 @@ __device__ inline void mfma_acc_mx4(f32x4 &acc, const i32x4 &b, const i32x4 &a, 
 // quad of row tiles' 8 dwords in two 16-byte reads, and column 64w + 16c + i
 // at dword 512 + 2(4(16w + i) + c) + s; a lane's byte is taken with one
 // bit-field extract per fragment.
-template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM>
+//
+// GR: 1 = the product grouped by expert (gemm_common.h).
+template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM, int GR>
 __global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(256 / TM, 256 / TM)))
-gemm_w4_kernel(const GemmArgs p)
+gemm_w4_kernel(const GemmArgs args)
 {
     static_assert(DB >= 2 && DB <= 4, "B sets");
     constexpr int kDB = DB;
@@ -212,7 +214,10 @@ gemm_w4_kernel(const GemmArgs p)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // This wave's place in the tile: rows wm*TM/WM.., columns wn*64*WM..
     const int wm = WM == 1 ? 0 : wave / 2, wn = WM == 1 ? wave : wave % 2;
-    const auto tc = tile_of_workgroup<int>((int)blockIdx.x, p.tiles_m, p.tiles_n, p.splits, p.remap, p.group_m);
+    GemmArgs p = args;
+    TileCoordT<int> tc;
+    if (!locate_tile<GR, TM, SCALE>(p, tc))
+        return;
     const int m0 = (int)tc.tm * TM;
     const int n0 = (int)tc.tn * TN;
     const int split = (int)tc.s;
@@ -224,7 +229,7 @@ gemm_w4_kernel(const GemmArgs p)
     // group rg, 64-byte chunk ch); lane l's global address selects row
     // 16*rg + l%16, K-bytes 64*ch + 16*(l/16) (the operand-block order of
     // gemm_common.h).  Rows >= M are past the range and load as zero.
-    const auto rA = make_rsrc(p.A + (int64_t)m0 * Kb, clamp_bytes((int64_t)(p.M - m0) * Kb));
+    const auto rA = row_rsrc<GR>(p, p.A, m0, Kb);
     uint32_t dma_voff[kDma];
 #pragma unroll
     for (int j = 0; j < kDma; ++j) {
@@ -234,9 +239,9 @@ gemm_w4_kernel(const GemmArgs p)
             // lands at row 8*blk + l/8, stored chunk l%8, so it fetches logical
             // chunk (l%8) ^ swizzle(row)
             const int r = 8 * blk + (lane >> 3);
-            dma_voff[j] = (uint32_t)r * Kb + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
+            dma_voff[j] = row_offset<GR>(p, m0, r, Kb) + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
         } else {
-            dma_voff[j] = (uint32_t)((blk / kCH) * 16 + (lane & 15)) * Kb +
+            dma_voff[j] = row_offset<GR>(p, m0, (blk / kCH) * 16 + (lane & 15), Kb) +
                           (uint32_t)((blk % kCH) * 64 + (lane >> 4) * 16);
         }
     }
@@ -258,12 +263,12 @@ gemm_w4_kernel(const GemmArgs p)
     // start at byte koff / 16 of a row, koff in K-bytes of two values each.)
     [[maybe_unused]] const int kblk = kMx4 ? p.K / 32 : p.K / 128;
     constexpr bool kX = kMx || kMx4;
-    [[maybe_unused]] const auto rXa = make_rsrc(kX ? static_cast<const uint8_t *>(p.sA) + (int64_t)m0 * kblk : nullptr,
-                                                kX ? clamp_bytes((int64_t)(p.M - m0) * kblk) : 0);
+    [[maybe_unused]] const auto rXa = kX ? row_rsrc<GR>(p, p.sA, m0, kblk) : make_rsrc(nullptr, 0);
     [[maybe_unused]] const auto rXb = make_rsrc(kX ? static_cast<const uint8_t *>(p.sB) + (int64_t)n0 * kblk : nullptr,
                                                 kX ? clamp_bytes((int64_t)(p.N - n0) * kblk) : 0);
-    [[maybe_unused]] const uint32_t xa_voff =
-        (uint32_t)(16 * ((wave * 64 + lane) % 16) + (wave * 64 + lane) / 16) * (uint32_t)kblk;
+    [[maybe_unused]] uint32_t xa_voff = 0;
+    if constexpr (kMx)
+        xa_voff = row_offset<GR>(p, m0, 16 * ((wave * 64 + lane) % 16) + (wave * 64 + lane) / 16, (uint32_t)kblk);
     [[maybe_unused]] const uint32_t xb_voff = (uint32_t)(64 * wave + 16 * (lane & 3) + (lane >> 2)) * (uint32_t)kblk;
     // mxfp4 copy j (0, 1) of this wave: dword e = 128*wave + 64*j + lane of the
     // row region (row 16*((e/2)%16) + e/32, dword e%2) and dword e' = 64*j +
@@ -273,7 +278,8 @@ gemm_w4_kernel(const GemmArgs p)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int e = 128 * wave + 64 * j + lane, e2 = 64 * j + lane;
-        xa4_voff[j] = (uint32_t)(16 * ((e / 2) % 16) + e / 32) * (uint32_t)kblk + 4u * (uint32_t)(e % 2);
+        if constexpr (kMx4)
+            xa4_voff[j] = row_offset<GR>(p, m0, 16 * ((e / 2) % 16) + e / 32, (uint32_t)kblk) + 4u * (uint32_t)(e % 2);
         xb4_voff[j] = (uint32_t)(64 * wave + 16 * ((e2 / 2) % 4) + (e2 / 8) % 16) * (uint32_t)kblk +
                       4u * (uint32_t)(e2 % 2);
     }
@@ -652,10 +658,10 @@ gemm_w4_kernel(const GemmArgs p)
     }
 }
 
-template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM>
+template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM, int GR = 0>
 void launch_w4(const GemmArgs &a, dim3 grid, hipStream_t s)
 {
-    gemm_w4_kernel<DT, SCALE, OUT, DB, SWZ, RA, ILV, SYNC, WM, TM><<<grid, 256, 0, s>>>(a);
+    gemm_w4_kernel<DT, SCALE, OUT, DB, SWZ, RA, ILV, SYNC, WM, TM, GR><<<grid, 256, 0, s>>>(a);
 }
 
 // Table entries: waves (WM x 4/WM), preload pair = (ILV, RA), layout, copy path.
@@ -708,6 +714,22 @@ static const KernelSpec kW4Kernels[] = {
     DGP_W4T(kDtypeFp8, kScaleTensor, kOutPartial, 2, 1, 1, 1, 0, 1, 128),
     DGP_W4T(kDtypeFp8, kScaleTensor, kOutBf16, 2, 1, 3, 1, 0, 1, 128),
 };
+
+// Product grouped by expert: the tuned form of each tile.
+#define DGP_W4G(DT, SC, DB, RA, TM)                                                            \
+    {kTiled, DT, SC, kOutBf16, TM, 256, 128, 4, 1, 4, 1, RA, DB, kSchedW4,                      \
+     &launch_w4<DT, SC, kOutBf16, DB, 1, RA, 1, 0, 1, TM, 1>, kLaySwizzled, kCopyAsync}
+static const KernelSpec kW4Grouped[] = {
+    DGP_W4G(kDtypeBf16, kScaleNone, 3, w4::kRA, 256),   DGP_W4G(kDtypeFp8, kScaleTensor, 3, w4::kRA, 256),
+    DGP_W4G(kDtypeFp8, kScaleMx, 3, w4::kRA, 256),      DGP_W4G(kDtypeFp4, kScaleMx32, 3, w4::kRA, 256),
+    DGP_W4G(kDtypeBf16, kScaleNone, 2, 7, 128),         DGP_W4G(kDtypeFp8, kScaleTensor, 2, 1, 128),
+};
+
+const KernelSpec *w4_grouped_kernels(int *count)
+{
+    *count = (int)(sizeof(kW4Grouped) / sizeof(kW4Grouped[0]));
+    return kW4Grouped;
+}
 
 const KernelSpec *w4_kernels(int *count)
 {

@@ -22,6 +22,12 @@ struct GemmArgs {
     int Ks;               // bytes of K per split
     int tiles_m, tiles_n, splits;
     int remap, group_m;
+    // Product grouped by expert only (the kernels' GR = 1 form): M is the
+    // number of product rows, tiles_m the most row tiles any offsets give.
+    const int32_t *offsets;   // [groups + 1] first row of each expert, then the end
+    const int32_t *rows;      // row of A of each product row, or NULL (row m takes row m)
+    int groups;
+    int a_rows;               // rows of A
 };
 
 // Kernel family selectors.
@@ -69,6 +75,12 @@ const KernelSpec *w4_kernels(int *count);
 const KernelSpec *stream_kernels(int *count);
 const KernelSpec *wave_kernels(int *count);
 const KernelSpec *kernel_table(int *count);
+// The forms compiled for the product grouped by expert (single pass), per
+// family and all of them (dgp_api.cpp).
+const KernelSpec *tiled_grouped_kernels(int *count);
+const KernelSpec *w4_grouped_kernels(int *count);
+const KernelSpec *stream_grouped_kernels(int *count);
+const KernelSpec *grouped_table(int *count);
 
 // Library-owned split-K workspace (noalloc.hip): the size of the fixed
 // per-device array, and its device address on the current device (taken

@@ -292,6 +292,36 @@ dgp_status dgp_gemm_preshuffle_splitk_noalloc(const void *A, const void *Bs, voi
                                               void *stream);
 
 /*
+ * dgp_gemm_preshuffle_grouped -- the product grouped by expert:
+ *
+ *   C[m] = A[rows ? rows[m] : m] * B_e^T   for offsets[e] <= m < offsets[e+1]
+ *
+ * for e < E, with every element type, scale mode and rounding of
+ * dgp_gemm_preshuffle (and its bits, where both take the same tile).  Bs is
+ * E preshuffled weights [N][K] one after the other; scales of B likewise: sB
+ * is fp32 [E] (DGP_SCALE_TENSOR; sA one fp32), fp32 [E][N/128][K/128], E8M0
+ * [E][N][K/128] or E8M0 [E][N][K/32].  offsets is int32 [E+1] in device
+ * memory, so the rows of each expert need not be known on the host: 0 <=
+ * offsets[e] <= offsets[e+1] <= M.  An expert may have no rows; rows of C
+ * that no expert owns (before offsets[0], from offsets[E] on) are left as
+ * they are.  Offsets that break the rule give wrong rows but never touch
+ * memory outside C's M rows.
+ * rows, where not NULL, is int32 [M] in device memory and names the row of A
+ * (and of its scales) that each row of C takes, so tokens that go to several
+ * experts need no copy; a row that A does not have counts as zeros.  A then
+ * has a_rows rows and at most 0xFF000000 bytes; without rows A has a_rows >= M.
+ *
+ * The tile is chosen by the average number of rows of an expert, M / min(E,
+ * M); cfg names another compiled one (16-row K-split tiles, and the tuned
+ * large tiles of each mode).  K > 0; M = 0, N = 0 or E = 0 is a no-op; E <=
+ * 65535.  One launch, no workspace.
+ */
+dgp_status dgp_gemm_preshuffle_grouped(const void *A, int64_t a_rows, const void *Bs, void *C, int64_t M, int64_t N,
+                                       int64_t K, int64_t E, const int32_t *offsets, const int32_t *rows, int dtype,
+                                       int scale_mode, const void *sA, const void *sB, const dgp_config *cfg,
+                                       void *stream);
+
+/*
  * Operators that write an operand of the product
  *
  * Each makes one operand A (dgp_quantize_b: a weight) in the form that a scale

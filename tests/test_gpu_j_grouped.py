@@ -1,0 +1,257 @@
+"""GPU tests of the product grouped by expert (gemm_preshuffle_grouped)
+against 64-bit references: every mode on every compiled tile, ragged and empty
+experts, rows outside every expert, row lists, and the whole chain of a
+mixture-of-experts layer."""
+import pytest
+import torch
+
+import dense_gemm_packer_amd as dgp
+from operand_common import EPS, MODES, dequantize, pow2
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+TILES = {
+    "none": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (128, 256), (256, 256)],
+    "tensor": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (128, 256), (256, 256)],
+    "block128": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (256, 256)],
+    "mx128": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (256, 256)],
+    "mx32": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (256, 256)],
+}
+
+
+def config(tile, remap=1, group_m=8):
+    if tile is None:
+        return None
+    tm, tn = tile
+    return dict(tile_m=tm, tile_n=tn, tile_k=0 if tm <= 32 else 128, xcd_remap=remap, group_m=group_m)
+
+
+def operands(mode, a_rows, e, n, k, seed):
+    g = torch.Generator().manual_seed(seed)
+    a = torch.randn(a_rows, k, generator=g) * torch.exp2(torch.randn(a_rows, 1, generator=g))
+    b = torch.randn(e, n, k, generator=g) * torch.exp2(torch.randn(e, 1, 1, generator=g))
+    if mode == "none":
+        A, B = a.bfloat16().to(DEV), b.bfloat16().to(DEV)
+        Bs = dgp.preshuffle_b(B.view(e * n, k)).view(e, n, k)
+        return A, None, Bs, None, A.cpu().double(), B.cpu().double()
+    A, sA = dgp.quantize(a.to(DEV), MODES[mode])
+    Bs, sB = dgp.quantize_b(b.to(DEV), MODES[mode])
+    codes = dgp.unshuffle_b(Bs.view(e * n, -1)).view(Bs.shape)
+    bd = []
+    for i in range(e):
+        if mode == "block128":
+            s = sB[i].cpu().double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+            bd.append(codes[i].cpu().double() * s)
+        else:
+            bd.append(dequantize(codes[i], sB[i], mode))
+    return A, sA, Bs, sB, dequantize(A, sA, mode), torch.stack(bd)
+
+
+def aligned_loss(a, b):
+    """What the e4m3 matrix instruction may lose: it aligns products to the
+    largest of their group and drops what lies more than 13 binades below it
+    (test_e4m3_alignment), so each of the 128 products of one step loses less
+    than 2^-13 of the step's largest product, which is at most the product of
+    the step's largest factors."""
+    big = lambda v: v.abs().unflatten(-1, (-1, 128)).amax(-1)  # noqa: E731
+    return 128 * 2.0 ** -13 * (big(a) @ big(b).t())
+
+
+def check(C, before, ad, bd, offsets, rows, k, loss=None):
+    """Rows of every expert within half a bf16 step of the 64-bit product, plus
+    one fp32 half step of the operands' magnitudes per addition (and `loss`);
+    the other rows as they were."""
+    got = C.cpu().double()
+    owned = torch.zeros(C.shape[0], dtype=torch.bool)
+    for e in range(len(offsets) - 1):
+        lo, hi = offsets[e], offsets[e + 1]
+        if hi <= lo:
+            continue
+        owned[lo:hi] = True
+        a = ad[lo:hi] if rows is None else ad[rows[lo:hi]]
+        want = a @ bd[e].t()
+        bound = 2.0 ** -8 * want.abs() + (k + 8) * EPS * (a.abs() @ bd[e].abs().t()) + 2.0 ** -133
+        if loss is not None:
+            bound = bound + loss(a, bd[e])
+        bad = ((got[lo:hi] - want).abs() > bound).nonzero()
+        assert bad.numel() == 0, f"expert {e}: row {int(bad[0, 0])} column {int(bad[0, 1])}"
+    assert torch.equal(C.cpu()[~owned].view(torch.int16), before[~owned].view(torch.int16))
+
+
+def run(mode, counts, n, k, seed, tile=None, gather=False, lead=0, pad=0, remap=1, group_m=8):
+    e = len(counts)
+    offsets = [lead]
+    for c in counts:
+        offsets.append(offsets[-1] + c)
+    m = offsets[-1] + pad
+    a_rows = max(1, m // 2) if gather else m
+    A, sA, Bs, sB, ad, bd = operands(mode, a_rows, e, n, k, seed)
+    rows = torch.randint(0, a_rows, (m,), generator=torch.Generator().manual_seed(seed + 1)) if gather else None
+    before = torch.randn(m, n, generator=torch.Generator().manual_seed(seed + 2)).bfloat16()
+    out = before.to(DEV)
+    C = dgp.gemm_preshuffle_grouped(A, Bs, torch.tensor(offsets, dtype=torch.int32, device=DEV), sA, sB, MODES[mode],
+                                    rows=None if rows is None else rows.to(torch.int32).to(DEV), out=out,
+                                    config=config(tile, remap, group_m))
+    torch.cuda.synchronize()
+    assert C is out
+    check(C, before, ad, bd, offsets, rows, k)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("mode,tile", [(m, t) for m, ts in TILES.items() for t in ts])
+def test_every_tile(mode, tile, gather):
+    run(mode, [5, 0, 33, 1, 300, 0, 17], 384, 1024, 7, tile, gather, lead=3, pad=6)
+
+
+@pytest.mark.parametrize("mode", list(MODES))
+@pytest.mark.parametrize("counts", [[1], [0, 0, 1], [16, 16], [40, 90, 7, 0], [700, 3], [0, 0], [260, 250, 0, 255]])
+def test_built_in_choice(mode, counts):
+    run(mode, counts, 256, 512, 11, gather=len(counts) % 2 == 0, pad=len(counts))
+
+
+@pytest.mark.parametrize("tile", [None, (16, 32), (128, 128)])
+@pytest.mark.parametrize("e", [63, 64, 65, 130, 200])
+def test_many_experts(e, tile):
+    g = torch.Generator().manual_seed(e)
+    counts = (torch.randint(0, 9, (e,), generator=g) * (torch.rand(e, generator=g) < 0.6)).tolist()
+    run("mx128", counts, 128, 128, 13, tile, gather=True)
+
+
+@pytest.mark.parametrize("mode", list(MODES))
+def test_one_token(mode):
+    """One token through 8 of 20 experts."""
+    counts = [0] * 20
+    for e in (0, 3, 4, 9, 10, 11, 18, 19):
+        counts[e] = 1
+    run(mode, counts, 256, 7168, 17, gather=True)
+
+
+@pytest.mark.parametrize("tile", [(16, 32), (128, 128), (256, 256)])
+@pytest.mark.parametrize("remap,group_m", [(0, 1), (1, 1), (1, 3)])
+def test_tile_order(tile, remap, group_m):
+    run("none", [130, 0, 1, 515], 640, 256, 19, tile, True, remap=remap, group_m=group_m)
+
+
+def test_matches_the_single_product():
+    """One expert with all rows: the bits of gemm_preshuffle on the same tile."""
+    for mode in MODES:
+        A, sA, Bs, sB, _, _ = operands(mode, 300, 1, 256, 1024, 23)
+        off = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+        cfg = dict(tile_m=128, tile_n=128, tile_k=128, xcd_remap=1, group_m=8)
+        C = dgp.gemm_preshuffle_grouped(A, Bs, off, sA, sB, MODES[mode], config=cfg)
+        D = dgp.gemm_preshuffle(A, Bs[0], sA, sB, MODES[mode], config=cfg)
+        assert torch.equal(C.view(torch.int16), D.view(torch.int16)), mode
+
+
+@pytest.mark.parametrize("mode", list(MODES))
+@pytest.mark.parametrize("tile", [(16, 64), (128, 128), (256, 256)])
+def test_rows_that_a_does_not_have_count_as_zeros(mode, tile):
+    m, n, k = 40, 256, 512
+    A, sA, Bs, sB, ad, bd = operands(mode, 9, 2, n, k, 29)
+    rows = torch.randint(0, 9, (m,), generator=torch.Generator().manual_seed(3)).to(torch.int32)
+    bad = [0, 7, 21, 39]
+    rows[bad] = torch.tensor([-1, 9, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    off = torch.tensor([0, 20, 40], dtype=torch.int32, device=DEV)
+    C = dgp.gemm_preshuffle_grouped(A, Bs, off, sA, sB, MODES[mode], rows=rows.to(DEV), config=config(tile))
+    C = C.cpu()
+    assert bool((C[bad] == 0).all())
+    keep = [i for i in range(m) if i not in bad]
+    for e, lo, hi in ((0, 0, 20), (1, 20, 40)):
+        idx = [i for i in keep if lo <= i < hi]
+        want = ad[rows[idx].long()] @ bd[e].t()
+        bound = 2.0 ** -8 * want.abs() + (k + 8) * EPS * (ad[rows[idx].long()].abs() @ bd[e].abs().t())
+        assert bool(((C[idx].double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("offsets", [[0, 50, 20, 64], [-7, 10, 30, 64], [0, 10, 30, 1 << 30], [90, 95, 100, 110],
+                                     [64, 0, 64, 0], [-2 ** 31, 2 ** 31 - 1, -5, 2 ** 31 - 1]])
+@pytest.mark.parametrize("tile", [(16, 16), (128, 128), (256, 256)])
+def test_offsets_that_break_the_rule_stay_inside_c(offsets, tile):
+    """Nothing is written past C's rows, whatever the offsets (they are clamped on the device)."""
+    m, n, k = 64, 128, 256
+    A, _, Bs, _, _, _ = operands("none", m, 3, n, k, 31)
+    buf = torch.full((m + 64, n), 3.0, dtype=torch.bfloat16, device=DEV)
+    dgp.gemm_preshuffle_grouped(A, Bs, torch.tensor(offsets, dtype=torch.int32, device=DEV), out=buf[32:32 + m],
+                                config=config(tile))
+    torch.cuda.synchronize()
+    assert bool((buf[:32] == 3.0).all()) and bool((buf[32 + m:] == 3.0).all())
+
+
+def test_captured_with_changing_routes():
+    """A captured product follows the offsets and the row list on every replay."""
+    m, n, k, e = 48, 256, 512, 6
+    A, sA, Bs, sB, ad, bd = operands("mx128", 20, e, n, k, 37)
+    off = torch.zeros(e + 1, dtype=torch.int32, device=DEV)
+    rows = torch.zeros(m, dtype=torch.int32, device=DEV)
+    out = torch.zeros(m, n, dtype=torch.bfloat16, device=DEV)
+    call = lambda: dgp.gemm_preshuffle_grouped(A, Bs, off, sA, sB, dgp.SCALE_MX128, rows=rows, out=out)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed in range(4):
+        g = torch.Generator().manual_seed(seed)
+        cuts = torch.sort(torch.randint(0, m + 1, (e - 1,), generator=g))[0].tolist()
+        offsets = [0] + cuts + [m - seed]
+        offsets[-1] = max(offsets[-1], offsets[-2])
+        r = torch.randint(0, 20, (m,), generator=g)
+        before = torch.randn(m, n, generator=g).bfloat16()
+        off.copy_(torch.tensor(offsets, dtype=torch.int32))
+        rows.copy_(r)
+        out.copy_(before)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, before, ad, bd, offsets, r, k)
+
+
+@pytest.mark.parametrize("mode", ["none", "block128", "mx128", "mx32"])
+@pytest.mark.parametrize("tokens", [1, 50])
+def test_mixture_of_experts_layer(mode, tokens):
+    """Norm with residual -> first product -> gated activation -> second
+    product, as one layer runs them, against 64 bits on the operands that the
+    quantising steps wrote."""
+    hidden, inner, e, topk = 512, 256, 5, 2
+    g = torch.Generator().manual_seed(tokens)
+    x = torch.randn(tokens, hidden, generator=g).bfloat16()
+    res = torch.randn(tokens, hidden, generator=g).bfloat16()
+    w = (1 + 0.1 * torch.randn(hidden, generator=g)).bfloat16()
+    route = torch.stack([torch.randperm(e, generator=g)[:topk] for _ in range(tokens)])
+    order = torch.argsort(route.flatten(), stable=True)
+    rows = (order // topk).to(torch.int32)
+    counts = torch.bincount(route.flatten(), minlength=e)
+    offsets = [0] + torch.cumsum(counts, 0).tolist()
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    _, _, B1, s1, _, bd1 = operands(mode, 1, e, 2 * inner, hidden, 41)
+    _, _, B2, s2, _, bd2 = operands(mode, 1, e, hidden, inner, 43)
+    A, sA, H = dgp.rmsnorm_quantize(x.to(DEV), w.to(DEV), MODES[mode], residual=res.to(DEV))
+    h = x.double() + res.double()
+    assert bool(((H.cpu().double() - h).abs() <= h.abs() * (2.0 ** -8 + EPS)).all())
+    y = h / torch.sqrt((h * h).mean(-1, keepdim=True) + 1e-6) * w.double()
+    ad = dequantize(A, sA, mode)
+    worst = {"none": 2.0 ** -8, "block128": 2.0 ** -4, "mx128": 2.0 ** -4, "mx32": 2.0 ** -2}[mode]
+    assert float((ad - y).norm() / y.norm()) <= worst
+    C1 = dgp.gemm_preshuffle_grouped(A, B1, off, sA, s1, MODES[mode], rows=rows.to(DEV))
+    loss = aligned_loss if mode in ("block128", "mx128") else None
+    check(C1, C1.cpu(), ad, bd1, offsets, rows.long(), hidden, loss)
+    A2, sA2 = dgp.swiglu_quantize(C1[:, :inner], C1[:, inner:], MODES[mode])
+    c1 = C1.cpu().double()
+    z = c1[:, :inner] * torch.sigmoid(c1[:, :inner]) * c1[:, inner:]
+    ad2 = dequantize(A2, sA2, mode)
+    assert float((ad2 - z).norm() / z.norm()) <= worst
+    C2 = dgp.gemm_preshuffle_grouped(A2, B2, off, sA2, s2, MODES[mode])
+    check(C2, C2.cpu(), ad2, bd2, offsets, None, inner, loss)
+
+
+def test_e4m3_alignment():
+    """2^16 - 2^16 + s in neighbouring K: s = 2^3, 13 binades below the largest
+    product, survives; through this library's e4m3 product."""
+    A, B = torch.zeros(1, 128), torch.zeros(16, 128)
+    A[:, 0], A[:, 1], A[:, 2] = 256, -256, 8
+    B[:, 0], B[:, 1], B[:, 2] = 256, 256, 1
+    one = torch.ones(1, device=DEV)
+    Bs = dgp.preshuffle_b(B.to(torch.float8_e4m3fn).to(DEV))
+    C = dgp.gemm_preshuffle(A.to(torch.float8_e4m3fn).to(DEV), Bs, one, one, dgp.SCALE_TENSOR)
+    assert bool((C == 8).all())

@@ -159,3 +159,53 @@ def test_binding_shape_checks(dgp):
         dgp._mode(17, True)
     with pytest.raises(TypeError):
         dgp.input_code(bf.double())
+
+
+def grouped(L, A=P, a_rows=64, Bs=P, C=P, M=64, N=128, K=256, E=4, offsets=P, rows=None, dtype=FP8, mode=MX, sA=P, sB=P,
+            cfg=None):
+    return L.dgp_gemm_preshuffle_grouped(A, a_rows, Bs, C, M, N, K, E, offsets, rows, dtype, mode, sA, sB, cfg, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=F16), DTYPE), (dict(dtype=F32), DTYPE), (dict(mode=NONE), SCALE), (dict(dtype=BF16), SCALE),
+    (dict(dtype=FP4, mode=MX), SCALE), (dict(M=-1), SHAPE), (dict(N=120), SHAPE), (dict(K=0), SHAPE), (dict(K=192), SHAPE),
+    (dict(mode=BLOCK, N=64), SHAPE), (dict(E=-1), SHAPE), (dict(E=65536), SHAPE), (dict(a_rows=-1), SHAPE),
+    (dict(a_rows=63), SHAPE), (dict(rows=P, a_rows=0), SHAPE), (dict(rows=P, a_rows=1 << 25), SHAPE),
+    (dict(A=None), NULL), (dict(Bs=None), NULL), (dict(C=None), NULL), (dict(offsets=None), NULL), (dict(sA=None), NULL),
+    (dict(A=P + 8), ALIGN), (dict(C=P + 4), ALIGN), (dict(offsets=P + 2), ALIGN), (dict(rows=P + 1), ALIGN),
+    (dict(sA=P + 2, mode=BLOCK), ALIGN),
+    (dict(M=1 << 29, a_rows=1 << 29, N=1 << 20), SHAPE),
+])
+def test_grouped_refusals(L, kw, status):
+    assert grouped(L, **kw) == status
+
+
+def test_grouped_configurations(L, dgp):
+    for cfg in (dict(tile_m=64, tile_n=128, tile_k=128), dict(tile_m=1, tile_n=16), dict(tile_m=16, tile_n=32, waves_m=2),
+                dict(tile_m=128, tile_n=128, tile_k=128, schedule=3), dict(tile_m=256, tile_n=256, tile_k=64)):
+        c = dgp.Config(**cfg)
+        assert grouped(L, cfg=ctypes.byref(c)) == CONFIG, cfg
+    assert grouped(L, M=0, A=None, Bs=None, C=None, offsets=None) == OK
+    assert grouped(L, E=0, A=None, Bs=None, C=None, offsets=None) == OK
+
+
+def test_grouped_binding_checks(dgp):
+    A = torch.zeros(6, 256, dtype=torch.bfloat16)
+    Bs = torch.zeros(3, 32, 256, dtype=torch.bfloat16)
+    off = torch.zeros(4, dtype=torch.int32)
+    rows = torch.zeros(9, dtype=torch.int32)
+    ok = lambda **kw: dgp.check_grouped_operands(**{**dict(A=A, Bs=Bs, offsets=off, sA=None, sB=None,  # noqa: E731
+                                                          mode=dgp.SCALE_NONE, rows=None, out=None), **kw})
+    ok()
+    ok(rows=rows, out=torch.zeros(9, 32, dtype=torch.bfloat16))
+    for kw in (dict(A=A[0]), dict(Bs=Bs[0]), dict(Bs=Bs.half()), dict(Bs=Bs[:, :, :128]), dict(offsets=off[:3]),
+               dict(offsets=off.long()), dict(rows=rows.long()), dict(rows=rows.view(3, 3)),
+               dict(out=torch.zeros(6, 32)), dict(rows=rows, out=torch.zeros(6, 32, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            ok(**kw)
+    f8 = dict(A=A.to(torch.float8_e4m3fn), Bs=Bs.to(torch.float8_e4m3fn), mode=dgp.SCALE_TENSOR)
+    ok(**f8, sA=torch.ones(1), sB=torch.ones(3))
+    with pytest.raises(ValueError):
+        ok(**f8, sA=torch.ones(1), sB=torch.ones(1))
+    with pytest.raises(ValueError):
+        ok(**{**f8, "mode": dgp.SCALE_MX128}, sA=torch.ones(12), sB=torch.ones(192))
