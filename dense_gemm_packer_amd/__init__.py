@@ -183,9 +183,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# (the handle without a Stream object around it, where torch has it: 1 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def _stream_handle(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -252,12 +260,21 @@ def check_gemm_operands(A: torch.Tensor, Bs: torch.Tensor, sA, sB, mode: int, ou
                              f"(got {t.numel()} {t.dtype})")
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _alloc_stream(stream):
     """Context in which outputs and workspaces are allocated: the launch
     stream, so the caching allocator never hands their memory to other work
     while the kernels that use it are still queued there."""
-    import contextlib
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _new(stream, dtype, device, *shape) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _config(config):
@@ -432,8 +449,7 @@ def gemm_preshuffle_grouped(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Te
     M = A.shape[0] if rows is None else rows.shape[0]
     E, N = Bs.shape[:2]
     if out is None:
-        with _alloc_stream(stream):
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = _new(stream, torch.bfloat16, A.device, M, N)
     _enqueue(A, stream, lib().dgp_gemm_preshuffle_grouped, A.data_ptr(), A.shape[0], Bs.data_ptr(), out.data_ptr(), M,
              N, k_elements(A), E, offsets.data_ptr(), _ptr(rows), dtype_code(A), mode, _ptr(sA), _ptr(sB),
              _config(config))
@@ -485,18 +501,20 @@ def _rows(t: torch.Tensor, what: str, shape=None, like: torch.Tensor | None = No
     """Checks a strided [M][K] input on the device; returns its row stride in elements."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be 2-D (got {t.dim()}-D)")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what} must be {tuple(shape)} (got {tuple(t.shape)})")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{what} is {t.dtype} on {t.device}, X {like.dtype} on {like.device}")
-    M, K = t.shape
-    if K > 1 and t.stride(1) != 1:
+    mine = t.shape
+    if len(mine) != 2:
+        raise ValueError(f"{what} must be 2-D (got {len(mine)}-D)")
+    if shape is not None:
+        if mine != shape:
+            raise ValueError(f"{what} must be {tuple(shape)} (got {tuple(mine)})")
+        if t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{what} is {t.dtype} on {t.device}, X {like.dtype} on {like.device}")
+    M, K = mine
+    ld, one = t.stride()
+    if one != 1 and K > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
     if M <= 1:
         return K
-    ld = t.stride(0)
     if ld < K:
         raise ValueError(f"{what}: rows overlap (stride {ld}, {K} elements)")
     return ld
@@ -515,12 +533,16 @@ def _mode(scale_mode: int, allow_none: bool) -> None:
         raise DgpError(5, f"scale mode {scale_mode} is not one this operator writes")
 
 
+# Columns per scale, and of the codes' tensor per element, of each mode.
+_BLOCK = {SCALE_BLOCK128: 128, SCALE_MX128: 128, SCALE_MX32: 32}
+
+
 def _operand_out(X, M, K, mode, scale, out, scales, stream):
     """Checks or allocates the codes and scales of an [M][K] operand; returns
     (Q, S) (S: the given scale, or None without scales)."""
-    block = {SCALE_BLOCK128: 128, SCALE_MX128: 128, SCALE_MX32: 32}.get(mode)
-    qshape = (M, K // 2) if mode == SCALE_MX32 else (M, K)
-    sshape = (1,) if block is None else (M, K // block)
+    cols = K // 2 if mode == SCALE_MX32 else K
+    if out is not None:
+        _dense(out, _CODES[mode], (M, cols), X, "out")
     if scale is not None:
         if mode != SCALE_TENSOR:
             raise DgpError(5, "a given scale goes with SCALE_TENSOR only")
@@ -529,19 +551,19 @@ def _operand_out(X, M, K, mode, scale, out, scales, stream):
         if scale.numel() != 1:
             raise ValueError(f"scale must hold one value (got {scale.numel()})")
         _dense(scale, torch.float32, scale.shape, X, "scale")
-    if out is not None:
-        _dense(out, _CODES[mode], qshape, X, "out")
-    if scales is not None:
-        if mode == SCALE_NONE:
+        scales = scale
+    elif mode == SCALE_NONE:
+        if scales is not None:
             raise ValueError("SCALE_NONE writes no scales")
-        _dense(scales, _SCALES[mode], sshape, X, "scales")
-    if out is None or (scales is None and scale is None and mode != SCALE_NONE):
-        with _alloc_stream(stream):
-            if out is None:
-                out = torch.empty(qshape, dtype=_CODES[mode], device=X.device)
-            if scales is None and scale is None and mode != SCALE_NONE:
-                scales = torch.empty(sshape, dtype=_SCALES[mode], device=X.device)
-    return out, scale if scale is not None else scales
+    else:
+        shape = (1,) if mode == SCALE_TENSOR else (M, K // _BLOCK[mode])
+        if scales is None:
+            scales = _new(stream, _SCALES[mode], X.device, *shape)
+        else:
+            _dense(scales, _SCALES[mode], shape, X, "scales")
+    if out is None:
+        out = _new(stream, _CODES[mode], X.device, M, cols)
+    return out, scales
 
 
 def _enqueue(X: torch.Tensor, stream, fn, *args) -> None:
@@ -552,10 +574,14 @@ def _enqueue(X: torch.Tensor, stream, fn, *args) -> None:
         with torch.cuda.device(index):
             return _enqueue(X, stream, fn, *args)
     if stream is None:
-        stream = torch.cuda.current_stream(index)
+        handle = _raw_stream(index)
     elif stream.device != X.device:
         raise ValueError(f"stream is on {stream.device}, the input on {X.device}")
-    _check(fn(*args, stream.cuda_stream))
+    else:
+        handle = stream.cuda_stream
+    status = fn(*args, handle)
+    if status != 0:
+        _check(status)
 
 
 def quantize(X: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -569,9 +595,7 @@ def quantize(X: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None
     Q, S = _operand_out(X, M, K, scale_mode, scale, out, scales, stream)
     ws = None
     if scale_mode == SCALE_TENSOR and scale is None:
-        with _alloc_stream(stream):
-            ws = torch.empty(lib().dgp_quantize_workspace_bytes(1, scale_mode) // 4, dtype=torch.float32,
-                             device=X.device)
+        ws = _new(stream, torch.float32, X.device, lib().dgp_quantize_workspace_bytes(1, scale_mode) // 4)
     _enqueue(X, stream, lib().dgp_quantize, X.data_ptr(), ld, input_code(X), Q.data_ptr(),
              None if scale is not None else S.data_ptr(), _ptr(scale), M, K, scale_mode, _ptr(ws),
              0 if ws is None else ws.numel() * 4)
@@ -600,12 +624,11 @@ def quantize_b(B: torch.Tensor, scale_mode: int, out: torch.Tensor | None = None
     if scales is not None:
         _dense(scales, _SCALES[scale_mode], sshape, B, "scales")
     need = lib().dgp_quantize_workspace_bytes(E, scale_mode)
-    with _alloc_stream(stream):
-        if out is None:
-            out = torch.empty(qshape, dtype=_CODES[scale_mode], device=B.device)
-        if scales is None:
-            scales = torch.empty(sshape, dtype=_SCALES[scale_mode], device=B.device)
-        ws = torch.empty(need // 4, dtype=torch.float32, device=B.device) if need else None
+    if out is None:
+        out = _new(stream, _CODES[scale_mode], B.device, *qshape)
+    if scales is None:
+        scales = _new(stream, _SCALES[scale_mode], B.device, *sshape)
+    ws = _new(stream, torch.float32, B.device, need // 4) if need else None
     _enqueue(B, stream, lib().dgp_quantize_b, B.data_ptr(), code, out.data_ptr(), scales.data_ptr(), E, N, K,
              scale_mode, _ptr(ws), need)
     return out, scales
@@ -636,8 +659,7 @@ def rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, scale_mode: int, res
         _dense(residual_out, X.dtype, X.shape, X, "residual_out")
     Q, S = _operand_out(X, M, K, scale_mode, scale, out, scales, stream)
     if residual is not None and residual_out is None:
-        with _alloc_stream(stream):
-            residual_out = torch.empty((M, K), dtype=X.dtype, device=X.device)
+        residual_out = _new(stream, X.dtype, X.device, M, K)
     _enqueue(X, stream, lib().dgp_rmsnorm_quantize, X.data_ptr(), ldx, _ptr(residual), ldr, code, weight.data_ptr(),
              input_code(weight), eps, Q.data_ptr(), None if scale is not None else _ptr(S), _ptr(scale),
              _ptr(residual_out), M, K, scale_mode)

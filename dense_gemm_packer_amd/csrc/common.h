@@ -21,6 +21,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kNumXcd = 8;          // gfx950: 8 XCDs, workgroups dealt round-robin
+constexpr int kNumCu = 256;         // compute units of all XCDs
 constexpr int kDtypeBf16 = 0;
 constexpr int kDtypeFp8 = 1;
 constexpr int kDtypeFp4 = 2;         // OCP E2M1, two per byte

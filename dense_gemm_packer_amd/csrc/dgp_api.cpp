@@ -6,8 +6,10 @@
 // allocates device memory or synchronises.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstdarg>
 #include <cstdio>
@@ -608,17 +610,65 @@ int64_t most_row_tiles(int64_t M, int64_t E, int64_t tm)
     return (M + live * (tm - 1)) / tm;
 }
 
-// Built-in choice for M rows over E experts.  Only the average row count is
-// known on the host.
-const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t N, int64_t E)
+// Built-in choice for M rows over E experts, of which the host knows the
+// average only: the tile with the least estimated time
+//
+//   (a + b k) (1 + s (x - 1)),  k = 128-byte k-steps, x = tiles on the busiest CU,
+//
+// a, b, s fitted per element type and tile to graph timings of 90 random
+// shapes (1 to 64 experts with 1 to 1000 rows each, unevenly filled, N 128 to
+// 7168, K 256 to 8192): a is the launch, the search for the tile and the
+// epilogue (us), b the k-step of a tile that has its CU to itself, s what a
+// further tile on the same CU adds (below 1 where two overlap, above it where
+// they contend).  The fit is within 8-20 % of a timing, and the tile it picks
+// is on average 1-2 % slower than the fastest one of its shape (at worst 35 %,
+// where several are within a few us of the launch).  Any one tile left out
+// costs 1-3 % on average and up to 80 % at worst, so all of them stay; a
+// 128 x 128 tile and a half-strip one were never missed and are not compiled.
+struct GroupedTile {
+    int tm, tn;
+    double a, b, s;
+};
+constexpr int kGroupedTiles = 8;
+constexpr GroupedTile kGroupedCost[5][kGroupedTiles] = {
+    // bf16
+    {{16, 16, 2.00, 0.114, 0.39}, {16, 32, 2.05, 0.140, 0.46}, {16, 64, 1.97, 0.213, 0.68}, {64, 64, 2.51, 0.275, 0.88},
+     {64, 128, 3.29, 0.341, 0.97}, {64, 256, 3.64, 0.460, 1.45}, {128, 256, 5.28, 0.558, 1.13}, {256, 256, 7.55, 0.994, 1.32}},
+    // fp8, per-tensor scales
+    {{16, 16, 2.58, 0.101, 0.39}, {16, 32, 2.61, 0.124, 0.42}, {16, 64, 2.71, 0.188, 0.79}, {64, 64, 2.76, 0.288, 0.74},
+     {64, 128, 3.47, 0.356, 0.87}, {64, 256, 3.97, 0.466, 1.22}, {128, 256, 5.30, 0.631, 0.93}, {256, 256, 8.22, 0.945, 1.26}},
+    // fp8, blockscale
+    {{16, 16, 2.86, 0.107, 0.61}, {16, 32, 2.64, 0.140, 0.45}, {16, 64, 2.74, 0.204, 0.80}, {64, 64, 2.99, 0.317, 0.69},
+     {64, 128, 3.67, 0.458, 0.74}, {64, 256, 4.25, 0.591, 1.10}, {128, 256, 4.85, 0.873, 1.25}, {256, 256, 5.52, 1.764, 1.27}},
+    // mxfp8
+    {{16, 16, 2.81, 0.115, 0.61}, {16, 32, 2.67, 0.151, 0.45}, {16, 64, 2.70, 0.225, 0.82}, {64, 64, 2.88, 0.302, 0.72},
+     {64, 128, 3.53, 0.409, 0.85}, {64, 256, 4.24, 0.581, 1.22}, {128, 256, 4.54, 0.787, 1.40}, {256, 256, 8.04, 1.012, 1.24}},
+    // mxfp4
+    {{16, 16, 3.04, 0.121, 0.32}, {16, 32, 2.92, 0.168, 0.41}, {16, 64, 2.99, 0.256, 0.75}, {64, 64, 3.03, 0.388, 0.62},
+     {64, 128, 3.61, 0.529, 0.70}, {64, 256, 4.04, 0.693, 1.14}, {128, 256, 4.46, 1.020, 1.36}, {256, 256, 8.43, 1.382, 1.21}},
+};
+
+// Row tiles to expect: one expert's are known; several leave half a tile each
+// unfilled on average once they have more rows than half a tile.
+double expected_row_tiles(int64_t M, int64_t E, int tm)
 {
     const int64_t live = E < M ? E : M;
-    const int64_t per = (M + live - 1) / live;
-    Query q{kStream, dtype, scale, kOutBf16, 16, N >= 64 ? 64 : 16};
-    if (per > 48) {
-        q = Query{kTiled, dtype, scale, kOutBf16, per > 160 ? 256 : 128, per > 160 ? 256 : 128};
+    if (E == 1)
+        return (double)((M + tm - 1) / tm);
+    return 2 * M > live * tm ? std::max((double)live, (double)M / tm + 0.5 * live) : (double)live;
+}
+
+const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t N, int64_t Kb, int64_t E)
+{
+    const GroupedTile *best = nullptr;
+    double least = 0;
+    for (const GroupedTile &t : kGroupedCost[scale]) {
+        const double x = std::ceil(expected_row_tiles(M, E, t.tm) * (double)((N + t.tn - 1) / t.tn) / kNumCu);
+        const double us = (t.a + t.b * (double)(Kb / 128)) * (1 + t.s * (x - 1));
+        if (!best || us < least)
+            best = &t, least = us;
     }
-    return find_spec(q, grouped_table);
+    return find_spec(Query{best->tm == 16 ? kStream : kTiled, dtype, scale, kOutBf16, best->tm, best->tn}, grouped_table);
 }
 
 struct Experts {
@@ -653,7 +703,7 @@ dgp_status run_grouped(const GemmCall &c, const Experts &x, hipStream_t stream)
     if (c.cfg && c.cfg->tile_m > 0)
         DGP_TRY(configured_spec(c, Kb, grouped_table, &spec));
     else
-        spec = default_grouped_spec(c.dtype, c.scale, c.M, c.N, x.E);
+        spec = default_grouped_spec(c.dtype, c.scale, c.M, c.N, Kb, x.E);
     if (!spec)
         return fail(DGP_ERR_CONFIG, "no compiled grouped kernel fits this shape");
     const int64_t tiles_m = most_row_tiles(c.M, x.E, spec->tm), tiles_n = (c.N + spec->tn - 1) / spec->tn;

@@ -689,8 +689,7 @@ static const KernelSpec kStreamKernels[] = {
     {kStream, DT, SC, kOutBf16, 16, TN, 0, 8, (TN >= 16 ? TN / 16 : 1), DEPTH, 0, 0, DEPTH, 0,      \
      &launch_ksplit<DT, 8, DEPTH, SC, kOutBf16, TN, 1>}
 #define DGP_KSPLITG_ALL(DT, DEPTH, DEPTH32, SC)                                                \
-    DGP_KSPLITG(DT, DEPTH, SC, 8), DGP_KSPLITG(DT, DEPTH, SC, 16), DGP_KSPLITG(DT, DEPTH32, SC, 32),  \
-        DGP_KSPLITG(DT, DEPTH, SC, 64)
+    DGP_KSPLITG(DT, DEPTH, SC, 16), DGP_KSPLITG(DT, DEPTH32, SC, 32), DGP_KSPLITG(DT, DEPTH, SC, 64)
 static const KernelSpec kStreamGrouped[] = {
     DGP_KSPLITG_ALL(kDtypeBf16, 4, 4, kScaleNone), DGP_KSPLITG_ALL(kDtypeFp8, 4, 4, kScaleTensor),
     DGP_KSPLITG_ALL(kDtypeFp8, 4, 4, kScaleBlock), DGP_KSPLITG_ALL(kDtypeFp8, 4, 3, kScaleMx),

@@ -49,12 +49,15 @@ gemm_tiled_kernel(const GemmArgs args)
     constexpr bool kXS = SCALE == kScaleBlock || SCALE == kScaleMx || kX4;
     constexpr int kES = SCALE == kScaleMx ? 1 : 4;             // bytes per scale copy
     constexpr int kXDwords = kX4 ? 2 * (TM + TN) : kXS ? TM + TN : 0;
-    constexpr int kXDma = kXDwords / (64 * S::kWaves);        // scale copies per wave per k-tile
-    static_assert(!kXS || (KT == 128 && kXDwords % (64 * S::kWaves) == 0 && TM % 64 == 0 &&
+    // Scale copies per wave per k-tile; where they cover more than the area
+    // (the 64-row tiles), the rest lands, as zeros, in padding behind it.
+    constexpr int kXDma = (kXDwords + 64 * S::kWaves - 1) / (64 * S::kWaves);
+    constexpr int kXArea = kXDma * 64 * S::kWaves;
+    static_assert(!kXS || (KT == 128 && kXDwords % 64 == 0 && TM % 64 == 0 &&
                            (kX4 ? DT == kDtypeFp4 : DT == kDtypeFp8 && S::kMT % 4 == 0) &&
                            (S::kNT == 2 || S::kNT == 4)),
                   "staged scales: one 128-byte k-tile per scale stage, whole copies per wave");
-    constexpr int kStageBytes = S::kBufBytes + kXDwords * 4;
+    constexpr int kStageBytes = S::kBufBytes + kXArea * 4;
     static_assert(DEPTH >= 1 && (DEPTH + 1) * kStageBytes <= 160 * 1024, "A ring must fit in LDS");
     // Prefetch distance DEPTH k-tiles: a ring of DEPTH+1 A buffers in LDS and
     // DEPTH sets of B registers.
@@ -118,6 +121,8 @@ gemm_tiled_kernel(const GemmArgs args)
             const bool on_a = g * 64 < 2 * TM;
             const int d = (on_a ? g * 64 : g * 64 - 2 * TM) + lane;
             x_rsrc[j] = on_a ? rXA : rXB;
+            if constexpr (kXArea != kXDwords)
+                x_rsrc[j] = g * 64 < kXDwords ? x_rsrc[j] : make_rsrc(nullptr, 0);
             x_voff[j] = (on_a ? row_offset<GR>(p, m0, d >> 1, rowb) : (uint32_t)(d >> 1) * rowb) + 4u * (uint32_t)(d & 1);
         }
     } else if constexpr (kXS) {
@@ -139,6 +144,8 @@ gemm_tiled_kernel(const GemmArgs args)
                 const int d = g * 64 - TM + lane;
                 const int col = (d % (TN / 16)) * 16 + d / (TN / 16);
                 x_rsrc[j] = rXB;
+                if constexpr (kXArea != kXDwords)
+                    x_rsrc[j] = g * 64 < kXDwords ? rXB : make_rsrc(nullptr, 0);
                 x_voff[j] = (uint32_t)(SCALE == kScaleBlock ? col / 128 : col) * kblk * kES;
             }
         }
@@ -740,15 +747,25 @@ static const KernelSpec kTiledKernels[] = {
     DGP_TILED_BOTH_OUT(kDtypeFp4, 128, 128, 2, 2, 128, 2, kScaleMx32, 0, 4),
 };
 
-// Product grouped by expert: the tuned 128 x 128 tile of every mode, and
-// blockscale's 256 x 256 one (the other modes' larger tiles: gemm_w4.hip).
+// Product grouped by expert: 64-row tiles for experts with a few dozen rows
+// (two or four waves side by side, each all 64 rows and 32 or 64 columns; two
+// or three workgroups share a CU), and the larger tiles of the modes that
+// gemm_w4.hip does not have them for.
 #define DGP_TILEDG(DT, TM, TN, WM, WN, DEPTH, SC, PD)                                          \
     {kTiled, DT, SC, kOutBf16, TM, TN, 128, WM * WN, WM, WN, 0, PD, DEPTH, kSchedInterleaved,   \
      &launch_tiled<DT, TM, TN, WM, WN, 128, DEPTH, SC, kOutBf16, 0, PD, 1>}
+#define DGP_TILEDG_ALL(TM, TN, WM, WN, PD)                                                     \
+    DGP_TILEDG(kDtypeBf16, TM, TN, WM, WN, 2, kScaleNone, PD), DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, 2, kScaleTensor, PD), \
+        DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, 2, kScaleBlock, PD), DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, 2, kScaleMx, PD), \
+        DGP_TILEDG(kDtypeFp4, TM, TN, WM, WN, 2, kScaleMx32, PD)
 static const KernelSpec kTiledGrouped[] = {
-    DGP_TILEDG(kDtypeBf16, 128, 128, 2, 2, 2, kScaleNone, 4), DGP_TILEDG(kDtypeFp8, 128, 128, 2, 2, 2, kScaleTensor, 4),
-    DGP_TILEDG(kDtypeFp8, 128, 128, 2, 2, 2, kScaleBlock, 4), DGP_TILEDG(kDtypeFp8, 128, 128, 2, 2, 2, kScaleMx, 4),
-    DGP_TILEDG(kDtypeFp4, 128, 128, 2, 2, 2, kScaleMx32, 4),  DGP_TILEDG(kDtypeFp8, 256, 256, 1, 8, 2, kScaleBlock, 4),
+    DGP_TILEDG_ALL(64, 64, 1, 2, 2),
+    DGP_TILEDG_ALL(64, 128, 1, 2, 2),
+    DGP_TILEDG_ALL(64, 256, 1, 4, 2),
+    DGP_TILEDG(kDtypeFp8, 128, 256, 1, 8, 2, kScaleBlock, 4),
+    DGP_TILEDG(kDtypeFp8, 128, 256, 1, 8, 2, kScaleMx, 4),
+    DGP_TILEDG(kDtypeFp4, 128, 256, 1, 8, 2, kScaleMx32, 4),
+    DGP_TILEDG(kDtypeFp8, 256, 256, 1, 8, 2, kScaleBlock, 4),
 };
 
 const KernelSpec *tiled_grouped_kernels(int *count)

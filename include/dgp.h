@@ -311,9 +311,9 @@ dgp_status dgp_gemm_preshuffle_splitk_noalloc(const void *A, const void *Bs, voi
  * experts need no copy; a row that A does not have counts as zeros.  A then
  * has a_rows rows and at most 0xFF000000 bytes; without rows A has a_rows >= M.
  *
- * The tile is chosen by the average number of rows of an expert, M / min(E,
- * M); cfg names another compiled one (16-row K-split tiles, and the tuned
- * large tiles of each mode).  K > 0; M = 0, N = 0 or E = 0 is a no-op; E <=
+ * The tile is chosen from M, N, K and E by estimated time; cfg names another
+ * compiled one (every mode: 16x16, 16x32 and 16x64 K-split tiles of 8 waves;
+ * 64x64, 64x128, 64x256, 128x256 and 256x256 with tile_k = 128).  K > 0; M = 0, N = 0 or E = 0 is a no-op; E <=
  * 65535.  One launch, no workspace.
  */
 dgp_status dgp_gemm_preshuffle_grouped(const void *A, int64_t a_rows, const void *Bs, void *C, int64_t M, int64_t N,

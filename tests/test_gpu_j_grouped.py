@@ -11,13 +11,7 @@ from operand_common import EPS, MODES, dequantize, pow2
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
-TILES = {
-    "none": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (128, 256), (256, 256)],
-    "tensor": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (128, 256), (256, 256)],
-    "block128": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (256, 256)],
-    "mx128": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (256, 256)],
-    "mx32": [(16, 8), (16, 16), (16, 32), (16, 64), (128, 128), (256, 256)],
-}
+TILES = {mode: [(16, 16), (16, 32), (16, 64), (64, 64), (64, 128), (64, 256), (128, 256), (256, 256)] for mode in MODES}
 
 
 def config(tile, remap=1, group_m=8):
@@ -110,7 +104,7 @@ def test_built_in_choice(mode, counts):
     run(mode, counts, 256, 512, 11, gather=len(counts) % 2 == 0, pad=len(counts))
 
 
-@pytest.mark.parametrize("tile", [None, (16, 32), (128, 128)])
+@pytest.mark.parametrize("tile", [None, (16, 32), (64, 128)])
 @pytest.mark.parametrize("e", [63, 64, 65, 130, 200])
 def test_many_experts(e, tile):
     g = torch.Generator().manual_seed(e)
@@ -127,7 +121,7 @@ def test_one_token(mode):
     run(mode, counts, 256, 7168, 17, gather=True)
 
 
-@pytest.mark.parametrize("tile", [(16, 32), (128, 128), (256, 256)])
+@pytest.mark.parametrize("tile", [(16, 32), (64, 64), (256, 256)])
 @pytest.mark.parametrize("remap,group_m", [(0, 1), (1, 1), (1, 3)])
 def test_tile_order(tile, remap, group_m):
     run("none", [130, 0, 1, 515], 640, 256, 19, tile, True, remap=remap, group_m=group_m)
@@ -138,14 +132,14 @@ def test_matches_the_single_product():
     for mode in MODES:
         A, sA, Bs, sB, _, _ = operands(mode, 300, 1, 256, 1024, 23)
         off = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
-        cfg = dict(tile_m=128, tile_n=128, tile_k=128, xcd_remap=1, group_m=8)
+        cfg = dict(tile_m=256, tile_n=256, tile_k=128, xcd_remap=1, group_m=8, schedule=1 if mode == "block128" else 4)
         C = dgp.gemm_preshuffle_grouped(A, Bs, off, sA, sB, MODES[mode], config=cfg)
         D = dgp.gemm_preshuffle(A, Bs[0], sA, sB, MODES[mode], config=cfg)
         assert torch.equal(C.view(torch.int16), D.view(torch.int16)), mode
 
 
 @pytest.mark.parametrize("mode", list(MODES))
-@pytest.mark.parametrize("tile", [(16, 64), (128, 128), (256, 256)])
+@pytest.mark.parametrize("tile", [(16, 64), (64, 256), (128, 256), (256, 256)])
 def test_rows_that_a_does_not_have_count_as_zeros(mode, tile):
     m, n, k = 40, 256, 512
     A, sA, Bs, sB, ad, bd = operands(mode, 9, 2, n, k, 29)
@@ -166,7 +160,7 @@ def test_rows_that_a_does_not_have_count_as_zeros(mode, tile):
 
 @pytest.mark.parametrize("offsets", [[0, 50, 20, 64], [-7, 10, 30, 64], [0, 10, 30, 1 << 30], [90, 95, 100, 110],
                                      [64, 0, 64, 0], [-2 ** 31, 2 ** 31 - 1, -5, 2 ** 31 - 1]])
-@pytest.mark.parametrize("tile", [(16, 16), (128, 128), (256, 256)])
+@pytest.mark.parametrize("tile", [(16, 16), (64, 64), (256, 256)])
 def test_offsets_that_break_the_rule_stay_inside_c(offsets, tile):
     """Nothing is written past C's rows, whatever the offsets (they are clamped on the device)."""
     m, n, k = 64, 128, 256

@@ -181,8 +181,8 @@ def test_grouped_refusals(L, kw, status):
 
 
 def test_grouped_configurations(L, dgp):
-    for cfg in (dict(tile_m=64, tile_n=128, tile_k=128), dict(tile_m=1, tile_n=16), dict(tile_m=16, tile_n=32, waves_m=2),
-                dict(tile_m=128, tile_n=128, tile_k=128, schedule=3), dict(tile_m=256, tile_n=256, tile_k=64)):
+    for cfg in (dict(tile_m=64, tile_n=32, tile_k=128), dict(tile_m=128, tile_n=128, tile_k=128), dict(tile_m=1, tile_n=16), dict(tile_m=16, tile_n=32, waves_m=2),
+                dict(tile_m=256, tile_n=256, tile_k=128, schedule=3), dict(tile_m=256, tile_n=256, tile_k=64)):
         c = dgp.Config(**cfg)
         assert grouped(L, cfg=ctypes.byref(c)) == CONFIG, cfg
     assert grouped(L, M=0, A=None, Bs=None, C=None, offsets=None) == OK
