@@ -1,6 +1,9 @@
 """Python binding of the gfx950 preshuffled-B GEMM library (libdgp.so).
 
-Argument marshalling only: every computation runs in the HIP kernels behind
+Argument marshalling only, through ctypes; the operators that write a
+product's operand and the product grouped by expert go through a small native
+module (csrc/torch_binding.cpp, _binding.so) that makes the same checks and
+calls the same C ABI: every computation runs in the HIP kernels behind
 the C ABI declared in include/dgp.h.  torch supplies device memory (outputs
 are allocated as torch tensors when not given) and the stream (the current
 torch stream unless one is passed).  There is no fallback: if the compiled
@@ -15,6 +18,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -24,6 +29,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdgp.so")
 # The LDS-poison debug build of the same sources (see lds_poison_build).
 LDS_POISON_LIB_PATH = os.path.join(_HERE, "libdgp_lds_poison.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 BF16 = 0
 FP8_E4M3 = 1
@@ -164,6 +170,34 @@ def _check(status: int) -> None:
         raise DgpError(status, lib().dgp_last_error().decode())
 
 
+_module = None     # the native module
+_bound = None      # the library its entry points are bound to
+
+
+def _native():
+    """The native half of the binding, bound to the active library."""
+    global _module, _bound
+    L = _lib or lib()
+    if _bound is not L:
+        if _module is None:
+            if not os.path.exists(BINDING_PATH):
+                raise ImportError(f"{BINDING_PATH} is missing: build it with __graft_entry__.build() "
+                                  "(or python dense_gemm_packer_amd/build.py)")
+            loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+            loader.exec_module(module)
+            _module = module
+        names = ("dgp_quantize_workspace_bytes", "dgp_quantize", "dgp_quantize_b", "dgp_rmsnorm_quantize",
+                 "dgp_swiglu_quantize", "dgp_gemm_preshuffle_grouped")
+        _module.bind(tuple(ctypes.cast(getattr(L, n), _vp).value for n in names), _check, _refuse_mode, _raw_stream)
+        _bound = L
+    return _module
+
+
+def _refuse_mode(scale_mode: int) -> None:
+    raise DgpError(5, f"scale mode {scale_mode} is not one this operator writes")
+
+
 def dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return BF16
@@ -268,13 +302,6 @@ def _alloc_stream(stream):
     stream, so the caching allocator never hands their memory to other work
     while the kernels that use it are still queued there."""
     return _CURRENT if stream is None else torch.cuda.stream(stream)
-
-
-def _new(stream, dtype, device, *shape) -> torch.Tensor:
-    if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _config(config):
@@ -401,35 +428,6 @@ def gemm_preshuffle_splitk(A: torch.Tensor, Bs: torch.Tensor, split_k: int,
     return out
 
 
-def check_grouped_operands(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Tensor, sA, sB, mode: int, rows,
-                           out) -> None:
-    """The shape and dtype checks of a grouped product that the C ABI cannot
-    make.  Raises ValueError before any launch."""
-    if A.dim() != 2 or Bs.dim() != 3:
-        raise ValueError(f"A must be 2-D and Bs 3-D (got {A.dim()}-D and {Bs.dim()}-D)")
-    if Bs.dtype != A.dtype:
-        raise ValueError(f"Bs is {Bs.dtype}, A is {A.dtype}: both operands take one element type")
-    E, N = Bs.shape[:2]
-    K = k_elements(A)
-    if Bs.shape[2] != A.shape[1]:
-        raise ValueError(f"Bs holds {Bs.shape[2] * K // max(A.shape[1], 1)} elements per row, A {K}")
-    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,):
-        raise ValueError(f"offsets must be {E + 1} int32 values (got {tuple(offsets.shape)} {offsets.dtype})")
-    if rows is not None and (rows.dtype != torch.int32 or rows.dim() != 1):
-        raise ValueError(f"rows must be a 1-D int32 tensor (got {tuple(rows.shape)} {rows.dtype})")
-    M = A.shape[0] if rows is None else rows.shape[0]
-    if out is not None and (out.dtype != torch.bfloat16 or tuple(out.shape) != (M, N)):
-        raise ValueError(f"out must be a ({M}, {N}) bfloat16 tensor (got {tuple(out.shape)} {out.dtype})")
-    want = scale_shapes(mode, A.shape[0], N, K)
-    if want is None:
-        return
-    dt, na, nb = want
-    for t, n, what in ((sA, na, "sA"), (sB, E * nb, "sB")):
-        if t is not None and (t.dtype != dt or t.numel() != n):
-            raise ValueError(f"{what} must hold {n} {dt} values for this scale mode and shape "
-                             f"(got {t.numel()} {t.dtype})")
-
-
 def gemm_preshuffle_grouped(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Tensor, sA: torch.Tensor | None = None,
                             sB: torch.Tensor | None = None, scale_mode: int | None = None,
                             rows: torch.Tensor | None = None, out: torch.Tensor | None = None, config=None,
@@ -440,20 +438,12 @@ def gemm_preshuffle_grouped(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Te
     weight: preshuffle_b(B.view(E * N, K)).view(E, N, K)), offsets int32 [E+1] on the device; rows (int32) names the row of A
     for each row of C.  Rows of C that no expert owns keep what `out` holds
     (unspecified without it)."""
-    for t, name in ((A, "A"), (Bs, "Bs"), (offsets, "offsets"), (sA, "sA"), (sB, "sB"), (rows, "rows"), (out, "out")):
-        if t is not None:
-            _dev(t, name)
-    _same_device(A, (Bs, "Bs"), (offsets, "offsets"), (sA, "sA"), (sB, "sB"), (rows, "rows"), (out, "out"))
-    mode = _scale_mode(A, sA, sB, scale_mode)
-    check_grouped_operands(A, Bs, offsets, sA, sB, mode, rows, out)
-    M = A.shape[0] if rows is None else rows.shape[0]
-    E, N = Bs.shape[:2]
-    if out is None:
-        out = _new(stream, torch.bfloat16, A.device, M, N)
-    _enqueue(A, stream, lib().dgp_gemm_preshuffle_grouped, A.data_ptr(), A.shape[0], Bs.data_ptr(), out.data_ptr(), M,
-             N, k_elements(A), E, offsets.data_ptr(), _ptr(rows), dtype_code(A), mode, _ptr(sA), _ptr(sB),
-             _config(config))
-    return out
+    if scale_mode is None:
+        scale_mode = _scale_mode(A, sA, sB, None)
+    if config is None:
+        return _native().grouped(A, Bs, offsets, sA, sB, scale_mode, rows, out, None, stream)
+    cfg = config if isinstance(config, Config) else Config(**config)
+    return _native().grouped(A, Bs, offsets, sA, sB, scale_mode, rows, out, ctypes.addressof(cfg), stream)
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20   # DGP_NOALLOC_SCRATCH_BYTES
@@ -483,123 +473,12 @@ def gemm_preshuffle_splitk_noalloc(A: torch.Tensor, Bs: torch.Tensor, split_k: i
 
 # ------------------------------------------- operators that write an operand
 
-_INPUT = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
-_CODES = {SCALE_NONE: torch.bfloat16, SCALE_TENSOR: torch.float8_e4m3fn, SCALE_BLOCK128: torch.float8_e4m3fn,
-          SCALE_MX128: torch.float8_e4m3fn, SCALE_MX32: torch.float4_e2m1fn_x2}
-_SCALES = {SCALE_TENSOR: torch.float32, SCALE_BLOCK128: torch.float32, SCALE_MX128: torch.uint8,
-           SCALE_MX32: torch.uint8}
-
-
-def input_code(t: torch.Tensor) -> int:
-    code = _INPUT.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported input type {t.dtype} (bfloat16, float16 or float32)")
-    return code
-
-
-def _rows(t: torch.Tensor, what: str, shape=None, like: torch.Tensor | None = None) -> int:
-    """Checks a strided [M][K] input on the device; returns its row stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a device tensor")
-    mine = t.shape
-    if len(mine) != 2:
-        raise ValueError(f"{what} must be 2-D (got {len(mine)}-D)")
-    if shape is not None:
-        if mine != shape:
-            raise ValueError(f"{what} must be {tuple(shape)} (got {tuple(mine)})")
-        if t.dtype != like.dtype or t.device != like.device:
-            raise ValueError(f"{what} is {t.dtype} on {t.device}, X {like.dtype} on {like.device}")
-    M, K = mine
-    ld, one = t.stride()
-    if one != 1 and K > 1:
-        raise ValueError(f"{what}: the elements of a row must be contiguous")
-    if M <= 1:
-        return K
-    if ld < K:
-        raise ValueError(f"{what}: rows overlap (stride {ld}, {K} elements)")
-    return ld
-
-
-def _dense(t: torch.Tensor, dtype, shape, X: torch.Tensor, what: str) -> None:
-    _dev(t, what)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be a {tuple(shape)} {dtype} tensor (got {tuple(t.shape)} {t.dtype})")
-    if t.device != X.device:
-        raise ValueError(f"{what} is on {t.device}, the input on {X.device}")
-
-
-def _mode(scale_mode: int, allow_none: bool) -> None:
-    if scale_mode not in _CODES or (scale_mode == SCALE_NONE and not allow_none):
-        raise DgpError(5, f"scale mode {scale_mode} is not one this operator writes")
-
-
-# Columns per scale, and of the codes' tensor per element, of each mode.
-_BLOCK = {SCALE_BLOCK128: 128, SCALE_MX128: 128, SCALE_MX32: 32}
-
-
-def _operand_out(X, M, K, mode, scale, out, scales, stream):
-    """Checks or allocates the codes and scales of an [M][K] operand; returns
-    (Q, S) (S: the given scale, or None without scales)."""
-    cols = K // 2 if mode == SCALE_MX32 else K
-    if out is not None:
-        _dense(out, _CODES[mode], (M, cols), X, "out")
-    if scale is not None:
-        if mode != SCALE_TENSOR:
-            raise DgpError(5, "a given scale goes with SCALE_TENSOR only")
-        if scales is not None:
-            raise ValueError("scale is given: there are no scales to write")
-        if scale.numel() != 1:
-            raise ValueError(f"scale must hold one value (got {scale.numel()})")
-        _dense(scale, torch.float32, scale.shape, X, "scale")
-        scales = scale
-    elif mode == SCALE_NONE:
-        if scales is not None:
-            raise ValueError("SCALE_NONE writes no scales")
-    else:
-        shape = (1,) if mode == SCALE_TENSOR else (M, K // _BLOCK[mode])
-        if scales is None:
-            scales = _new(stream, _SCALES[mode], X.device, *shape)
-        else:
-            _dense(scales, _SCALES[mode], shape, X, "scales")
-    if out is None:
-        out = _new(stream, _CODES[mode], X.device, M, cols)
-    return out, scales
-
-
-def _enqueue(X: torch.Tensor, stream, fn, *args) -> None:
-    """fn(*args, stream) with X's device current: on the given stream, or on
-    the current stream of that device."""
-    index = X.device.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return _enqueue(X, stream, fn, *args)
-    if stream is None:
-        handle = _raw_stream(index)
-    elif stream.device != X.device:
-        raise ValueError(f"stream is on {stream.device}, the input on {X.device}")
-    else:
-        handle = stream.cuda_stream
-    status = fn(*args, handle)
-    if status != 0:
-        _check(status)
-
-
 def quantize(X: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
              scales: torch.Tensor | None = None, stream=None):
     """(Q, S): the rows of X ([M][K] bfloat16, float16 or float32; the row
     stride is free) as the A operand of a quantised product (dgp_quantize).
     SCALE_TENSOR measures the scale, or takes the given one (then S is it)."""
-    ld = _rows(X, "X")
-    _mode(scale_mode, False)
-    M, K = X.shape
-    Q, S = _operand_out(X, M, K, scale_mode, scale, out, scales, stream)
-    ws = None
-    if scale_mode == SCALE_TENSOR and scale is None:
-        ws = _new(stream, torch.float32, X.device, lib().dgp_quantize_workspace_bytes(1, scale_mode) // 4)
-    _enqueue(X, stream, lib().dgp_quantize, X.data_ptr(), ld, input_code(X), Q.data_ptr(),
-             None if scale is not None else S.data_ptr(), _ptr(scale), M, K, scale_mode, _ptr(ws),
-             0 if ws is None else ws.numel() * 4)
-    return Q, S
+    return _native().quantize(X, scale_mode, scale, out, scales, stream)
 
 
 def quantize_b(B: torch.Tensor, scale_mode: int, out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
@@ -608,30 +487,7 @@ def quantize_b(B: torch.Tensor, scale_mode: int, out: torch.Tensor | None = None
     preshuffled in one pass (dgp_quantize_b): Bs as preshuffle_b of the codes,
     sB as the product reads it ([E][...] for a stack; SCALE_TENSOR: one value
     per weight, BLOCK128: 128 x 128 blocks)."""
-    _dev(B, "B")
-    if B.dim() not in (2, 3):
-        raise ValueError(f"B must be 2-D or 3-D (got {B.dim()}-D)")
-    _mode(scale_mode, False)
-    lead = tuple(B.shape[:-2])
-    E = B.shape[0] if lead else 1
-    N, K = B.shape[-2:]
-    code = input_code(B)
-    qshape = lead + ((N, K // 2) if scale_mode == SCALE_MX32 else (N, K))
-    sshape = {SCALE_TENSOR: lead or (1,), SCALE_BLOCK128: lead + (N // 128, K // 128),
-              SCALE_MX128: lead + (N, K // 128), SCALE_MX32: lead + (N, K // 32)}[scale_mode]
-    if out is not None:
-        _dense(out, _CODES[scale_mode], qshape, B, "out")
-    if scales is not None:
-        _dense(scales, _SCALES[scale_mode], sshape, B, "scales")
-    need = lib().dgp_quantize_workspace_bytes(E, scale_mode)
-    if out is None:
-        out = _new(stream, _CODES[scale_mode], B.device, *qshape)
-    if scales is None:
-        scales = _new(stream, _SCALES[scale_mode], B.device, *sshape)
-    ws = _new(stream, torch.float32, B.device, need // 4) if need else None
-    _enqueue(B, stream, lib().dgp_quantize_b, B.data_ptr(), code, out.data_ptr(), scales.data_ptr(), E, N, K,
-             scale_mode, _ptr(ws), need)
-    return out, scales
+    return _native().quantize_b(B, scale_mode, out, scales, stream)
 
 
 def rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, scale_mode: int, residual: torch.Tensor | None = None,
@@ -642,28 +498,7 @@ def rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, scale_mode: int, res
     or (Q, S, H) with a residual: H = h in X's type, the residual stream's new
     value (residual_out may be the residual itself).  SCALE_NONE: Q is
     bfloat16 and S None; SCALE_TENSOR takes a given scale."""
-    ldx = _rows(X, "X")
-    _mode(scale_mode, True)
-    M, K = X.shape
-    code = input_code(X)
-    ldr = 0
-    if residual is not None:
-        ldr = _rows(residual, "residual", X.shape, X)
-    _dev(weight, "weight")
-    if weight.dim() != 1 or weight.shape[0] != K or weight.dtype not in (X.dtype, torch.float32):
-        raise ValueError(f"weight must hold {K} values of {X.dtype} or float32 (got {tuple(weight.shape)} {weight.dtype})")
-    _same_device(X, (weight, "weight"))
-    if residual_out is not None:
-        if residual is None:
-            raise ValueError("residual_out needs a residual")
-        _dense(residual_out, X.dtype, X.shape, X, "residual_out")
-    Q, S = _operand_out(X, M, K, scale_mode, scale, out, scales, stream)
-    if residual is not None and residual_out is None:
-        residual_out = _new(stream, X.dtype, X.device, M, K)
-    _enqueue(X, stream, lib().dgp_rmsnorm_quantize, X.data_ptr(), ldx, _ptr(residual), ldr, code, weight.data_ptr(),
-             input_code(weight), eps, Q.data_ptr(), None if scale is not None else _ptr(S), _ptr(scale),
-             _ptr(residual_out), M, K, scale_mode)
-    return (Q, S) if residual is None else (Q, S, residual_out)
+    return _native().rmsnorm_quantize(X, weight, scale_mode, residual, eps, scale, out, scales, residual_out, stream)
 
 
 def swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None,
@@ -672,14 +507,7 @@ def swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, scale_mode: int, scale
     (dgp_swiglu_quantize).  gate and up are [M][K] with free row strides: the
     two halves of one product's columns are C[:, :K] and C[:, K:].  SCALE_NONE:
     Q is bfloat16 and S None; SCALE_TENSOR takes a given scale."""
-    ldg = _rows(gate, "gate")
-    ldu = _rows(up, "up", gate.shape, gate)
-    _mode(scale_mode, True)
-    M, K = gate.shape
-    Q, S = _operand_out(gate, M, K, scale_mode, scale, out, scales, stream)
-    _enqueue(gate, stream, lib().dgp_swiglu_quantize, gate.data_ptr(), ldg, up.data_ptr(), ldu, input_code(gate),
-             Q.data_ptr(), None if scale is not None else _ptr(S), _ptr(scale), M, K, scale_mode)
-    return Q, S
+    return _native().swiglu_quantize(gate, up, scale_mode, scale, out, scales, stream)
 
 
 def check_arch(name: str) -> bool:

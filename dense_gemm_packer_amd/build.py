@@ -6,13 +6,15 @@ disabled for all device code.  The same sources compiled with
 DGP_LDS_POISON=1 give the LDS-poison debug build, libdgp_lds_poison.so
 (every kernel's LDS filled with 0xFF before use, every global -> LDS copy's
 destination poisoned until the copy lands), which the tests run beside the
-release build.
+release build.  csrc/torch_binding.cpp, host code against torch's headers,
+gives the native half of the Python binding, _binding.so.
 """
 import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -24,6 +26,9 @@ SOURCES = ["dgp_api.cpp", "packer.hip", "gemm_tiled.hip", "gemm_lds.hip", "gemm_
 HEADERS = ["common.h", "launch.h", "gemm_common.h"]
 ARCH = "gfx950"
 
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = "torch_binding.cpp"
+CXX = os.environ.get("CXX", shutil.which("g++") or "g++")
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -62,15 +67,32 @@ def _link(objs, lib):
     os.replace(tmp, lib)
 
 
+def _binding(tmp):
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    libs = os.path.join(base, "lib")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in inc),
+           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, f"-L{libs}", "-lc10", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for {BINDING_SOURCE}:\n{r.stdout}{r.stderr}")
+    return r.stdout + r.stderr
+
+
 def build(force: bool = True, jobs: int = 0) -> str:
-    """Compile every source twice and link libdgp.so and libdgp_lds_poison.so;
-    returns the release library's path."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    """Compile every source twice and link libdgp.so and libdgp_lds_poison.so,
+    and the Python binding's native module; returns the release library's path."""
+    srcs = [os.path.join(CSRC, s) for s in (*SOURCES, BINDING_SOURCE)]
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [
         os.path.join(HERE, "..", "include", h) for h in ("dgp.h", "dgp_diag.h")]
-    if not force and os.path.exists(LIB) and os.path.exists(POISON_LIB):
+    made = (LIB, POISON_LIB, BINDING)
+    if not force and all(os.path.exists(p) for p in made):
         newest = max(os.path.getmtime(p) for p in srcs + hdrs)
-        if min(os.path.getmtime(LIB), os.path.getmtime(POISON_LIB)) >= newest:
+        if min(os.path.getmtime(p) for p in made) >= newest:
             return LIB
     os.makedirs(BUILD, exist_ok=True)
     # the slowest sources first, so the pool's tail is short
@@ -78,12 +100,17 @@ def build(force: bool = True, jobs: int = 0) -> str:
     todo = [(f, False) for f in order] + [(f, True) for f in order]
     jobs = jobs or min(len(todo), os.cpu_count() or 4, 16)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
+        binding = ex.submit(_binding, BINDING + ".tmp")
         results = dict(zip(todo, ex.map(_compile, todo)))
+        notes = binding.result()
+    if notes.strip():
+        print(notes, file=sys.stderr)
     for _, msgs in results.values():
         if msgs.strip():
             print(msgs, file=sys.stderr)
     _link([results[(f, False)][0] for f in SOURCES], LIB)
     _link([results[(f, True)][0] for f in SOURCES], POISON_LIB)
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

@@ -611,41 +611,44 @@ int64_t most_row_tiles(int64_t M, int64_t E, int64_t tm)
 }
 
 // Built-in choice for M rows over E experts, of which the host knows the
-// average only: the tile with the least estimated time
+// average only: the tile with the least estimated time, the fourth root of
+// c^4 + m^4 (a maximum that is smooth where both count) of
 //
-//   (a + b k) (1 + s (x - 1)),  k = 128-byte k-steps, x = tiles on the busiest CU,
+//   c = (a + b k) (1 + s (x - 1)),  k = 128-byte k-steps, x = tiles on the busiest CU,
+//   m = a + weight bytes / w,
 //
-// a, b, s fitted per element type and tile to graph timings of 90 random
-// shapes (1 to 64 experts with 1 to 1000 rows each, unevenly filled, N 128 to
-// 7168, K 256 to 8192): a is the launch, the search for the tile and the
-// epilogue (us), b the k-step of a tile that has its CU to itself, s what a
-// further tile on the same CU adds (below 1 where two overlap, above it where
-// they contend).  The fit is within 8-20 % of a timing, and the tile it picks
-// is on average 1-2 % slower than the fastest one of its shape (at worst 35 %,
-// where several are within a few us of the launch).  Any one tile left out
-// costs 1-3 % on average and up to 80 % at worst, so all of them stay; a
-// 128 x 128 tile and a half-strip one were never missed and are not compiled.
+// with a, b, s, w fitted per element type and tile to graph timings of 160
+// random shapes (1 to 128 experts with 1 to 1000 rows each, unevenly filled, N
+// 128 to 7168, K 256 to 8192; weights of 0.1 MB to 4 GB): a (us) is the launch,
+// the search for the tile and the epilogue, b (us) the k-step of a tile that
+// has its CU to itself, s what a further tile on the same CU adds (below 1
+// where two overlap, above it where they contend), w (MB/us) the rate at which
+// the tile streams weights.  The fit is within 8-20 % of a timing, and the tile
+// that it picks is on average 2-3 % slower than the fastest one of its shape
+// (at worst 35 %, on two of 800).  Any one tile left out costs 0-4 % more on
+// average and up to 66 % at worst, so all of them stay; a 128 x 128 tile and a
+// half-strip one were not missed and are not compiled.
 struct GroupedTile {
     int tm, tn;
-    double a, b, s;
+    double a, b, s, w;
 };
 constexpr int kGroupedTiles = 8;
 constexpr GroupedTile kGroupedCost[5][kGroupedTiles] = {
     // bf16
-    {{16, 16, 2.00, 0.114, 0.39}, {16, 32, 2.05, 0.140, 0.46}, {16, 64, 1.97, 0.213, 0.68}, {64, 64, 2.51, 0.275, 0.88},
-     {64, 128, 3.29, 0.341, 0.97}, {64, 256, 3.64, 0.460, 1.45}, {128, 256, 5.28, 0.558, 1.13}, {256, 256, 7.55, 0.994, 1.32}},
+    {{16, 16, 1.30, 0.128, 0.54, 8.00}, {16, 32, 1.17, 0.158, 0.73, 8.00}, {16, 64, 1.37, 0.230, 0.89, 7.45}, {64, 64, 2.10, 0.290, 0.99, 7.98},
+     {64, 128, 2.74, 0.355, 1.14, 6.14}, {64, 256, 3.02, 0.479, 1.58, 5.98}, {128, 256, 4.55, 0.581, 1.43, 5.65}, {256, 256, 7.02, 1.001, 1.32, 6.86}},
     // fp8, per-tensor scales
-    {{16, 16, 2.58, 0.101, 0.39}, {16, 32, 2.61, 0.124, 0.42}, {16, 64, 2.71, 0.188, 0.79}, {64, 64, 2.76, 0.288, 0.74},
-     {64, 128, 3.47, 0.356, 0.87}, {64, 256, 3.97, 0.466, 1.22}, {128, 256, 5.30, 0.631, 0.93}, {256, 256, 8.22, 0.945, 1.26}},
+    {{16, 16, 2.11, 0.119, 0.47, 8.00}, {16, 32, 2.04, 0.147, 0.54, 7.39}, {16, 64, 2.35, 0.196, 0.88, 6.82}, {64, 64, 2.33, 0.309, 0.87, 7.43},
+     {64, 128, 2.88, 0.375, 1.01, 6.07}, {64, 256, 3.30, 0.491, 1.42, 6.02}, {128, 256, 4.49, 0.672, 1.16, 5.42}, {256, 256, 7.37, 0.961, 1.34, 6.60}},
     // fp8, blockscale
-    {{16, 16, 2.86, 0.107, 0.61}, {16, 32, 2.64, 0.140, 0.45}, {16, 64, 2.74, 0.204, 0.80}, {64, 64, 2.99, 0.317, 0.69},
-     {64, 128, 3.67, 0.458, 0.74}, {64, 256, 4.25, 0.591, 1.10}, {128, 256, 4.85, 0.873, 1.25}, {256, 256, 5.52, 1.764, 1.27}},
+    {{16, 16, 2.53, 0.111, 0.69, 8.00}, {16, 32, 2.04, 0.171, 0.57, 7.50}, {16, 64, 2.38, 0.212, 0.89, 6.71}, {64, 64, 2.45, 0.352, 0.84, 8.00},
+     {64, 128, 3.05, 0.484, 0.88, 6.34}, {64, 256, 3.63, 0.611, 1.25, 6.09}, {128, 256, 4.32, 0.888, 1.35, 7.10}, {256, 256, 5.28, 1.780, 1.10, 8.00}},
     // mxfp8
-    {{16, 16, 2.81, 0.115, 0.61}, {16, 32, 2.67, 0.151, 0.45}, {16, 64, 2.70, 0.225, 0.82}, {64, 64, 2.88, 0.302, 0.72},
-     {64, 128, 3.53, 0.409, 0.85}, {64, 256, 4.24, 0.581, 1.22}, {128, 256, 4.54, 0.787, 1.40}, {256, 256, 8.04, 1.012, 1.24}},
+    {{16, 16, 2.49, 0.119, 0.69, 8.00}, {16, 32, 2.16, 0.172, 0.55, 7.65}, {16, 64, 2.40, 0.227, 0.89, 6.61}, {64, 64, 2.37, 0.332, 0.86, 7.66},
+     {64, 128, 2.91, 0.439, 1.00, 6.11}, {64, 256, 3.50, 0.610, 1.40, 5.95}, {128, 256, 3.95, 0.808, 1.52, 6.40}, {256, 256, 7.19, 1.037, 1.31, 6.52}},
     // mxfp4
-    {{16, 16, 3.04, 0.121, 0.32}, {16, 32, 2.92, 0.168, 0.41}, {16, 64, 2.99, 0.256, 0.75}, {64, 64, 3.03, 0.388, 0.62},
-     {64, 128, 3.61, 0.529, 0.70}, {64, 256, 4.04, 0.693, 1.14}, {128, 256, 4.46, 1.020, 1.36}, {256, 256, 8.43, 1.382, 1.21}},
+    {{16, 16, 2.60, 0.147, 0.37, 8.00}, {16, 32, 2.45, 0.193, 0.50, 7.06}, {16, 64, 2.61, 0.271, 0.84, 5.99}, {64, 64, 2.51, 0.447, 0.75, 8.00},
+     {64, 128, 2.97, 0.583, 0.89, 5.98}, {64, 256, 3.38, 0.728, 1.36, 5.77}, {128, 256, 3.94, 1.048, 1.43, 7.55}, {256, 256, 7.48, 1.434, 1.26, 5.54}},
 };
 
 // Row tiles to expect: one expert's are known; several leave half a tile each
@@ -662,11 +665,13 @@ const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t 
 {
     const GroupedTile *best = nullptr;
     double least = 0;
+    const double weights = (double)(E < M ? E : M) * (double)N * (double)Kb * 1e-6;
     for (const GroupedTile &t : kGroupedCost[scale]) {
         const double x = std::ceil(expected_row_tiles(M, E, t.tm) * (double)((N + t.tn - 1) / t.tn) / kNumCu);
-        const double us = (t.a + t.b * (double)(Kb / 128)) * (1 + t.s * (x - 1));
-        if (!best || us < least)
-            best = &t, least = us;
+        const double c = (t.a + t.b * (double)(Kb / 128)) * (1 + t.s * (x - 1)), m = t.a + weights / t.w;
+        const double us4 = c * c * c * c + m * m * m * m;
+        if (!best || us4 < least)
+            best = &t, least = us4;
     }
     return find_spec(Query{best->tm == 16 ? kStream : kTiled, dtype, scale, kOutBf16, best->tm, best->tn}, grouped_table);
 }

@@ -107,58 +107,90 @@ def test_swiglu_refusals(L, kw, status):
     assert swiglu(L, **kw) == status
 
 
-def test_binding_refuses_host_tensors(dgp):
-    x = torch.zeros(4, 256, dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        dgp.quantize(x, dgp.SCALE_BLOCK128)
-    with pytest.raises(ValueError):
-        dgp.quantize_b(x, dgp.SCALE_BLOCK128)
-    with pytest.raises(ValueError):
-        dgp.rmsnorm_quantize(x, x[0], dgp.SCALE_BLOCK128)
-    with pytest.raises(ValueError):
-        dgp.swiglu_quantize(x, x, dgp.SCALE_BLOCK128)
+# The binding's own checks, in the order they are made; host tensors that pass
+# them all are refused last.
+
+def bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
 
 
-class Fake:
-    """Stands for a device tensor in the binding's shape checks."""
+@pytest.mark.parametrize("kw,error,match", [
+    (dict(), ValueError, "device tensor"), (dict(X=bf(256)), ValueError, "2-D"), (dict(X=bf(256, 4).t()), ValueError, "contiguous"),
+    (dict(X=bf(1, 256).expand(4, 256)), ValueError, "overlap"), (dict(X=bf(4, 256).double()), TypeError, "input type"),
+    (dict(X=None), TypeError, "must be a tensor"), (dict(X=[1, 2]), TypeError, "must be a tensor"),
+    (dict(scale_mode="x"), TypeError, None), (dict(out=bf(4, 256)), ValueError, "out must be"),
+    (dict(out=torch.zeros(4, 128, dtype=torch.float8_e4m3fn)), ValueError, "out must be"),
+    (dict(out=torch.zeros(256, 4, dtype=torch.float8_e4m3fn).t()), ValueError, "contiguous"),
+    (dict(scales=torch.zeros(4, 2)), ValueError, "scales must be"),
+    (dict(scales=torch.zeros(4, dtype=torch.uint8)), ValueError, "scales must be"),
+    (dict(scale=torch.ones(1)), ValueError, "SCALE_TENSOR only"),
+    (dict(scale_mode=1, scale=torch.ones(2)), ValueError, "one value"),
+    (dict(scale_mode=1, scale=torch.ones(1).double()), ValueError, "scale must be"),
+    (dict(scale_mode=1, scale=torch.ones(1), scales=torch.ones(1)), ValueError, "no scales to write"),
+    (dict(scale_mode=4, out=torch.zeros(4, 128, dtype=torch.uint8)), ValueError, "out must be"),
+    (dict(stream="s"), ValueError, "device tensor"),
+])
+def test_quantize_binding_checks(dgp, kw, error, match):
+    with pytest.raises(error, match=match):
+        dgp.quantize(**{**dict(X=bf(4, 256), scale_mode=MX), **kw})
 
-    def __init__(self, t, device="cuda:0"):
-        self.t, self.is_cuda, self.device = t, True, torch.device(device)
 
-    def __getattr__(self, name):
-        return getattr(self.t, name)
+@pytest.mark.parametrize("mode", [NONE, 5, -1, 17])
+def test_modes_an_operator_does_not_write(dgp, mode):
+    for f in (lambda: dgp.quantize(bf(4, 256), mode), lambda: dgp.quantize_b(bf(128, 256), mode)):
+        with pytest.raises(dgp.DgpError) as e:
+            f()
+        assert e.value.status == SCALE
+    if mode != NONE:
+        for f in (lambda: dgp.rmsnorm_quantize(bf(4, 256), bf(256), mode), lambda: dgp.swiglu_quantize(bf(4, 256), bf(4, 256), mode)):
+            with pytest.raises(dgp.DgpError):
+                f()
 
 
-def test_binding_shape_checks(dgp):
-    bf = torch.zeros(4, 256, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="2-D"):
-        dgp._rows(Fake(bf[0]), "X")
-    with pytest.raises(ValueError, match="contiguous"):
-        dgp._rows(Fake(bf.t()), "X")
-    with pytest.raises(ValueError, match="overlap"):
-        dgp._rows(Fake(bf[:1].expand(4, 256)), "X")
-    with pytest.raises(ValueError, match="must be"):
-        dgp._rows(Fake(bf), "residual", torch.Size((3, 256)), Fake(bf))
-    with pytest.raises(ValueError, match="float16"):
-        dgp._rows(Fake(bf.half()), "residual", bf.shape, Fake(bf))
-    assert dgp._rows(Fake(bf[:, :128]), "X") == 256 and dgp._rows(Fake(bf[:1, :128]), "X") == 128
-    X = Fake(bf)
-    for kw in (dict(scale=Fake(torch.ones(2)), mode=dgp.SCALE_TENSOR), dict(scale=Fake(torch.ones(1).double()), mode=dgp.SCALE_TENSOR),
-               dict(out=Fake(bf), mode=dgp.SCALE_MX128), dict(scales=Fake(torch.ones(4, 2)), mode=dgp.SCALE_MX128),
-               dict(scales=Fake(torch.ones(4, 2)), mode=dgp.SCALE_NONE),
-               dict(scales=Fake(torch.ones(4, 2), "cuda:1"), mode=dgp.SCALE_BLOCK128)):
-        mode = kw.pop("mode")
-        with pytest.raises(ValueError):
-            dgp._operand_out(X, 4, 256, mode, kw.get("scale"), kw.get("out"), kw.get("scales"), None)
-    with pytest.raises(dgp.DgpError) as e:
-        dgp._operand_out(X, 4, 256, dgp.SCALE_MX128, Fake(torch.ones(1)), None, None, None)
-    assert e.value.status == SCALE
-    with pytest.raises(dgp.DgpError):
-        dgp._mode(dgp.SCALE_NONE, False)
-    with pytest.raises(dgp.DgpError):
-        dgp._mode(17, True)
-    with pytest.raises(TypeError):
-        dgp.input_code(bf.double())
+@pytest.mark.parametrize("kw,error,match", [
+    (dict(), ValueError, "device tensor"), (dict(B=bf(256)), ValueError, "2-D or 3-D"), (dict(B=bf(2, 2, 128, 256)), ValueError, "2-D or 3-D"),
+    (dict(B=bf(256, 128).t()), ValueError, "contiguous"), (dict(B=bf(128, 256).long()), TypeError, "input type"),
+    (dict(out=torch.zeros(128, 256, dtype=torch.uint8)), ValueError, "out must be"),
+    (dict(scales=torch.zeros(128, 1, dtype=torch.uint8)), ValueError, "scales must be"),
+    (dict(B=bf(3, 128, 256), scales=torch.zeros(128, 2, dtype=torch.uint8)), ValueError, "scales must be"),
+])
+def test_quantize_b_binding_checks(dgp, kw, error, match):
+    with pytest.raises(error, match=match):
+        dgp.quantize_b(**{**dict(B=bf(128, 256), scale_mode=MX), **kw})
+
+
+@pytest.mark.parametrize("kw,error,match", [
+    (dict(), ValueError, "device tensor"), (dict(weight=bf(128)), ValueError, "weight must hold"),
+    (dict(weight=bf(1, 256)), ValueError, "weight must hold"), (dict(weight=bf(256).half()), ValueError, "weight must hold"),
+    (dict(weight=bf(512)[::2]), ValueError, "contiguous"), (dict(residual=bf(3, 256)), ValueError, "residual must be"),
+    (dict(residual=bf(4, 256).half()), ValueError, "residual is"), (dict(residual_out=bf(4, 256)), ValueError, "needs a residual"),
+    (dict(residual=bf(4, 256), residual_out=bf(4, 256).float()), ValueError, "residual_out must be"),
+    (dict(eps="x"), TypeError, None), (dict(scale_mode=NONE, scales=torch.ones(4, 2)), ValueError, "writes no scales"),
+    (dict(weight=torch.zeros(256)), ValueError, "device tensor"),
+])
+def test_rmsnorm_binding_checks(dgp, kw, error, match):
+    with pytest.raises(error, match=match):
+        dgp.rmsnorm_quantize(**{**dict(X=bf(4, 256), weight=bf(256), scale_mode=BLOCK), **kw})
+
+
+@pytest.mark.parametrize("kw,error,match", [
+    (dict(), ValueError, "device tensor"), (dict(up=bf(4, 128)), ValueError, "up must be"),
+    (dict(up=bf(4, 256).float()), ValueError, "up is"), (dict(gate=bf(4, 512)[:, :256]), ValueError, "device tensor"),
+    (dict(up=bf(256, 4).t()), ValueError, "contiguous"),
+])
+def test_swiglu_binding_checks(dgp, kw, error, match):
+    with pytest.raises(error, match=match):
+        dgp.swiglu_quantize(**{**dict(gate=bf(4, 256), up=bf(4, 256), scale_mode=BLOCK), **kw})
+
+
+def test_binding_follows_the_active_library(dgp):
+    """Inside lds_poison_build the native module calls that library."""
+    dgp._native()
+    with dgp.lds_poison_build() as poison:
+        dgp._native()
+        assert dgp._bound is poison
+    dgp._native()
+    assert dgp._bound is dgp.lib()
 
 
 def grouped(L, A=P, a_rows=64, Bs=P, C=P, M=64, N=128, K=256, E=4, offsets=P, rows=None, dtype=FP8, mode=MX, sA=P, sB=P,
@@ -189,23 +221,29 @@ def test_grouped_configurations(L, dgp):
     assert grouped(L, E=0, A=None, Bs=None, C=None, offsets=None) == OK
 
 
-def test_grouped_binding_checks(dgp):
-    A = torch.zeros(6, 256, dtype=torch.bfloat16)
-    Bs = torch.zeros(3, 32, 256, dtype=torch.bfloat16)
-    off = torch.zeros(4, dtype=torch.int32)
-    rows = torch.zeros(9, dtype=torch.int32)
-    ok = lambda **kw: dgp.check_grouped_operands(**{**dict(A=A, Bs=Bs, offsets=off, sA=None, sB=None,  # noqa: E731
-                                                          mode=dgp.SCALE_NONE, rows=None, out=None), **kw})
-    ok()
-    ok(rows=rows, out=torch.zeros(9, 32, dtype=torch.bfloat16))
-    for kw in (dict(A=A[0]), dict(Bs=Bs[0]), dict(Bs=Bs.half()), dict(Bs=Bs[:, :, :128]), dict(offsets=off[:3]),
-               dict(offsets=off.long()), dict(rows=rows.long()), dict(rows=rows.view(3, 3)),
-               dict(out=torch.zeros(6, 32)), dict(rows=rows, out=torch.zeros(6, 32, dtype=torch.bfloat16))):
-        with pytest.raises(ValueError):
-            ok(**kw)
-    f8 = dict(A=A.to(torch.float8_e4m3fn), Bs=Bs.to(torch.float8_e4m3fn), mode=dgp.SCALE_TENSOR)
-    ok(**f8, sA=torch.ones(1), sB=torch.ones(3))
-    with pytest.raises(ValueError):
-        ok(**f8, sA=torch.ones(1), sB=torch.ones(1))
-    with pytest.raises(ValueError):
-        ok(**{**f8, "mode": dgp.SCALE_MX128}, sA=torch.ones(12), sB=torch.ones(192))
+F8 = torch.float8_e4m3fn
+f8 = dict(A=torch.zeros(6, 256, dtype=F8), Bs=torch.zeros(3, 32, 256, dtype=F8))
+
+
+@pytest.mark.parametrize("kw,error,match", [
+    (dict(), ValueError, "device tensor"),
+    (dict(rows=torch.zeros(9, dtype=torch.int32), out=bf(9, 32)), ValueError, "device tensor"),
+    (dict(A=bf(256)), ValueError, "2-D"), (dict(Bs=bf(32, 256)), ValueError, "3-D"), (dict(A=bf(6, 256).float()), TypeError, "element type"),
+    (dict(Bs=bf(3, 32, 256).half()), ValueError, "one element type"), (dict(Bs=bf(3, 32, 128)), ValueError, "elements per row"),
+    (dict(A=bf(256, 6).t()), ValueError, "contiguous"), (dict(offsets=torch.zeros(3, dtype=torch.int32)), ValueError, "offsets must be"),
+    (dict(offsets=torch.zeros(4, dtype=torch.int64)), ValueError, "offsets must be"),
+    (dict(offsets=torch.zeros(8, dtype=torch.int32)[::2]), ValueError, "contiguous"),
+    (dict(rows=torch.zeros(9)), ValueError, "rows must be"), (dict(rows=torch.zeros(3, 3, dtype=torch.int32)), ValueError, "rows must be"),
+    (dict(out=torch.zeros(6, 32)), ValueError, "out must be"),
+    (dict(rows=torch.zeros(9, dtype=torch.int32), out=bf(6, 32)), ValueError, "out must be"),
+    (dict(**f8, scale_mode=TENSOR, sA=torch.ones(1), sB=torch.ones(3)), ValueError, "device tensor"),
+    (dict(**f8, scale_mode=TENSOR, sA=torch.ones(1), sB=torch.ones(1)), ValueError, "sB must hold 3"),
+    (dict(**f8, scale_mode=TENSOR, sA=torch.ones(6), sB=torch.ones(3)), ValueError, "sA must hold 1"),
+    (dict(**f8, scale_mode=MX, sA=torch.ones(12), sB=torch.ones(192)), ValueError, "sA must hold 12"),
+    (dict(**f8, scale_mode=MX, sA=torch.ones(12, dtype=torch.uint8), sB=torch.ones(64, dtype=torch.uint8)), ValueError, "sB must hold 192"),
+    (dict(**f8, sA=torch.ones(1), sB=torch.ones(3)), ValueError, "ambiguous"),
+])
+def test_grouped_binding_checks(dgp, kw, error, match):
+    base = dict(A=bf(6, 256), Bs=bf(3, 32, 256), offsets=torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(error, match=match):
+        dgp.gemm_preshuffle_grouped(**{**base, **kw})
