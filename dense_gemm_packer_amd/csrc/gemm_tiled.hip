@@ -27,7 +27,15 @@ namespace dgp {
 
 
 // GR: 1 = the product grouped by expert (gemm_common.h).
-template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD, int GR>
+// XG: 0 = E8M0 scales staged per k-tile (below); else XG k-tiles at once, in 16-byte pieces.  Per
+// k-tile a row has only 1 (mxfp8) or 8 (mxfp4) bytes of them, and a copy of
+// one lane per row or dword touches one cache line per lane: on a 64 x 256
+// tile the scale copies then take more address cycles than A and B together
+// (12 copies of up to 64 lines against 40 of 16).  Staged for 16 (mxfp8) or 4
+// (mxfp4) k-tiles, a row's 16 or 32 bytes come in one or two pieces, into one
+// of two LDS areas behind the A ring, while the k-tiles before them run.  Rows
+// of the scale arrays have to be whole dwords (mxfp8: K % 512 == 0).
+template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD, int GR, int XG>
 __global__ void __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
                                amdgpu_waves_per_eu((WM * WN + 3) / 4, (WM * WN + 3) / 4)))
 gemm_tiled_kernel(const GemmArgs args)
@@ -48,7 +56,11 @@ gemm_tiled_kernel(const GemmArgs args)
     constexpr bool kX4 = SCALE == kScaleMx32;
     constexpr bool kXS = SCALE == kScaleBlock || SCALE == kScaleMx || kX4;
     constexpr int kES = SCALE == kScaleMx ? 1 : 4;             // bytes per scale copy
-    constexpr int kXDwords = kX4 ? 2 * (TM + TN) : kXS ? TM + TN : 0;
+    constexpr bool kWide = XG > 0;
+    static_assert(!kWide || ((kX4 || SCALE == kScaleMx) && XG >= DEPTH && (XG & (XG - 1)) == 0 && (kX4 ? 8 : 1) * XG % 16 == 0),
+                  "wide staging: E8M0 scales, whole 16-byte pieces, issued at least DEPTH k-tiles ahead");
+    constexpr int kXRow = (kX4 ? 8 : 1) * XG;                  // wide: scale bytes per row and stage
+    constexpr int kXDwords = kWide ? (TM + TN) * kXRow / 16 : kX4 ? 2 * (TM + TN) : kXS ? TM + TN : 0;
     // Scale copies per wave per k-tile; where they cover more than the area
     // (the 64-row tiles), the rest lands, as zeros, in padding behind it.
     constexpr int kXDma = (kXDwords + 64 * S::kWaves - 1) / (64 * S::kWaves);
@@ -57,12 +69,13 @@ gemm_tiled_kernel(const GemmArgs args)
                            (kX4 ? DT == kDtypeFp4 : DT == kDtypeFp8 && S::kMT % 4 == 0) &&
                            (S::kNT == 2 || S::kNT == 4)),
                   "staged scales: one 128-byte k-tile per scale stage, whole copies per wave");
-    constexpr int kStageBytes = S::kBufBytes + kXArea * 4;
-    static_assert(DEPTH >= 1 && (DEPTH + 1) * kStageBytes <= 160 * 1024, "A ring must fit in LDS");
+    constexpr int kStageBytes = S::kBufBytes + (kWide ? 0 : kXArea * 4);
+    constexpr int kWideBytes = kWide ? kXArea * 16 : 0;        // one of the two wide areas
+    static_assert(DEPTH >= 1 && (DEPTH + 1) * kStageBytes + 2 * kWideBytes <= 160 * 1024, "A ring must fit in LDS");
     // Prefetch distance DEPTH k-tiles: a ring of DEPTH+1 A buffers in LDS and
     // DEPTH sets of B registers.
     constexpr int kRing = DEPTH + 1;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * kStageBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * kStageBytes + 2 * kWideBytes];
     if constexpr (kLdsPoison) {   // debug build: all of LDS poisoned before the first copy
         lds_poison_fill(lds, (int)sizeof(lds));
         __syncthreads();
@@ -110,7 +123,22 @@ gemm_tiled_kernel(const GemmArgs args)
     // Rows >= M and (blockscale) column blocks past N load as zero.
     [[maybe_unused]] __amdgpu_buffer_rsrc_t x_rsrc[kXDma > 0 ? kXDma : 1];
     [[maybe_unused]] uint32_t x_voff[kXDma > 0 ? kXDma : 1];
-    if constexpr (kX4) {
+    if constexpr (kWide) {
+        // piece e of a stage: row e / (kXRow / 16) of the tile's rows, then its columns
+        const uint32_t rowb = kX4 ? Kb / 16u : Kb / 128u;   // E8M0 bytes per row
+        const auto rXA = row_rsrc<GR>(p, p.sA, m0, rowb);
+        const auto rXB = make_rsrc((const uint8_t *)p.sB + (int64_t)n0 * rowb, clamp_bytes((int64_t)(p.N - n0) * rowb));
+        constexpr int kPieces = kXRow / 16;
+        static_assert(TM % (64 / kPieces) == 0 && TN % (64 / kPieces) == 0, "a wave's pieces are rows or columns");
+#pragma unroll
+        for (int j = 0; j < kXDma; ++j) {
+            const int e0 = (j * S::kWaves + wave) * 64, r0 = e0 / kPieces;
+            const int r = (e0 + lane) / kPieces;
+            const uint32_t at = 16u * (uint32_t)(lane % kPieces);
+            x_rsrc[j] = r0 < TM ? rXA : r0 < TM + TN ? rXB : make_rsrc(nullptr, 0);
+            x_voff[j] = (r0 < TM ? row_offset<GR>(p, m0, r, rowb) : (uint32_t)(r - TM) * rowb) + at;
+        }
+    } else if constexpr (kX4) {
         const uint32_t rowb = Kb / 16u;    // E8M0 bytes per row: one per 32 elements = 16 bytes
         const auto rXA = row_rsrc<GR>(p, p.sA, m0, rowb);
         const auto rXB = make_rsrc((const uint8_t *)p.sB + (int64_t)n0 * rowb,
@@ -174,7 +202,7 @@ gemm_tiled_kernel(const GemmArgs args)
 #pragma unroll
         for (int j = 0; j < S::kDmaPerWave; ++j)
             lds_dma16(rA, lds + buf_off + (j * S::kWaves + wave) * 1024, dma_voff[j], koff);
-        if constexpr (kXS) {
+        if constexpr (kXS && !kWide) {
 #pragma unroll
             for (int j = 0; j < kXDma; ++j) {
                 uint8_t *d = lds + buf_off + S::kBufBytes + (j * S::kWaves + wave) * 256;
@@ -190,6 +218,22 @@ gemm_tiled_kernel(const GemmArgs args)
     auto kofs = [&](int t) {   // first K byte of tile t, clamped to the last tile
         return kbase + (uint32_t)(t < ntiles ? t : ntiles - 1) * KT;
     };
+    // Wide scale stage c (k-tiles c XG ..) into area c % 2; bytes past a row's
+    // end are the next row's or zero, and no k-tile reads them.
+    [[maybe_unused]] auto copy_scales = [&](int c) {
+        if constexpr (kWide) {
+            const uint32_t koff = kbase + (uint32_t)c * (uint32_t)(XG * KT);
+            uint8_t *d = lds + kRing * kStageBytes + (c & 1) * kWideBytes;
+#pragma unroll
+            for (int j = 0; j < kXDma; ++j)
+                lds_dma16(x_rsrc[j], d + (j * S::kWaves + wave) * 1024, x_voff[j], kX4 ? koff / 16u : koff / 128u);
+        }
+    };
+    // This k-tile's scales of tile row (or TM + column) r, wide staging.
+    [[maybe_unused]] auto wide_at = [&](int t, int r) -> const uint8_t * {
+        return lds + kRing * kStageBytes + ((t / (kWide ? XG : 1)) & 1) * kWideBytes + r * kXRow +
+               (t % (kWide ? XG : 1)) * (kX4 ? 8 : 1);
+    };
 
     // Prologue: A and B of tiles 0..DEPTH-1, in the exact order the loop body
     // issues them (A copy, then B chunk by chunk), so the compiler's load
@@ -204,6 +248,7 @@ gemm_tiled_kernel(const GemmArgs args)
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    copy_scales(0);
     prologue_tile(std::integral_constant<int, 0>{});
     if constexpr (DEPTH > 1)
         prologue_tile(std::integral_constant<int, (DEPTH > 1 ? 1 : 0)>{});
@@ -215,8 +260,11 @@ gemm_tiled_kernel(const GemmArgs args)
 
     // Loads issued after the A (and scale) copy of tile t, when step t
     // begins: the B loads of tile t, then DEPTH-1 more tiles of A copies,
-    // scale copies and B loads.
-    constexpr int kAfter = S::kBLoads + (DEPTH - 1) * (S::kDmaPerWave + kXDma + S::kBLoads);
+    // scale copies and B loads.  (Wide scale copies are not counted: where
+    // some lie in between the wait is for a few loads more, never fewer; and
+    // a stage's copies are older than all the loads counted here when its
+    // first k-tile begins, XG >= DEPTH k-tiles after them.)
+    constexpr int kAfter = S::kBLoads + (DEPTH - 1) * (S::kDmaPerWave + (kWide ? 0 : kXDma) + S::kBLoads);
     static_assert(kAfter <= 63, "vmcnt field is 6 bits");
 
     uint32_t cur = 0;                                   // LDS offset of tile t
@@ -310,7 +358,7 @@ gemm_tiled_kernel(const GemmArgs args)
     // byte l/16 of the row's scale dword for that step.  Same fenced order as
     // the blockscale k-tile: LDS reads (fragment and scale dword) PD
     // fragments ahead, then the fragment's MFMAs.
-    [[maybe_unused]] auto mx4_step = [&](auto setc, uint32_t knext) {
+    [[maybe_unused]] auto mx4_step = [&](auto setc, [[maybe_unused]] int t, uint32_t knext) {
         if constexpr (SCALE == kScaleMx32) {
             constexpr int SET = decltype(setc)::value;
             static_assert(DT == kDtypeFp4 && S::kStepCh == 1 && PD >= 1, "mxfp4: one 64-byte chunk per MFMA step");
@@ -321,20 +369,22 @@ gemm_tiled_kernel(const GemmArgs args)
             const uint32_t sh = 8u * (uint32_t)(lane >> 4);
             const uint8_t *abase = lds + cur + (wm * S::kMT * S::kCH) * 1024 + lane * 16;
             const uint8_t *xs = lds + cur + S::kBufBytes;
-            const uint8_t *xap = xs + ((wm * S::kMT * 16 + rit) * 2) * 4;
-            const uint8_t *xbp = xs + 2 * TM * 4 + ((wn * S::kNT * 16 + rit) * 2) * 4;
+            constexpr int kXStride = kWide ? kXRow : 8;        // bytes from row to row
+            const uint8_t *xap = kWide ? wide_at(t, wm * S::kMT * 16 + rit) : xs + ((wm * S::kMT * 16 + rit) * 2) * 4;
+            const uint8_t *xbp = kWide ? wide_at(t, TM + wn * S::kNT * 16 + rit)
+                                       : xs + 2 * TM * 4 + ((wn * S::kNT * 16 + rit) * 2) * 4;
             int eb[S::kNT][S::kSteps];
 #pragma unroll
             for (int nt = 0; nt < S::kNT; ++nt)
 #pragma unroll
                 for (int st = 0; st < S::kSteps; ++st)
-                    eb[nt][st] = (int)((*reinterpret_cast<const uint32_t *>(xbp + (nt * 32 + st) * 4) >> sh) & 0xFFu);
+                    eb[nt][st] = (int)((*reinterpret_cast<const uint32_t *>(xbp + nt * 16 * kXStride + st * 4) >> sh) & 0xFFu);
             Frag ring[kR];
             uint32_t ra[kR];
             auto fetch = [&](int f) {
                 const int st = f / S::kMT, mt = f % S::kMT;
                 ring[f % kR] = lds_frag<DT>(abase + (mt * S::kCH + st) * 1024);
-                ra[f % kR] = *reinterpret_cast<const uint32_t *>(xap + (mt * 32 + st) * 4);
+                ra[f % kR] = *reinterpret_cast<const uint32_t *>(xap + mt * 16 * kXStride + st * 4);
             };
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -367,17 +417,29 @@ gemm_tiled_kernel(const GemmArgs args)
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAfter) : "memory");
         const uint32_t knext = kofs(t + DEPTH);
         dma_a(nxt, knext);
+        if constexpr (kWide)
+            if (t % XG == 0 && t + XG < ntiles)
+                copy_scales(t / XG + 1);
 
         constexpr int SET = decltype(setc)::value;
         if constexpr (SCALE == kScaleBlock) {
             block_step(setc, knext);
         } else if constexpr (SCALE == kScaleMx32) {
-            mx4_step(setc, knext);
+            mx4_step(setc, t, knext);
         } else {
             // mxfp8: this tile's E8M0 scales, the lane's row tiles (A) and column strips (B).
             [[maybe_unused]] i32x4 xa[kXS ? S::kMT / 4 : 1];
             [[maybe_unused]] int xb[kXS ? S::kNT : 1];
-            if constexpr (kXS) {
+            if constexpr (kXS && kWide) {
+                const int rit = lane & 15;
+#pragma unroll
+                for (int mt = 0; mt < S::kMT; ++mt)
+                    xa[mt / 4][mt % 4] = *wide_at(t, (wm * S::kMT + mt) * 16 + rit);
+#pragma unroll
+                for (int nt = 0; nt < S::kNT; ++nt)
+                    xb[nt] = *wide_at(t, TM + (wn * S::kNT + nt) * 16 + rit);
+                __builtin_amdgcn_sched_barrier(0);
+            } else if constexpr (kXS) {
                 const uint8_t *xs = lds + cur + S::kBufBytes;
                 const int rit = lane & 15;
 #pragma unroll
@@ -698,10 +760,22 @@ gemm_pingpong_kernel(const GemmArgs p)
     }
 }
 
-template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD, int GR = 0>
+template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD, int GR = 0, int XG = 0>
 void launch_tiled(const GemmArgs &a, dim3 grid, hipStream_t s)
 {
-    gemm_tiled_kernel<DT, TM, TN, WM, WN, KT, DEPTH, SCALE, OUT, PV, PD, GR><<<grid, WM * WN * 64, 0, s>>>(a);
+    gemm_tiled_kernel<DT, TM, TN, WM, WN, KT, DEPTH, SCALE, OUT, PV, PD, GR, XG><<<grid, WM * WN * 64, 0, s>>>(a);
+}
+
+// Grouped form: wide scale staging where the scale rows are whole dwords.
+template <int DT, int TM, int TN, int WM, int WN, int DEPTH, int SCALE, int PD>
+void launch_tiled_grouped(const GemmArgs &a, dim3 grid, hipStream_t s)
+{
+    constexpr int kWide = SCALE == kScaleMx32 ? 4 : SCALE == kScaleMx ? 16 : 0;
+    if constexpr (SCALE == kScaleMx) {
+        if (a.K % 512 != 0)
+            return launch_tiled<DT, TM, TN, WM, WN, 128, DEPTH, SCALE, kOutBf16, 0, PD, 1, 0>(a, grid, s);
+    }
+    launch_tiled<DT, TM, TN, WM, WN, 128, DEPTH, SCALE, kOutBf16, 0, PD, 1, kWide>(a, grid, s);
 }
 
 template <int DT, int SCALE, int OUT>
@@ -753,7 +827,7 @@ static const KernelSpec kTiledKernels[] = {
 // gemm_w4.hip does not have them for.
 #define DGP_TILEDG(DT, TM, TN, WM, WN, DEPTH, SC, PD)                                          \
     {kTiled, DT, SC, kOutBf16, TM, TN, 128, WM * WN, WM, WN, 0, PD, DEPTH, kSchedInterleaved,   \
-     &launch_tiled<DT, TM, TN, WM, WN, 128, DEPTH, SC, kOutBf16, 0, PD, 1>}
+     &launch_tiled_grouped<DT, TM, TN, WM, WN, DEPTH, SC, PD>}
 #define DGP_TILEDG_ALL(TM, TN, WM, WN, PD)                                                     \
     DGP_TILEDG(kDtypeBf16, TM, TN, WM, WN, 2, kScaleNone, PD), DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, 2, kScaleTensor, PD), \
         DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, 2, kScaleBlock, PD), DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, 2, kScaleMx, PD), \
