@@ -617,17 +617,17 @@ int64_t most_row_tiles(int64_t M, int64_t E, int64_t tm)
 //   c = (a + b k) (1 + s (x - 1)),  k = 128-byte k-steps, x = tiles on the busiest CU,
 //   m = a + weight bytes / w,
 //
-// with a, b, s, w fitted per element type and tile to graph timings of 160
+// with a, b, s, w fitted per element type and tile to graph timings of 190
 // random shapes (1 to 128 experts with 1 to 1000 rows each, unevenly filled, N
 // 128 to 7168, K 256 to 8192; weights of 0.1 MB to 4 GB): a (us) is the launch,
 // the search for the tile and the epilogue, b (us) the k-step of a tile that
 // has its CU to itself, s what a further tile on the same CU adds (below 1
-// where two overlap, above it where they contend), w (MB/us) the rate at which
-// the tile streams weights.  The fit is within 8-20 % of a timing, and the tile
-// that it picks is on average 2-3 % slower than the fastest one of its shape
-// (at worst 35 %, on two of 800).  Any one tile left out costs 0-4 % more on
-// average and up to 66 % at worst, so all of them stay; a 128 x 128 tile and a
-// half-strip one were not missed and are not compiled.
+// where two overlap, above it where they contend), w (MB/us, at most the
+// memory's 8) the rate at which the tile streams weights.  The fit is within
+// 7-21 % of a timing, and the tile that it picks is on average 2-3 % slower
+// than the fastest one of its shape (at worst 50 %, where the rows are far from
+// evenly spread).  Any one tile left out costs up to 4 % more on average and
+// 75 % at worst, so all of them stay.
 struct GroupedTile {
     int tm, tn;
     double a, b, s, w;
@@ -635,20 +635,25 @@ struct GroupedTile {
 constexpr int kGroupedTiles = 8;
 constexpr GroupedTile kGroupedCost[5][kGroupedTiles] = {
     // bf16
-    {{16, 16, 1.30, 0.128, 0.54, 8.00}, {16, 32, 1.17, 0.158, 0.73, 8.00}, {16, 64, 1.37, 0.230, 0.89, 7.45}, {64, 64, 2.10, 0.290, 0.99, 7.98},
-     {64, 128, 2.74, 0.355, 1.14, 6.14}, {64, 256, 3.02, 0.479, 1.58, 5.98}, {128, 256, 4.55, 0.581, 1.43, 5.65}, {256, 256, 7.02, 1.001, 1.32, 6.86}},
+    {{16, 16, 1.41, 0.120, 0.60, 8.00}, {16, 32, 1.65, 0.154, 0.75, 8.00}, {16, 64, 1.73, 0.220, 0.95, 7.44},
+     {64, 64, 2.30, 0.268, 1.07, 8.00}, {64, 128, 2.67, 0.308, 1.43, 6.30}, {64, 256, 3.06, 0.470, 1.64, 5.87},
+     {128, 256, 4.50, 0.587, 1.48, 5.63}, {256, 256, 6.76, 1.022, 1.27, 6.76}},
     // fp8, per-tensor scales
-    {{16, 16, 2.11, 0.119, 0.47, 8.00}, {16, 32, 2.04, 0.147, 0.54, 7.39}, {16, 64, 2.35, 0.196, 0.88, 6.82}, {64, 64, 2.33, 0.309, 0.87, 7.43},
-     {64, 128, 2.88, 0.375, 1.01, 6.07}, {64, 256, 3.30, 0.491, 1.42, 6.02}, {128, 256, 4.49, 0.672, 1.16, 5.42}, {256, 256, 7.37, 0.961, 1.34, 6.60}},
+    {{16, 16, 2.07, 0.107, 0.52, 8.00}, {16, 32, 2.20, 0.135, 0.58, 7.23}, {16, 64, 2.44, 0.183, 0.91, 6.69},
+     {64, 64, 2.45, 0.279, 0.96, 7.79}, {64, 128, 2.97, 0.301, 1.33, 6.15}, {64, 256, 3.40, 0.472, 1.52, 5.93},
+     {128, 256, 4.58, 0.666, 1.25, 5.47}, {256, 256, 7.34, 0.969, 1.37, 6.75}},
     // fp8, blockscale
-    {{16, 16, 2.53, 0.111, 0.69, 8.00}, {16, 32, 2.04, 0.171, 0.57, 7.50}, {16, 64, 2.38, 0.212, 0.89, 6.71}, {64, 64, 2.45, 0.352, 0.84, 8.00},
-     {64, 128, 3.05, 0.484, 0.88, 6.34}, {64, 256, 3.63, 0.611, 1.25, 6.09}, {128, 256, 4.32, 0.888, 1.35, 7.10}, {256, 256, 5.28, 1.780, 1.10, 8.00}},
+    {{16, 16, 2.52, 0.103, 0.74, 8.00}, {16, 32, 2.21, 0.159, 0.60, 7.25}, {16, 64, 2.47, 0.198, 0.92, 6.52},
+     {64, 64, 2.58, 0.334, 0.90, 8.00}, {64, 128, 3.08, 0.394, 1.25, 6.68}, {64, 256, 3.71, 0.598, 1.32, 6.05},
+     {128, 256, 4.43, 0.899, 1.38, 7.08}, {256, 256, 5.20, 1.824, 1.07, 8.00}},
     // mxfp8
-    {{16, 16, 2.49, 0.119, 0.69, 8.00}, {16, 32, 2.16, 0.172, 0.55, 7.65}, {16, 64, 2.40, 0.227, 0.89, 6.61}, {64, 64, 2.37, 0.332, 0.86, 7.66},
-     {64, 128, 2.91, 0.439, 1.00, 6.11}, {64, 256, 3.50, 0.610, 1.40, 5.95}, {128, 256, 3.95, 0.808, 1.52, 6.40}, {256, 256, 7.19, 1.037, 1.31, 6.52}},
+    {{16, 16, 2.48, 0.109, 0.74, 8.00}, {16, 32, 2.33, 0.157, 0.57, 7.35}, {16, 64, 2.51, 0.216, 0.91, 6.40},
+     {64, 64, 2.54, 0.305, 0.93, 8.00}, {64, 128, 3.02, 0.367, 1.29, 6.41}, {64, 256, 3.60, 0.541, 1.51, 5.92},
+     {128, 256, 4.22, 0.806, 1.50, 6.60}, {256, 256, 7.17, 1.045, 1.34, 6.78}},
     // mxfp4
-    {{16, 16, 2.60, 0.147, 0.37, 8.00}, {16, 32, 2.45, 0.193, 0.50, 7.06}, {16, 64, 2.61, 0.271, 0.84, 5.99}, {64, 64, 2.51, 0.447, 0.75, 8.00},
-     {64, 128, 2.97, 0.583, 0.89, 5.98}, {64, 256, 3.38, 0.728, 1.36, 5.77}, {128, 256, 3.94, 1.048, 1.43, 7.55}, {256, 256, 7.48, 1.434, 1.26, 5.54}},
+    {{16, 16, 2.62, 0.126, 0.39, 6.73}, {16, 32, 2.54, 0.173, 0.51, 6.24}, {16, 64, 2.67, 0.244, 0.87, 5.59},
+     {64, 64, 2.69, 0.397, 0.71, 8.00}, {64, 128, 3.16, 0.497, 1.06, 6.78}, {64, 256, 3.72, 0.609, 1.30, 5.75},
+     {128, 256, 4.69, 0.983, 1.26, 6.69}, {256, 256, 7.42, 1.467, 1.23, 6.46}},
 };
 
 // Row tiles to expect: one expert's are known; several leave half a tile each
