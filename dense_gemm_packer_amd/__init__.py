@@ -1,9 +1,8 @@
 """Python binding of the gfx950 preshuffled-B GEMM library (libdgp.so).
 
-Argument marshalling only, through ctypes; the operators that write a
-product's operand and the product grouped by expert go through a small native
-module (csrc/torch_binding.cpp, _binding.so) that makes the same checks and
-calls the same C ABI: every computation runs in the HIP kernels behind
+Argument marshalling only, through ctypes; the one-pass products and the
+operators that write their operands go through a small native module
+(csrc/torch_binding.cpp, _binding.so), whose calls cost less on the host: every computation runs in the HIP kernels behind
 the C ABI declared in include/dgp.h.  torch supplies device memory (outputs
 are allocated as torch tensors when not given) and the stream (the current
 torch stream unless one is passed).  There is no fallback: if the compiled
@@ -188,7 +187,7 @@ def _native():
             loader.exec_module(module)
             _module = module
         names = ("dgp_quantize_workspace_bytes", "dgp_quantize", "dgp_quantize_b", "dgp_rmsnorm_quantize",
-                 "dgp_swiglu_quantize", "dgp_gemm_preshuffle_grouped")
+                 "dgp_swiglu_quantize", "dgp_gemm_preshuffle_grouped", "dgp_gemm_preshuffle")
         _module.bind(tuple(ctypes.cast(getattr(L, n), _vp).value for n in names), _check, _refuse_mode, _raw_stream)
         _bound = L
     return _module
@@ -375,21 +374,11 @@ def gemm_preshuffle(A: torch.Tensor, Bs: torch.Tensor, sA: torch.Tensor | None =
                     sB: torch.Tensor | None = None, scale_mode: int | None = None,
                     out: torch.Tensor | None = None, config=None, stream=None) -> torch.Tensor:
     """C = A * B^T (bf16 [M][N]) with Bs = preshuffle_b(B)."""
-    _dev(A, "A"), _dev(Bs, "Bs")
-    for s, name in ((sA, "sA"), (sB, "sB"), (out, "out")):
-        if s is not None:
-            _dev(s, name)
-    _same_device(A, (Bs, "Bs"), (sA, "sA"), (sB, "sB"), (out, "out"))
-    mode = _scale_mode(A, sA, sB, scale_mode)
-    check_gemm_operands(A, Bs, sA, sB, mode, out)
-    M, K = A.shape[0], k_elements(A)
-    N = Bs.shape[0]
-    if out is None:
-        with _alloc_stream(stream):
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-    _check(lib().dgp_gemm_preshuffle(_ptr(A), _ptr(Bs), _ptr(out), M, N, K, dtype_code(A), mode,
-                                     _ptr(sA), _ptr(sB), _config(config), _stream_handle(stream)))
-    return out
+    if scale_mode is None:
+        _dev(A, "A")
+        scale_mode = _scale_mode(A, sA, sB, None)
+    cfg = None if config is None else config if isinstance(config, Config) else Config(**config)
+    return _native().gemm(A, Bs, sA, sB, scale_mode, out, None if cfg is None else ctypes.addressof(cfg), stream)
 
 
 def splitk_workspace_bytes(M: int, N: int, split_k: int) -> int:
@@ -440,10 +429,9 @@ def gemm_preshuffle_grouped(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Te
     (unspecified without it)."""
     if scale_mode is None:
         scale_mode = _scale_mode(A, sA, sB, None)
-    if config is None:
-        return _native().grouped(A, Bs, offsets, sA, sB, scale_mode, rows, out, None, stream)
-    cfg = config if isinstance(config, Config) else Config(**config)
-    return _native().grouped(A, Bs, offsets, sA, sB, scale_mode, rows, out, ctypes.addressof(cfg), stream)
+    cfg = None if config is None else config if isinstance(config, Config) else Config(**config)
+    return _native().grouped(A, Bs, offsets, sA, sB, scale_mode, rows, out,
+                             None if cfg is None else ctypes.addressof(cfg), stream)
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20   # DGP_NOALLOC_SCRATCH_BYTES

@@ -911,6 +911,8 @@ dgp_status dgp_quantize(const void *X, int64_t ldx, int x_type, void *Q, void *S
     RowQuantArgs a{};
     a.X = X, a.Q = Q, a.S = S, a.scale = scale;
     a.ldx = a.ldu = ldx, a.M = M, a.K = K;
+    if (measure && small_tensor(M, K))
+        return hip_status(launch_small_tensor_quant(a, x_type, (hipStream_t)stream), "quantisation launch");
     if (measure) {
         a.nparts = amax_parts(M, K);
         a.parts = (const uint32_t *)ws;

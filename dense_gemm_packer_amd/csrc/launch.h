@@ -124,6 +124,8 @@ struct NormArgs {
 };
 constexpr int kAmaxParts = 256;   // most partial maxima per matrix
 hipError_t launch_row_quant(const RowQuantArgs &a, int x_type, int mode, bool gated, hipStream_t s);
+bool small_tensor(int64_t M, int64_t K);   // measured per-tensor scale in one launch
+hipError_t launch_small_tensor_quant(const RowQuantArgs &a, int x_type, hipStream_t s);
 hipError_t launch_amax(const void *X, int64_t ldx, int x_type, int64_t groups, int64_t M, int64_t K, int parts_per_group,
                        uint32_t *parts, hipStream_t s);
 hipError_t launch_quantize_b(const WeightQuantArgs &a, int x_type, int mode, hipStream_t s);

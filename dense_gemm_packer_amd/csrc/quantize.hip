@@ -324,6 +324,57 @@ __global__ __launch_bounds__(256) void row_quant_kernel(const RowQuantArgs a)
     }
 }
 
+// Per-tensor quantisation of a small matrix in one launch: one workgroup holds
+// it all in registers between the maximum and the codes.  64 K elements are
+// 1-2 us for one CU to read; the two launches of a larger matrix cost 3 us
+// more on the host and 2 us more between them.
+constexpr int kSmallTensor = 65536;
+template <int XT>
+__global__ __launch_bounds__(1024) void small_tensor_quant_kernel(const RowQuantArgs a)
+{
+    constexpr int U = kSmallTensor / 8 / 1024;
+    const uint32_t k8 = (uint32_t)(a.K / 8), total = (uint32_t)a.M * k8;
+    Raw8<XT> r[U];
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t i = threadIdx.x + u * 1024u;
+        if (i < total) {
+            const uint32_t row = i / k8, col = (i - row * k8) * 8u;
+            r[u] = load_raw8<XT>(a.X, (int64_t)row * a.ldx + col);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (threadIdx.x + u * 1024u < total) {
+            float x[8];
+            to_float8<XT>(r[u], x);
+            m = umax(m, amax_bits(x));
+        }
+    }
+    __shared__ uint32_t red[16];
+    m = max64(m);
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int w = 1; w < 16; ++w)
+        m = umax(m, red[w]);
+    const float s = scale_f32(m), f = 1.0f / s;
+    if (threadIdx.x == 0)
+        static_cast<float *>(a.S)[0] = s;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t i = threadIdx.x + u * 1024u;
+        if (i < total) {
+            float x[8];
+            to_float8<XT>(r[u], x);
+            emit8<kScaleTensor, false>(x, i, a.Q, a.S, f);
+        }
+    }
+}
+
 // Largest magnitude of a matrix (of each of gridDim.y stacked ones), one
 // partial per workgroup: parts[group][gridDim.x].  The maximum is taken in
 // integers, so the order of the partials never matters.
@@ -621,6 +672,19 @@ hipError_t launch_row_quant(const RowQuantArgs &a, int x_type, int mode, bool ga
     case kTypeF32: return gated ? launch_rows_mode<kTypeF32, true>(a, mode, s) : launch_rows_mode<kTypeF32, false>(a, mode, s);
     default: return hipErrorInvalidValue;
     }
+}
+
+bool small_tensor(int64_t M, int64_t K) { return M * K <= kSmallTensor; }
+
+hipError_t launch_small_tensor_quant(const RowQuantArgs &a, int x_type, hipStream_t s)
+{
+    switch (x_type) {
+    case kDtypeBf16: small_tensor_quant_kernel<kDtypeBf16><<<1, 1024, 0, s>>>(a); break;
+    case kTypeF16: small_tensor_quant_kernel<kTypeF16><<<1, 1024, 0, s>>>(a); break;
+    case kTypeF32: small_tensor_quant_kernel<kTypeF32><<<1, 1024, 0, s>>>(a); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
 }
 
 hipError_t launch_amax(const void *X, int64_t ldx, int x_type, int64_t groups, int64_t M, int64_t K, int parts_per_group,

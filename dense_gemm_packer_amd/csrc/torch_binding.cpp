@@ -1,5 +1,5 @@
 // Native half of the Python binding for the operators that write a product's
-// operand and for the product grouped by expert (dense_gemm_packer_amd's
+// operand and for the products that take it (dense_gemm_packer_amd's
 // __init__.py): argument checks, allocation of the outputs and the call of the
 // C ABI, in one step.  A decode step makes many of these calls on a few rows
 // each, where the kernel takes 2-4 us: with the checks and allocations in
@@ -33,6 +33,7 @@ struct Abi {
     decltype(&dgp_rmsnorm_quantize) rmsnorm;
     decltype(&dgp_swiglu_quantize) swiglu;
     decltype(&dgp_gemm_preshuffle_grouped) grouped;
+    decltype(&dgp_gemm_preshuffle) gemm;
 };
 Abi abi;
 PyObject *raise_status;     // raises DgpError for a status code
@@ -432,6 +433,80 @@ void check_scales(const Tensor &t, const char *what, int mode, int64_t n, const 
     dense(t, t.scalar_type(), t.sizes(), A, what);
 }
 
+// The scales of a product's operands, `stack` weights of N rows.  (K or N
+// that break a mode's divisibility rule are the C ABI's to refuse.)
+void check_all_scales(const Tensor &sA, const Tensor &sB, int mode, int64_t a_rows, int64_t stack, int64_t N, int64_t K,
+                      const Tensor &A)
+{
+    if (mode == DGP_SCALE_TENSOR) {
+        check_scales(sA, "sA", mode, 1, A);
+        check_scales(sB, "sB", mode, stack, A);
+    } else if (mode == DGP_SCALE_BLOCK128 && K % 128 == 0 && N % 128 == 0) {
+        check_scales(sA, "sA", mode, a_rows * (K / 128), A);
+        check_scales(sB, "sB", mode, stack * (N / 128) * (K / 128), A);
+    } else if (mode == DGP_SCALE_MX128 && K % 128 == 0) {
+        check_scales(sA, "sA", mode, a_rows * (K / 128), A);
+        check_scales(sB, "sB", mode, stack * N * (K / 128), A);
+    } else if (mode == DGP_SCALE_MX32 && K % 32 == 0) {
+        check_scales(sA, "sA", mode, a_rows * (K / 32), A);
+        check_scales(sB, "sB", mode, stack * N * (K / 32), A);
+    }
+}
+
+long product_mode(PyObject *o)
+{
+    const long mode = PyLong_AsLong(o);
+    if (mode == -1 && PyErr_Occurred())
+        throw python_error();
+    return mode;
+}
+
+const dgp_config *config_at(PyObject *o)
+{
+    if (o == Py_None)
+        return nullptr;
+    const void *p = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred())
+        throw python_error();
+    return (const dgp_config *)p;
+}
+
+// gemm(A, Bs, sA, sB, mode, out, config address, stream)
+PyObject *gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 8);
+    const Tensor &A = tensor(a[0], "A"), &Bs = tensor(a[1], "Bs");
+    const Tensor sA = maybe(a[2], "sA"), sB = maybe(a[3], "sB");
+    const long mode = product_mode(a[4]);
+    Tensor C = maybe(a[5], "out");
+    const dgp_config *cfg = config_at(a[6]);
+    if (A.dim() != 2 || Bs.dim() != 2)
+        bad_value(text("A and Bs must be 2-D (got ", A.dim(), "-D and ", Bs.dim(), "-D)"));
+    on_device(A, "A");
+    const int dtype = operand_code(A);
+    if (Bs.scalar_type() != A.scalar_type())
+        bad_value(text("Bs is ", Bs.scalar_type(), ", A is ", A.scalar_type(), ": both operands take one element type"));
+    const int64_t per = dtype == DGP_FP4_E2M1 ? 2 : 1;
+    const int64_t M = A.size(0), N = Bs.size(0), K = A.size(1) * per;
+    if (Bs.size(1) != A.size(1))
+        bad_value(text("Bs holds ", Bs.size(1) * per, " elements per row, A ", K));
+    if (!A.is_contiguous() || !Bs.is_contiguous())
+        bad_value("A and Bs must be contiguous");
+    same_device(Bs, "Bs", A);
+    const int64_t shape_c[2] = {M, N};
+    if (C.defined())
+        dense(C, ScalarType::BFloat16, shape_c, A, "out");
+    check_all_scales(sA, sB, (int)mode, M, 1, N, K, A);
+    Place place(A, a[7]);
+    if (!C.defined())
+        C = empty(shape_c, ScalarType::BFloat16, A);
+    call(abi.gemm, (const void *)A.data_ptr(), (const void *)Bs.data_ptr(), C.data_ptr(), M, N, K, dtype, (int)mode,
+         (const void *)ptr(sA), (const void *)ptr(sB), cfg, place.handle());
+    return THPVariable_Wrap(C);
+    END_HANDLE_TH_ERRORS
+}
+
 // grouped(A, Bs, offsets, sA, sB, mode, rows, out, config address, stream)
 PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -440,12 +515,8 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor &A = tensor(a[0], "A"), &Bs = tensor(a[1], "Bs"), &off = tensor(a[2], "offsets");
     const Tensor sA = maybe(a[3], "sA"), sB = maybe(a[4], "sB"), rows = maybe(a[6], "rows");
     Tensor C = maybe(a[7], "out");
-    const long mode = PyLong_AsLong(a[5]);
-    if (mode == -1 && PyErr_Occurred())
-        throw python_error();
-    const void *cfg = a[8] == Py_None ? nullptr : PyLong_AsVoidPtr(a[8]);
-    if (PyErr_Occurred())
-        throw python_error();
+    const long mode = product_mode(a[5]);
+    const dgp_config *cfg = config_at(a[8]);
     if (A.dim() != 2 || Bs.dim() != 3)
         bad_value(text("A must be 2-D and Bs 3-D (got ", A.dim(), "-D and ", Bs.dim(), "-D)"));
     const int dtype = operand_code(A);
@@ -470,45 +541,32 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int64_t shape_c[2] = {M, N};
     if (C.defined())
         dense(C, ScalarType::BFloat16, shape_c, A, "out");
-    // (K or N that break a mode's divisibility rule are the C ABI's to refuse)
-    const int64_t kb = K / 128;
-    if (mode == DGP_SCALE_TENSOR) {
-        check_scales(sA, "sA", DGP_SCALE_TENSOR, 1, A);
-        check_scales(sB, "sB", DGP_SCALE_TENSOR, E, A);
-    } else if (mode == DGP_SCALE_BLOCK128 && K % 128 == 0 && N % 128 == 0) {
-        check_scales(sA, "sA", DGP_SCALE_BLOCK128, A.size(0) * kb, A);
-        check_scales(sB, "sB", DGP_SCALE_BLOCK128, E * (N / 128) * kb, A);
-    } else if (mode == DGP_SCALE_MX128 && K % 128 == 0) {
-        check_scales(sA, "sA", DGP_SCALE_MX128, A.size(0) * kb, A);
-        check_scales(sB, "sB", DGP_SCALE_MX128, E * N * kb, A);
-    } else if (mode == DGP_SCALE_MX32 && K % 32 == 0) {
-        check_scales(sA, "sA", DGP_SCALE_MX32, A.size(0) * (K / 32), A);
-        check_scales(sB, "sB", DGP_SCALE_MX32, E * N * (K / 32), A);
-    }
+    check_all_scales(sA, sB, (int)mode, A.size(0), E, N, K, A);
     on_device(A, "A");
     Place place(A, a[9]);
     if (!C.defined())
         C = empty(shape_c, ScalarType::BFloat16, A);
     call(abi.grouped, (const void *)A.data_ptr(), A.size(0), (const void *)Bs.data_ptr(), C.data_ptr(), M, N, K, E,
          (const int32_t *)off.data_ptr(), (const int32_t *)ptr(rows), dtype, (int)mode, (const void *)ptr(sA),
-         (const void *)ptr(sB), (const dgp_config *)cfg, place.handle());
+         (const void *)ptr(sB), cfg, place.handle());
     return THPVariable_Wrap(C);
     END_HANDLE_TH_ERRORS
 }
 
 // bind(addresses, raise_status, refuse_mode, current_stream): addresses of the
-// six entry points in Abi's order.
+// entry points in Abi's order.
 PyObject *bind(PyObject *, PyObject *args)
 {
     PyObject *addr, *rs, *rm, *cs;
     if (!PyArg_ParseTuple(args, "O!OOO", &PyTuple_Type, &addr, &rs, &rm, &cs))
         return nullptr;
-    void *p[6];
-    if (PyTuple_GET_SIZE(addr) != 6) {
-        PyErr_SetString(PyExc_ValueError, "six addresses expected");
+    constexpr int kEntries = sizeof(Abi) / sizeof(void *);
+    void *p[kEntries];
+    if (PyTuple_GET_SIZE(addr) != kEntries) {
+        PyErr_Format(PyExc_ValueError, "%d addresses expected", kEntries);
         return nullptr;
     }
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(addr, i));
         if (!p[i]) {
             if (!PyErr_Occurred())
@@ -517,7 +575,8 @@ PyObject *bind(PyObject *, PyObject *args)
         }
     }
     abi = Abi{(decltype(Abi::workspace_bytes))p[0], (decltype(Abi::quantize))p[1], (decltype(Abi::quantize_b))p[2],
-              (decltype(Abi::rmsnorm))p[3], (decltype(Abi::swiglu))p[4], (decltype(Abi::grouped))p[5]};
+              (decltype(Abi::rmsnorm))p[3], (decltype(Abi::swiglu))p[4], (decltype(Abi::grouped))p[5],
+              (decltype(Abi::gemm))p[6]};
     Py_XSETREF(raise_status, Py_NewRef(rs));
     Py_XSETREF(refuse_mode, Py_NewRef(rm));
     Py_XSETREF(current_stream, Py_NewRef(cs));
@@ -525,7 +584,7 @@ PyObject *bind(PyObject *, PyObject *args)
 }
 
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(quantize), FAST(quantize_b), FAST(rmsnorm_quantize), FAST(swiglu_quantize), FAST(grouped),
+PyMethodDef methods[] = {FAST(quantize), FAST(quantize_b), FAST(rmsnorm_quantize), FAST(swiglu_quantize), FAST(grouped), FAST(gemm),
                          {"bind", bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

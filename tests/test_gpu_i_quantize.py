@@ -33,6 +33,14 @@ def test_quantize(x_type, mode, m, k):
     check_operand(Q, S, x, mode)
 
 
+@pytest.mark.parametrize("x_type", list(TYPES))
+@pytest.mark.parametrize("m,k", [(511, 128), (512, 128), (513, 128), (8, 8192), (9, 8192)])
+def test_quantize_tensor_around_the_one_launch_limit(x_type, m, k):
+    wide = rows(m, k + 256, TYPES[x_type], m)
+    for x in (wide[:, :k], wide[:, :k].contiguous()):
+        check_operand(*dgp.quantize(x.to(DEV) if x.is_contiguous() else wide.to(DEV)[:, :k], dgp.SCALE_TENSOR), x, "tensor")
+
+
 @pytest.mark.parametrize("mode", ["tensor", "block128", "mx128"])
 def test_quantize_odd_block_count(mode):
     x = rows(7, 128 * 9, torch.bfloat16, 3)
@@ -125,10 +133,11 @@ def test_nonfinite_block_gets_a_nan_scale(x_type, mode, bad):
     check_operand(Q.view(torch.uint8).cpu()[keep].view(Q.dtype), s[keep], x[keep], mode)
 
 
+@pytest.mark.parametrize("m", [40, 300])     # one launch, and two
 @pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
-def test_nonfinite_tensor_gets_a_nan_scale(bad):
-    x = rows(300, 512, torch.bfloat16, 9)
-    x[250, 400] = bad
+def test_nonfinite_tensor_gets_a_nan_scale(bad, m):
+    x = rows(m, 512, torch.bfloat16, 9)
+    x[m - 3, 400] = bad
     Q, S = dgp.quantize(x.to(DEV), dgp.SCALE_TENSOR)
     assert bool(torch.isnan(S).all()) and bool(torch.isnan(Q.cpu().double()).all())
 
