@@ -51,9 +51,10 @@ const KernelSpec *grouped_table(int *count)
     static const std::vector<KernelSpec> all = [] {
         std::vector<KernelSpec> v;
         int n = 0;
-        const KernelSpec *t = tiled_grouped_kernels(&n);
+        // (the one-wave-per-SIMD kernels first: a tile that both have is theirs)
+        const KernelSpec *t = w4_grouped_kernels(&n);
         v.insert(v.end(), t, t + n);
-        t = w4_grouped_kernels(&n);
+        t = tiled_grouped_kernels(&n);
         v.insert(v.end(), t, t + n);
         t = stream_grouped_kernels(&n);
         v.insert(v.end(), t, t + n);
@@ -152,6 +153,7 @@ bool spec_fits(const KernelSpec &k, int64_t Ks)
 struct Query {
     int family, dtype, scale, out, tm, tn;
     int kt = -1, wm = -1, depth = -1, pv = -1, pd = -1, sched = -1, lay = -1, copy = -1;
+    int64_t K = 0;   // for kernels that need K to be a multiple of something
 };
 
 const KernelSpec *find_spec(const Query &q, const KernelSpec *(*table)(int *) = kernel_table)
@@ -165,7 +167,7 @@ const KernelSpec *find_spec(const Query &q, const KernelSpec *(*table)(int *) = 
             k.tn == q.tn && (q.kt < 0 || k.kt == q.kt) && (q.wm < 0 || wm == q.wm) &&
             (q.depth < 0 || k.depth == q.depth) && (q.pv < 0 || k.pv == q.pv) && (q.pd < 0 || k.pd == q.pd) &&
             (q.sched < 0 || k.sched == q.sched) && (q.lay < 0 || (k.family == kTiled && k.lay == q.lay)) &&
-            (q.copy < 0 || (k.family == kTiled && k.copy == q.copy)))
+            (q.copy < 0 || (k.family == kTiled && k.copy == q.copy)) && (k.k_mult == 0 || q.K % k.k_mult == 0))
             return &k;
     }
     return nullptr;
@@ -398,6 +400,7 @@ dgp_status configured_spec(const GemmCall &c, int64_t Ks, const KernelSpec *(*ta
         q.wm = c.cfg->waves_m > 0 ? c.cfg->waves_m : -1;   // matched against waves per workgroup
         q.depth = c.cfg->prefetch > 0 ? c.cfg->prefetch : -1;
     }
+    q.K = c.K;
     const KernelSpec *spec = find_spec(q, table);
     if (!spec)
         return fail(DGP_ERR_CONFIG,
@@ -617,17 +620,17 @@ int64_t most_row_tiles(int64_t M, int64_t E, int64_t tm)
 //   c = (a + b k) (1 + s (x - 1)),  k = 128-byte k-steps, x = tiles on the busiest CU,
 //   m = a + weight bytes / w,
 //
-// with a, b, s, w fitted per element type and tile to graph timings of 190
+// with a, b, s, w fitted per element type and tile to graph timings of 210
 // random shapes (1 to 128 experts with 1 to 1000 rows each, unevenly filled, N
 // 128 to 7168, K 256 to 8192; weights of 0.1 MB to 4 GB): a (us) is the launch,
 // the search for the tile and the epilogue, b (us) the k-step of a tile that
 // has its CU to itself, s what a further tile on the same CU adds (below 1
 // where two overlap, above it where they contend), w (MB/us, at most the
 // memory's 8) the rate at which the tile streams weights.  The fit is within
-// 7-21 % of a timing, and the tile that it picks is on average 2-3 % slower
-// than the fastest one of its shape (at worst 50 %, where the rows are far from
-// evenly spread).  Any one tile left out costs up to 4 % more on average and
-// 75 % at worst, so all of them stay.
+// 6-22 % of a timing, and the tile that it picks is on average 2-3 % slower
+// than the fastest one of its shape (at worst 26-59 %, where the rows are far
+// from evenly spread).  Any one tile left out costs up to 5 % more on average
+// in some type, so all of them stay.
 struct GroupedTile {
     int tm, tn;
     double a, b, s, w;
@@ -635,25 +638,25 @@ struct GroupedTile {
 constexpr int kGroupedTiles = 8;
 constexpr GroupedTile kGroupedCost[5][kGroupedTiles] = {
     // bf16
-    {{16, 16, 1.41, 0.120, 0.60, 8.00}, {16, 32, 1.65, 0.154, 0.75, 8.00}, {16, 64, 1.73, 0.220, 0.95, 7.44},
-     {64, 64, 2.30, 0.268, 1.07, 8.00}, {64, 128, 2.67, 0.308, 1.43, 6.30}, {64, 256, 3.06, 0.470, 1.64, 5.87},
-     {128, 256, 4.50, 0.587, 1.48, 5.63}, {256, 256, 6.76, 1.022, 1.27, 6.76}},
+    {{16, 16, 1.17, 0.112, 0.64, 8.00}, {16, 32, 1.05, 0.153, 0.82, 8.00}, {16, 64, 1.51, 0.215, 1.01, 7.91},
+     {64, 64, 2.19, 0.249, 1.15, 7.92}, {64, 128, 2.36, 0.283, 1.58, 6.26}, {64, 256, 3.00, 0.370, 1.78, 5.67},
+     {128, 256, 4.41, 0.571, 1.61, 5.76}, {256, 256, 7.27, 0.986, 1.39, 6.92}},
     // fp8, per-tensor scales
-    {{16, 16, 2.07, 0.107, 0.52, 8.00}, {16, 32, 2.20, 0.135, 0.58, 7.23}, {16, 64, 2.44, 0.183, 0.91, 6.69},
-     {64, 64, 2.45, 0.279, 0.96, 7.79}, {64, 128, 2.97, 0.301, 1.33, 6.15}, {64, 256, 3.40, 0.472, 1.52, 5.93},
-     {128, 256, 4.58, 0.666, 1.25, 5.47}, {256, 256, 7.34, 0.969, 1.37, 6.75}},
+    {{16, 16, 2.04, 0.104, 0.53, 8.00}, {16, 32, 1.95, 0.136, 0.61, 7.82}, {16, 64, 2.29, 0.186, 0.93, 6.77},
+     {64, 64, 2.34, 0.260, 1.03, 8.00}, {64, 128, 2.61, 0.292, 1.44, 6.54}, {64, 256, 3.23, 0.360, 1.55, 5.85},
+     {128, 256, 4.27, 0.671, 1.28, 5.66}, {256, 256, 7.24, 0.941, 1.44, 7.90}},
     // fp8, blockscale
-    {{16, 16, 2.52, 0.103, 0.74, 8.00}, {16, 32, 2.21, 0.159, 0.60, 7.25}, {16, 64, 2.47, 0.198, 0.92, 6.52},
-     {64, 64, 2.58, 0.334, 0.90, 8.00}, {64, 128, 3.08, 0.394, 1.25, 6.68}, {64, 256, 3.71, 0.598, 1.32, 6.05},
-     {128, 256, 4.43, 0.899, 1.38, 7.08}, {256, 256, 5.20, 1.824, 1.07, 8.00}},
+    {{16, 16, 2.45, 0.103, 0.74, 8.00}, {16, 32, 1.98, 0.156, 0.64, 7.71}, {16, 64, 2.35, 0.197, 0.95, 6.58},
+     {64, 64, 2.57, 0.317, 0.94, 8.00}, {64, 128, 2.87, 0.384, 1.33, 7.43}, {64, 256, 3.48, 0.598, 1.35, 6.20},
+     {128, 256, 4.58, 0.857, 1.45, 7.21}, {256, 256, 5.63, 1.738, 1.19, 8.00}},
     // mxfp8
-    {{16, 16, 2.48, 0.109, 0.74, 8.00}, {16, 32, 2.33, 0.157, 0.57, 7.35}, {16, 64, 2.51, 0.216, 0.91, 6.40},
-     {64, 64, 2.54, 0.305, 0.93, 8.00}, {64, 128, 3.02, 0.367, 1.29, 6.41}, {64, 256, 3.60, 0.541, 1.51, 5.92},
-     {128, 256, 4.22, 0.806, 1.50, 6.60}, {256, 256, 7.17, 1.045, 1.34, 6.78}},
+    {{16, 16, 2.39, 0.105, 0.75, 8.00}, {16, 32, 2.09, 0.155, 0.61, 8.00}, {16, 64, 2.37, 0.212, 0.95, 6.44},
+     {64, 64, 2.52, 0.292, 0.96, 8.00}, {64, 128, 2.78, 0.352, 1.36, 6.77}, {64, 256, 3.36, 0.494, 1.48, 5.88},
+     {128, 256, 4.46, 0.733, 1.51, 6.36}, {256, 256, 7.22, 1.031, 1.39, 8.00}},
     // mxfp4
-    {{16, 16, 2.62, 0.126, 0.39, 6.73}, {16, 32, 2.54, 0.173, 0.51, 6.24}, {16, 64, 2.67, 0.244, 0.87, 5.59},
-     {64, 64, 2.69, 0.397, 0.71, 8.00}, {64, 128, 3.16, 0.497, 1.06, 6.78}, {64, 256, 3.72, 0.609, 1.30, 5.75},
-     {128, 256, 4.69, 0.983, 1.26, 6.69}, {256, 256, 7.42, 1.467, 1.23, 6.46}},
+    {{16, 16, 2.61, 0.128, 0.38, 8.00}, {16, 32, 2.48, 0.171, 0.52, 7.02}, {16, 64, 2.61, 0.245, 0.88, 5.83},
+     {64, 64, 2.68, 0.379, 0.72, 8.00}, {64, 128, 3.01, 0.498, 1.08, 7.60}, {64, 256, 3.77, 0.569, 0.96, 5.43},
+     {128, 256, 4.93, 0.811, 1.38, 6.20}, {256, 256, 7.05, 1.362, 1.25, 6.40}},
 };
 
 // Row tiles to expect: one expert's are known; several leave half a tile each
@@ -666,7 +669,7 @@ double expected_row_tiles(int64_t M, int64_t E, int tm)
     return 2 * M > live * tm ? std::max((double)live, (double)M / tm + 0.5 * live) : (double)live;
 }
 
-const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t N, int64_t Kb, int64_t E)
+const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t N, int64_t K, int64_t Kb, int64_t E)
 {
     const GroupedTile *best = nullptr;
     double least = 0;
@@ -678,7 +681,9 @@ const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t 
         if (!best || us4 < least)
             best = &t, least = us4;
     }
-    return find_spec(Query{best->tm == 16 ? kStream : kTiled, dtype, scale, kOutBf16, best->tm, best->tn}, grouped_table);
+    Query q{best->tm == 16 ? kStream : kTiled, dtype, scale, kOutBf16, best->tm, best->tn};
+    q.K = K;
+    return find_spec(q, grouped_table);
 }
 
 struct Experts {
@@ -713,7 +718,7 @@ dgp_status run_grouped(const GemmCall &c, const Experts &x, hipStream_t stream)
     if (c.cfg && c.cfg->tile_m > 0)
         DGP_TRY(configured_spec(c, Kb, grouped_table, &spec));
     else
-        spec = default_grouped_spec(c.dtype, c.scale, c.M, c.N, Kb, x.E);
+        spec = default_grouped_spec(c.dtype, c.scale, c.M, c.N, c.K, Kb, x.E);
     if (!spec)
         return fail(DGP_ERR_CONFIG, "no compiled grouped kernel fits this shape");
     const int64_t tiles_m = most_row_tiles(c.M, x.E, spec->tm), tiles_n = (c.N + spec->tn - 1) / spec->tn;

@@ -766,18 +766,6 @@ void launch_tiled(const GemmArgs &a, dim3 grid, hipStream_t s)
     gemm_tiled_kernel<DT, TM, TN, WM, WN, KT, DEPTH, SCALE, OUT, PV, PD, GR, XG><<<grid, WM * WN * 64, 0, s>>>(a);
 }
 
-// Grouped form: wide scale staging where the scale rows are whole dwords.
-template <int DT, int TM, int TN, int WM, int WN, int DEPTH, int SCALE, int PD>
-void launch_tiled_grouped(const GemmArgs &a, dim3 grid, hipStream_t s)
-{
-    constexpr int kWide = SCALE == kScaleMx32 ? 4 : SCALE == kScaleMx ? 16 : 0;
-    if constexpr (SCALE == kScaleMx) {
-        if (a.K % 512 != 0)
-            return launch_tiled<DT, TM, TN, WM, WN, 128, DEPTH, SCALE, kOutBf16, 0, PD, 1, 0>(a, grid, s);
-    }
-    launch_tiled<DT, TM, TN, WM, WN, 128, DEPTH, SCALE, kOutBf16, 0, PD, 1, kWide>(a, grid, s);
-}
-
 template <int DT, int SCALE, int OUT>
 void launch_pingpong(const GemmArgs &a, dim3 grid, hipStream_t s)
 {
@@ -822,31 +810,29 @@ static const KernelSpec kTiledKernels[] = {
 };
 
 // Product grouped by expert: 64-row tiles for experts with a few dozen rows
-// (two or four waves side by side, each all 64 rows and 32 or 64 columns; two
-// or three workgroups share a CU), and the larger tiles of the modes that
-// gemm_w4.hip does not have them for.
-#define DGP_TILEDG(DT, TM, TN, WM, WN, DEPTH, SC, PD)                                          \
-    {kTiled, DT, SC, kOutBf16, TM, TN, 128, WM * WN, WM, WN, 0, PD, DEPTH, kSchedInterleaved,   \
-     &launch_tiled_grouped<DT, TM, TN, WM, WN, DEPTH, SC, PD>}
-#define DGP_TILEDG_ALL(TM, TN, WM, WN, D, PD)                                                  \
-    DGP_TILEDG(kDtypeBf16, TM, TN, WM, WN, D, kScaleNone, PD), DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, D, kScaleTensor, PD), \
-        DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, D, kScaleBlock, PD), DGP_TILEDG(kDtypeFp8, TM, TN, WM, WN, D, kScaleMx, PD), \
-        DGP_TILEDG(kDtypeFp4, TM, TN, WM, WN, D, kScaleMx32, PD)
+// (two or four waves side by side, each all 64 rows and 32 columns, or 64 of
+// the 256-column tile; two or three workgroups share a CU), and the larger
+// tiles of the modes that gemm_w4.hip does not have them for.
+#define DGP_TILEDGX(DT, TM, TN, WN, DEPTH, SC, PD, XG, KMULT)                                  \
+    {kTiled, DT, SC, kOutBf16, TM, TN, 128, WN, 1, WN, 0, PD, DEPTH, kSchedInterleaved,         \
+     &launch_tiled<DT, TM, TN, 1, WN, 128, DEPTH, SC, kOutBf16, 0, PD, 1, XG>, 0, 0, KMULT}
+#define DGP_TILEDG(DT, TM, TN, WN, DEPTH, SC, PD) DGP_TILEDGX(DT, TM, TN, WN, DEPTH, SC, PD, 0, 0)
+// (mxfp8 twice: wide scale staging, and for rows of scales that are not whole dwords)
+#define DGP_TILEDG_ALL(TM, TN, WN, D, PD)                                                      \
+    DGP_TILEDG(kDtypeBf16, TM, TN, WN, D, kScaleNone, PD), DGP_TILEDG(kDtypeFp8, TM, TN, WN, D, kScaleTensor, PD), \
+        DGP_TILEDG(kDtypeFp8, TM, TN, WN, D, kScaleBlock, PD), DGP_TILEDGX(kDtypeFp8, TM, TN, WN, D, kScaleMx, PD, 16, 512), \
+        DGP_TILEDG(kDtypeFp8, TM, TN, WN, D, kScaleMx, PD), DGP_TILEDGX(kDtypeFp4, TM, TN, WN, D, kScaleMx32, PD, 4, 0)
 static const KernelSpec kTiledGrouped[] = {
-    DGP_TILEDG_ALL(64, 64, 1, 2, 2, 2),
+    DGP_TILEDG_ALL(64, 64, 2, 2, 2),
     // (four waves of 64 x 32 rather than two of 64 x 64: 182 against 203 us
     // per-tensor fp8, 107 against 118 us mxfp4, for 32 experts x 32 rows, N
     // 4096, K 7168; equal within 5 % at 100 rows)
-    DGP_TILEDG_ALL(64, 128, 1, 4, 3, 3),
-    // (prefetch 3 and 4 k-tiles measured equal to 2: a CU has about 32 KiB of
-    // loads beyond the L2 in flight whatever is issued)
-    DGP_TILEDG_ALL(64, 256, 1, 4, 2, 2),
-    // (mxfp4: four waves of 128 x 64, 657 against 694 us for 32 experts x 1000
-    // rows, N 4096, K 7168; the fp8 modes: eight of 128 x 32, equal or 3 % ahead)
-    DGP_TILEDG(kDtypeFp8, 128, 256, 1, 8, 2, kScaleBlock, 4),
-    DGP_TILEDG(kDtypeFp8, 128, 256, 1, 8, 2, kScaleMx, 4),
-    DGP_TILEDG(kDtypeFp4, 128, 256, 1, 4, 2, kScaleMx32, 3),
-    DGP_TILEDG(kDtypeFp8, 256, 256, 1, 8, 2, kScaleBlock, 4),
+    DGP_TILEDG_ALL(64, 128, 4, 3, 3),
+    // (prefetch 3 and 4 k-tiles measured equal to 2)
+    DGP_TILEDG(kDtypeFp8, 64, 256, 4, 2, kScaleBlock, 2), DGP_TILEDG(kDtypeFp8, 64, 256, 4, 2, kScaleMx, 2),
+    // (eight waves of 128 x 32 rather than four of 128 x 64: equal or 3 % ahead)
+    DGP_TILEDG(kDtypeFp8, 128, 256, 8, 2, kScaleBlock, 4), DGP_TILEDG(kDtypeFp8, 128, 256, 8, 2, kScaleMx, 4),
+    DGP_TILEDG(kDtypeFp8, 256, 256, 8, 2, kScaleBlock, 4),
 };
 
 const KernelSpec *tiled_grouped_kernels(int *count)

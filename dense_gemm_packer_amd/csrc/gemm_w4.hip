@@ -46,6 +46,12 @@ constexpr int kRA = 7;                   // tuned LDS read-ahead (fragments ahea
 // stage, 3 k-tiles ahead (false), or early in the next k-tile, 2 ahead (true).
 constexpr bool kDmaLate = false;
 constexpr int kDmaAhead = kDmaLate ? 2 : 3;
+// Workgroups per CU (waves per SIMD) of a tile of tm rows.  (mxfp4, 128 rows:
+// its 88 KiB of LDS leave room for one.)
+constexpr int waves_per_simd(int tm, int scale)
+{
+    return tm == 256 || (tm == 128 && scale == kScaleMx32) ? 1 : 2;
+}
 
 // WM = waves along M: 1 = the 1 x 4 split (each wave all TM rows, 64
 // columns), 2 = 2 x 2 (each wave TM/2 rows, 128 columns).  TM = tile rows:
@@ -99,35 +105,57 @@ struct Plan {
 
 }  // namespace w4
 
-// acc += B-fragment x A-fragment, in place on AGPRs: bf16 K32 ...
+// acc += B-fragment x A-fragment, in place: on AGPRs, or (V: tiles of 64
+// rows, whose accumulators leave room for everything in the 256 VGPRs of a
+// wave that shares its SIMD with another) on VGPRs.  bf16 K32 ...
+template <bool V>
 __device__ inline void mfma_acc(f32x4 &acc, const i32x4 &b, const i32x4 &a)
 {
-    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+    if constexpr (V)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(b), "v"(a));
+    else
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
 // ... and e4m3 K128 (unscaled form: both operands OCP e4m3).
+template <bool V>
 __device__ inline void mfma_acc(f32x4 &acc, const i32x8 &b, const i32x8 &a)
 {
-    asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+    if constexpr (V)
+        asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0" : "+v"(acc) : "v"(b), "v"(a));
+    else
+        asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
 // ... and the hardware-scaled e4m3 K128 form (mxfp8): eb scales the B
 // fragment (first operand: lane l's byte for its column), ea the A fragment
 // (its row), both E8M0 in the low byte (op_sel byte 0).
+template <bool V>
 __device__ inline void mfma_acc_mx(f32x4 &acc, const i32x8 &b, const i32x8 &a, int eb, int ea)
 {
-    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-                 : "+a"(acc)
-                 : "v"(b), "v"(a), "v"(eb), "v"(ea));
+    if constexpr (V)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                     : "+v"(acc)
+                     : "v"(b), "v"(a), "v"(eb), "v"(ea));
+    else
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                     : "+a"(acc)
+                     : "v"(b), "v"(a), "v"(eb), "v"(ea));
 }
 
 // ... and the hardware-scaled E2M1 K128 form (mxfp4: 16 bytes = 32 values per
 // lane, one 32-value block, cbsz = blgp = 4).
+template <bool V>
 __device__ inline void mfma_acc_mx4(f32x4 &acc, const i32x4 &b, const i32x4 &a, int eb, int ea)
 {
-    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                 : "+a"(acc)
-                 : "v"(b), "v"(a), "v"(eb), "v"(ea));
+    if constexpr (V)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+v"(acc)
+                     : "v"(b), "v"(a), "v"(eb), "v"(ea));
+    else
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(acc)
+                     : "v"(b), "v"(a), "v"(eb), "v"(ea));
 }
 
 // DB: B register sets = k-tiles of B loads in flight (2..4).
@@ -168,8 +196,13 @@ __device__ inline void mfma_acc_mx4(f32x4 &acc, const i32x4 &b, const i32x4 &a, 
 // bit-field extract per fragment.
 //
 // GR: 1 = the product grouped by expert (gemm_common.h).
-template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM, int GR>
-__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(256 / TM, 256 / TM)))
+// XG: 0 = E8M0 scales staged per k-tile as above; else for XG k-tiles at once
+// in 16-byte pieces, row by row, into two areas in turn (gemm_tiled.hip says
+// why), which also fits tiles of fewer rows: a lane then reads each row's and
+// column's 1 (mxfp8) or 8 (mxfp4) bytes of a k-tile by themselves.
+template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM, int GR, int XG>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256),
+                               amdgpu_waves_per_eu(w4::waves_per_simd(TM, SCALE), w4::waves_per_simd(TM, SCALE))))
 gemm_w4_kernel(const GemmArgs args)
 {
     static_assert(DB >= 2 && DB <= 4, "B sets");
@@ -181,21 +214,25 @@ gemm_w4_kernel(const GemmArgs args)
     static_assert(!kMx || (DT == kDtypeFp8 && SWZ && !SYNC && !kDmaLate), "mxfp8: fp8, swizzled rows, async copies");
     static_assert(!kMx4 || (DT == kDtypeFp4 && SWZ && !SYNC && !kDmaLate), "mxfp4: fp4, swizzled rows, async copies");
     constexpr int kRA = RA;
+    constexpr bool kAccV = TM == 64;   // accumulators in VGPRs
     static_assert(WM == 1 || WM == 2, "waves along M: 1 (1 x 4) or 2 (2 x 2)");
     static_assert(WM == 1 || !(kMx || kMx4), "the MX scale staging assumes the 1 x 4 split");
-    static_assert(TM == 256 || (TM == 128 && !(kMx || kMx4)), "tile rows: 256, or 128 without MX scales");
+    constexpr bool kWide = XG > 0;
+    static_assert(TM == 256 || ((TM == 128 || TM == 64) && (kWide || !(kMx || kMx4))),
+                  "tile rows: 256, or 128 and 64 without MX scales or with wide staging");
+    static_assert(!kWide || ((kMx || kMx4) && (XG & (XG - 1)) == 0 && (kMx4 ? 8 : 1) * XG % 16 == 0), "whole 16-byte pieces");
     using P = Plan<DT, RA, WM, TM>;
     constexpr int kBuf = P::kBuf, kDma = P::kDma;
     constexpr int kMT = P::kMT, kNT = P::kNT;
     using Frag = typename Op<DT>::Frag;
     constexpr int kFr = P::kFr, kBar = P::kBar, kStepCh = P::kStepCh;
-    static_assert(!kMx || (kFr == kMT && kMT % 4 == 0 && kRA < kFr - 4), "mxfp8: one k-step per k-tile, quad ring");
-    static_assert(!kMx4 || (kFr == 2 * kMT && kRA < kMT - 4), "mxfp4: two k-steps per k-tile, quad ring");
+    static_assert(!kMx || (kFr == kMT && kMT % 4 == 0 && (kWide || kRA < kFr - 4)), "mxfp8: one k-step per k-tile, quad ring");
+    static_assert(!kMx4 || (kFr == 2 * kMT && (kWide || kRA < kMT - 4)), "mxfp4: two k-steps per k-tile, quad ring");
     static_assert(!kMx4 || kFr % 2 == 0, "mxfp4: the row-scale slot of fragment f is f % 2 across k-tiles");
     // The barrier's count: the scale copies of the k-tiles in between are
     // 2 (mxfp8) or 4 (mxfp4) more loads per k-tile (those of the barrier's
     // own tile precede its last A copy).
-    constexpr int kXCopies = kMx ? 2 : kMx4 ? 4 : 0;
+    constexpr int kXCopies = kWide ? 0 : kMx ? 2 : kMx4 ? 4 : 0;
     constexpr int kVm = P::vm_at_barrier() + kXCopies * (kDmaAhead - 2);
     static_assert(kVm <= 63, "vmcnt field is 6 bits");
     // One LDS object (the A ring, then for mxfp8 the scale stages): the
@@ -203,7 +240,15 @@ gemm_w4_kernel(const GemmArgs args)
     // one object apart by their order, where a second object made it wait
     // for every copy in flight before each read.
     constexpr int kXStage = kMx ? 2048 : kMx4 ? 4096 : 0;   // scale bytes per stage
-    constexpr int kXBytes = kRing * kXStage;
+    constexpr int kXRow = (kMx4 ? 8 : 1) * XG;              // wide: bytes per row and stage of XG k-tiles
+    constexpr int kXWide = ((TM + TN) * kXRow / 16 + 255) / 256;   // wide: 16-byte copies per wave and stage
+    constexpr int kWideBytes = kXWide * NW * 1024;          // one of the two areas
+    constexpr int kXBytes = kWide ? 2 * kWideBytes : kRing * kXStage;
+    // Wide copies are not in kVm: the wait for a k-tile's A copy is then for
+    // some loads more, never fewer.  A stage is first read behind the barrier
+    // XG - 1 k-tiles after its copies, by when more loads follow them than
+    // that barrier leaves outstanding.
+    static_assert(!kWide || (XG - 1) * (kDma + P::kBLoads) >= kVm, "a wide stage has landed when it is first read");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * kBuf + kXBytes];
     if constexpr (kLdsPoison) {   // debug build: all of LDS poisoned before the first copy
         lds_poison_fill(lds, (int)sizeof(lds));
@@ -286,8 +331,42 @@ gemm_w4_kernel(const GemmArgs args)
     auto xstage = [&](int t) -> uint32_t * {
         return reinterpret_cast<uint32_t *>(lds + kRing * kBuf + (kX ? (t & (kRing - 1)) * kXStage : 0));
     };
+    // Wide staging: piece e of a stage is row e / (kXRow / 16) of the tile's
+    // rows, then of its columns.
+    [[maybe_unused]] __amdgpu_buffer_rsrc_t xw_rsrc[kWide ? kXWide : 1];
+    [[maybe_unused]] uint32_t xw_voff[kWide ? kXWide : 1];
+    if constexpr (kWide) {
+        constexpr int kPieces = kXRow / 16;
+        static_assert(TM % (64 / kPieces) == 0, "a wave's pieces are rows or columns");
+#pragma unroll
+        for (int j = 0; j < kXWide; ++j) {
+            const int e0 = (j * NW + wave) * 64, r0 = e0 / kPieces, r = (e0 + lane) / kPieces;
+            xw_rsrc[j] = r0 < TM ? rXa : r0 < TM + TN ? rXb : make_rsrc(nullptr, 0);
+            xw_voff[j] = (r0 < TM ? row_offset<GR>(p, m0, r, (uint32_t)kblk) : (uint32_t)(r - TM) * (uint32_t)kblk) +
+                         16u * (uint32_t)(lane % kPieces);
+        }
+    }
+    [[maybe_unused]] auto copy_wide = [&](int c) {   // stage c: k-tiles c XG .. (bytes past a row's end: unread)
+        if constexpr (kWide) {
+            const uint32_t koff = kbase + (uint32_t)c * (uint32_t)(XG * KT);
+            uint8_t *d = lds + kRing * kBuf + (c & 1) * kWideBytes;
+#pragma unroll
+            for (int j = 0; j < kXWide; ++j)
+                lds_dma16(xw_rsrc[j], d + (j * NW + wave) * 1024, xw_voff[j], kMx4 ? koff / 16u : koff / 128u);
+        }
+    };
+    // k-tile t's scales of tile row (or TM + column) r, wide staging.
+    [[maybe_unused]] auto wide_at = [&](int t, int r) -> const uint8_t * {
+        constexpr int kG = kWide ? XG : 1;
+        return lds + kRing * kBuf + ((t / kG) & 1) * kWideBytes + r * kXRow + (t % kG) * (kMx4 ? 8 : 1);
+    };
+    [[maybe_unused]] uint32_t xw4[kRA + 1];   // mxfp4: the row scale dword of each fragment of the ring
+    [[maybe_unused]] u32x2 xwb4[4];           // and the next k-tile's strips' dwords of both steps
+    [[maybe_unused]] int xw8[kRA + 1];        // mxfp8: the row scale byte of each fragment of the ring
     auto dma_scales = [&](int t, uint32_t koff) {
-        if constexpr (kMx) {
+        if constexpr (kWide) {
+            // (issued by the k-tile a stage begins with, for the stage after it)
+        } else if constexpr (kMx) {
             lds_dma<1>(rXa, xstage(t) + wave * 64, xa_voff, koff / 128u);
             lds_dma<1>(rXb, xstage(t) + 256 + wave * 64, xb_voff, koff / 128u);
         } else if constexpr (kMx4) {
@@ -305,7 +384,15 @@ gemm_w4_kernel(const GemmArgs args)
     [[maybe_unused]] int eb4[4][2];            // mxfp4: this k-tile's column scale bytes [strip][step]
     [[maybe_unused]] const uint32_t xsh = 8u * (uint32_t)(lane >> 4);   // mxfp4: this lane's byte of a dword
     auto read_xb = [&](int t) {
-        if constexpr (kMx) {
+        if constexpr (kWide && kMx) {
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                xb_next[nt] = *wide_at(t, TM + 64 * wave + 16 * nt + (lane & 15));
+        } else if constexpr (kWide) {
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                xwb4[nt] = *reinterpret_cast<const u32x2 *>(wide_at(t, TM + 64 * wave + 16 * nt + (lane & 15)));
+        } else if constexpr (kMx) {
             xb_next = *reinterpret_cast<const i32x4 *>(xstage(t) + 256 + 4 * (wave * 16 + (lane & 15)));
         } else if constexpr (kMx4) {
             const uint32_t *b = xstage(t) + 512 + 8 * (wave * 16 + (lane & 15));
@@ -346,9 +433,13 @@ gemm_w4_kernel(const GemmArgs args)
     auto copy_write = [&](int j, uint32_t st) {
         *reinterpret_cast<i32x4 *>(lds + st + (j * NW + wave) * 1024 + lane * 16) = cp[j];
     };
-    auto read_frag = [&](int f, uint32_t st) {   // fragment f of the tile in stage st
+    auto read_frag = [&](int f, uint32_t st, [[maybe_unused]] int tt) {   // fragment f of tile tt, in stage st
         const int s = f / kMT, mt = f % kMT;
-        if constexpr (kMx) {
+        if constexpr (kWide && kMx) {
+            xw8[f % (kRA + 1)] = *wide_at(tt, 16 * mt + (lane & 15));
+        } else if constexpr (kWide) {
+            xw4[f % (kRA + 1)] = *reinterpret_cast<const uint32_t *>(wide_at(tt, 16 * mt + (lane & 15)) + 4 * s);
+        } else if constexpr (kMx) {
             if (mt % 4 == 0)
                 xq[mt / 4] = *reinterpret_cast<const i32x4 *>(lds + kRing * kBuf + (st / kBuf) * kXStage +
                                                               4 * (16 * (lane & 15) + mt));
@@ -371,6 +462,7 @@ gemm_w4_kernel(const GemmArgs args)
         }
     };
 
+    copy_wide(0);
     // Prologue: copies of tiles 0..kDmaAhead-1, B of tiles 0..DB-1, all
     // landed; then the first kRA fragments of tile 0.  (The register copy
     // loads its last prologue tile into registers: tile 0 writes it.)
@@ -405,14 +497,14 @@ gemm_w4_kernel(const GemmArgs args)
     read_xb(0);
 #pragma unroll
     for (int f = 0; f < kRA; ++f)
-        read_frag(f, stage(0));
+        read_frag(f, stage(0), 0);
     // mxfp4: fragment f's row scale byte, extracted (VALU) one fragment
     // ahead into slot f % 2 -- the hardware-scaled MFMA needs 2 wait states
     // after a vector-ALU write of its scale register, and the extraction sits
     // three MFMAs before the first one that reads it.
     [[maybe_unused]] int ea4v[2] = {0, 0};
     if constexpr (kMx4)
-        ea4v[0] = (int)__builtin_amdgcn_ubfe((uint32_t)xq4[0][0][0], xsh, 8u);
+        ea4v[0] = (int)__builtin_amdgcn_ubfe(kWide ? xw4[0] : (uint32_t)xq4[0][0][0], xsh, 8u);
 
     // One k-tile.  SET = t % kDB holds tile t's B (and receives tile t+kDB's
     // as it is consumed); the wrapped reloads at its start refill set
@@ -435,7 +527,8 @@ gemm_w4_kernel(const GemmArgs args)
                     for (int c = 0; c < kNT; ++c)
 #pragma unroll
                         for (int s2 = 0; s2 < 2; ++s2)
-                            eb4[c][s2] = (int)__builtin_amdgcn_ubfe((uint32_t)xb4_next[c / 2][(c % 2) * 2 + s2], xsh, 8u);
+                            eb4[c][s2] = (int)__builtin_amdgcn_ubfe(
+                                kWide ? xwb4[c][s2] : (uint32_t)xb4_next[c / 2][(c % 2) * 2 + s2], xsh, 8u);
                     // the first MFMA below reads one of these: 2 wait states
                     // after the extractions, in whatever order they issue
                     __builtin_amdgcn_sched_barrier(0);
@@ -460,27 +553,28 @@ gemm_w4_kernel(const GemmArgs args)
             auto next_ea4 = [&]() {   // the next fragment's (that of the next k-tile after the last)
                 if constexpr (kMx4) {
                     const int g = (f + 1) % kFr, st1 = g / kMT, mt1 = g % kMT;
-                    ea4v[(f + 1) & 1] =
-                        (int)__builtin_amdgcn_ubfe((uint32_t)xq4[mt1 / 4][(mt1 % 4) / 2][(mt1 % 2) * 2 + st1], xsh, 8u);
+                    ea4v[(f + 1) & 1] = (int)__builtin_amdgcn_ubfe(
+                        kWide ? xw4[g % (kRA + 1)] : (uint32_t)xq4[mt1 / 4][(mt1 % 4) / 2][(mt1 % 2) * 2 + st1], xsh, 8u);
                 }
             };
             auto mf = [&](int nt) {
                 if constexpr (kMx4)
-                    mfma_acc_mx4(acc[mt][nt], breg[SET][nt][st], a, eb4[nt][st], ea4);
+                    mfma_acc_mx4<kAccV>(acc[mt][nt], breg[SET][nt][st], a, eb4[nt][st], ea4);
                 else if constexpr (DT == kDtypeBf16)
-                    mfma_acc(acc[mt][nt], breg[SET][nt][st], a);
+                    mfma_acc<kAccV>(acc[mt][nt], breg[SET][nt][st], a);
                 else if constexpr (kMx)
-                    mfma_acc_mx(acc[mt][nt], cat(breg[SET][nt][0], breg[SET][nt][1]), a, xb_cur[nt], xq[mt / 4][mt % 4]);
+                    mfma_acc_mx<kAccV>(acc[mt][nt], cat(breg[SET][nt][0], breg[SET][nt][1]), a, xb_cur[nt],
+                                kWide ? xw8[f % (kRA + 1)] : xq[mt / 4][mt % 4]);
                 else
-                    mfma_acc(acc[mt][nt], cat(breg[SET][nt][0], breg[SET][nt][1]), a);
+                    mfma_acc<kAccV>(acc[mt][nt], cat(breg[SET][nt][0], breg[SET][nt][1]), a);
             };
             auto lds_read = [&]() {
                 if (f == kBar)   // past the barrier: the next k-tile's column scales
                     read_xb(t + 1);
                 if (f + kRA < kFr)
-                    read_frag(f + kRA, cur);
+                    read_frag(f + kRA, cur, t);
                 else
-                    read_frag(f + kRA - kFr, nx1);
+                    read_frag(f + kRA - kFr, nx1, t + 1);
             };
             auto b_loads = [&]() {
 #pragma unroll
@@ -496,6 +590,9 @@ gemm_w4_kernel(const GemmArgs args)
                 }
             };
             auto a_copies = [&]() {
+                if constexpr (kWide)
+                    if (f == kBar && t % XG == 0 && t + XG < ntiles)
+                        copy_wide(t / XG + 1);
 #pragma unroll
                 for (int j = 0; j < kDma; ++j) {
                     if constexpr (SYNC) {
@@ -592,6 +689,19 @@ gemm_w4_kernel(const GemmArgs args)
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (GR != 0) {
+        // The fences order instructions, not the values: naming the
+        // accumulators here keeps every use of them behind the wait.
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+                if constexpr (kAccV)
+                    asm volatile("" : "+v"(acc[i][j]));
+                else
+                    asm volatile("" : "+a"(acc[i][j]));
+            }
+    }
 
     float scale = 1.0f;
     if constexpr (SCALE == kScaleTensor)
@@ -658,10 +768,10 @@ gemm_w4_kernel(const GemmArgs args)
     }
 }
 
-template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM, int GR = 0>
+template <int DT, int SCALE, int OUT, int DB, int SWZ, int RA, int ILV, int SYNC, int WM, int TM, int GR = 0, int XG = 0>
 void launch_w4(const GemmArgs &a, dim3 grid, hipStream_t s)
 {
-    gemm_w4_kernel<DT, SCALE, OUT, DB, SWZ, RA, ILV, SYNC, WM, TM, GR><<<grid, 256, 0, s>>>(a);
+    gemm_w4_kernel<DT, SCALE, OUT, DB, SWZ, RA, ILV, SYNC, WM, TM, GR, XG><<<grid, 256, 0, s>>>(a);
 }
 
 // Table entries: waves (WM x 4/WM), preload pair = (ILV, RA), layout, copy path.
@@ -715,14 +825,27 @@ static const KernelSpec kW4Kernels[] = {
     DGP_W4T(kDtypeFp8, kScaleTensor, kOutBf16, 2, 1, 3, 1, 0, 1, 128),
 };
 
-// Product grouped by expert: the tuned form of each tile.
-#define DGP_W4G(DT, SC, DB, RA, TM)                                                            \
+// Product grouped by expert: B k-tiles in flight, LDS read-ahead, tile rows,
+// wide scale staging.  64 rows (two workgroups per CU): B three k-tiles deep,
+// as a k-tile is a quarter of the 256-row tile's (785 against 907 us bf16, 225
+// against 268 us mxfp4, for the interleaved tile of gemm_tiled.hip; 32 experts
+// x 250 rows, N 4096, K 7168; four deep: 1-4 % slower).  Wide staging against
+// staging per k-tile, 256 rows: mxfp4 526 against 595 us, mxfp8 770 against 858
+// us (1000 rows; mxfp4 with B three deep 520, but 372 against 362 us at N 7168,
+// K 2048); 128 rows against the interleaved tile: mxfp8 320 against 389, mxfp4
+// 215 against 232 us (250 rows).
+#define DGP_W4G(DT, SC, DB, RA, TM, XG, KMULT)                                                 \
     {kTiled, DT, SC, kOutBf16, TM, 256, 128, 4, 1, 4, 1, RA, DB, kSchedW4,                      \
-     &launch_w4<DT, SC, kOutBf16, DB, 1, RA, 1, 0, 1, TM, 1>, kLaySwizzled, kCopyAsync}
+     &launch_w4<DT, SC, kOutBf16, DB, 1, RA, 1, 0, 1, TM, 1, XG>, kLaySwizzled, kCopyAsync, KMULT}
 static const KernelSpec kW4Grouped[] = {
-    DGP_W4G(kDtypeBf16, kScaleNone, 3, w4::kRA, 256),   DGP_W4G(kDtypeFp8, kScaleTensor, 3, w4::kRA, 256),
-    DGP_W4G(kDtypeFp8, kScaleMx, 3, w4::kRA, 256),      DGP_W4G(kDtypeFp4, kScaleMx32, 3, w4::kRA, 256),
-    DGP_W4G(kDtypeBf16, kScaleNone, 2, 7, 128),         DGP_W4G(kDtypeFp8, kScaleTensor, 2, 1, 128),
+    DGP_W4G(kDtypeBf16, kScaleNone, 3, w4::kRA, 256, 0, 0), DGP_W4G(kDtypeFp8, kScaleTensor, 3, w4::kRA, 256, 0, 0),
+    DGP_W4G(kDtypeFp8, kScaleMx, 3, w4::kRA, 256, 16, 512), DGP_W4G(kDtypeFp4, kScaleMx32, 2, 7, 256, 4, 0),
+    DGP_W4G(kDtypeBf16, kScaleNone, 2, 7, 128, 0, 0),       DGP_W4G(kDtypeFp8, kScaleTensor, 2, 1, 128, 0, 0),
+    DGP_W4G(kDtypeFp8, kScaleMx, 2, 1, 128, 16, 512),       DGP_W4G(kDtypeFp4, kScaleMx32, 2, 7, 128, 4, 0),
+    DGP_W4G(kDtypeBf16, kScaleNone, 3, 3, 64, 0, 0),        DGP_W4G(kDtypeFp8, kScaleTensor, 3, 1, 64, 0, 0),
+    DGP_W4G(kDtypeFp8, kScaleMx, 3, 1, 64, 16, 512),        DGP_W4G(kDtypeFp4, kScaleMx32, 3, 3, 64, 4, 0),
+    // mxfp8 rows of scales that are not whole dwords (K % 512 != 0)
+    DGP_W4G(kDtypeFp8, kScaleMx, 3, w4::kRA, 256, 0, 0),
 };
 
 const KernelSpec *w4_grouped_kernels(int *count)

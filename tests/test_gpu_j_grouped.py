@@ -10,6 +10,7 @@ from operand_common import EPS, MODES, dequantize, pow2
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+E4M3 = ("tensor", "block128", "mx128")
 
 TILES = {mode: [(16, 16), (16, 32), (16, 64), (64, 64), (64, 128), (64, 256), (128, 256), (256, 256)] for mode in MODES}
 
@@ -89,13 +90,23 @@ def run(mode, counts, n, k, seed, tile=None, gather=False, lead=0, pad=0, remap=
                                     config=config(tile, remap, group_m))
     torch.cuda.synchronize()
     assert C is out
-    check(C, before, ad, bd, offsets, rows, k)
+    check(C, before, ad, bd, offsets, rows, k, aligned_loss if mode in E4M3 else None)
 
 
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("mode,tile", [(m, t) for m, ts in TILES.items() for t in ts])
 def test_every_tile(mode, tile, gather):
     run(mode, [5, 0, 33, 1, 300, 0, 17], 384, 1024, 7, tile, gather, lead=3, pad=6)
+
+
+@pytest.mark.parametrize("tile", [(64, 64), (64, 128), (64, 256), (128, 256), (256, 256)])
+@pytest.mark.parametrize("mode,k", [("mx128", 128), ("mx128", 640), ("mx128", 1152), ("mx128", 1536), ("mx128", 3584),
+                                    ("mx32", 256), ("mx32", 768), ("mx32", 1280), ("none", 64), ("none", 192),
+                                    ("tensor", 128), ("tensor", 384), ("block128", 128), ("block128", 640)])
+def test_k_lengths(mode, k, tile):
+    """One k-tile, odd numbers of them, scale rows that are not whole dwords
+    (mxfp8, K % 512 != 0), and scale stages that end past the row's last byte."""
+    run(mode, [37, 0, 70, 200], 384, k, 47, tile, gather=k % 256 == 128)
 
 
 @pytest.mark.parametrize("mode", list(MODES))
@@ -132,7 +143,7 @@ def test_matches_the_single_product():
     for mode in MODES:
         A, sA, Bs, sB, _, _ = operands(mode, 300, 1, 256, 1024, 23)
         off = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
-        cfg = dict(tile_m=256, tile_n=256, tile_k=128, xcd_remap=1, group_m=8, schedule=1 if mode == "block128" else 4)
+        cfg = dict(tile_m=256, tile_n=256, tile_k=128, xcd_remap=1, group_m=8)
         C = dgp.gemm_preshuffle_grouped(A, Bs, off, sA, sB, MODES[mode], config=cfg)
         D = dgp.gemm_preshuffle(A, Bs[0], sA, sB, MODES[mode], config=cfg)
         assert torch.equal(C.view(torch.int16), D.view(torch.int16)), mode
@@ -228,7 +239,7 @@ def test_mixture_of_experts_layer(mode, tokens):
     worst = {"none": 2.0 ** -8, "block128": 2.0 ** -4, "mx128": 2.0 ** -4, "mx32": 2.0 ** -2}[mode]
     assert float((ad - y).norm() / y.norm()) <= worst
     C1 = dgp.gemm_preshuffle_grouped(A, B1, off, sA, s1, MODES[mode], rows=rows.to(DEV))
-    loss = aligned_loss if mode in ("block128", "mx128") else None
+    loss = aligned_loss if mode in E4M3 else None
     check(C1, C1.cpu(), ad, bd1, offsets, rows.long(), hidden, loss)
     A2, sA2 = dgp.swiglu_quantize(C1[:, :inner], C1[:, inner:], MODES[mode])
     c1 = C1.cpu().double()
