@@ -722,8 +722,13 @@ dgp_status run_grouped(const GemmCall &c, const Experts &x, hipStream_t stream)
     if (!spec)
         return fail(DGP_ERR_CONFIG, "no compiled grouped kernel fits this shape");
     const int64_t tiles_m = most_row_tiles(c.M, x.E, spec->tm), tiles_n = (c.N + spec->tn - 1) / spec->tn;
-    if (tiles_m * tiles_n > INT32_MAX)
-        return fail(DGP_ERR_SHAPE, "grid of %lld workgroups too large", (long long)(tiles_m * tiles_n));
+    // a launch's threads fit 32 bits, and so do the sums of the search for a
+    // tile: 64 experts at a time, of which offsets that break the rule may give
+    // each all M rows
+    const int64_t scanned = std::min<int64_t>(x.E, 64) * ((c.M + spec->tm - 1) / spec->tm) + tiles_m;
+    if (tiles_m * tiles_n > UINT32_MAX / (spec->waves * 64) || scanned > INT32_MAX)
+        return fail(DGP_ERR_SHAPE, "M=%lld rows and N=%lld columns make too many %d x %d tiles", (long long)c.M,
+                    (long long)c.N, spec->tm, spec->tn);
     DGP_TRY(check_device_arch());
     GemmArgs a{};
     a.A = (const uint8_t *)c.A, a.Bs = (const uint8_t *)c.Bs, a.C = c.C;
@@ -827,6 +832,41 @@ dgp_status check_codes(const void *Q, const void *S, const float *scale, int sca
     return DGP_OK;
 }
 
+// An output of M dense rows of out_row bytes against an input of M rows of
+// in_row bytes, in_ld bytes apart: apart in memory, or (may_be_same: kernels
+// that read a row's elements before the same threads write them) the same
+// dense rows.
+dgp_status check_apart(const void *out, int64_t out_row, const void *in, int64_t in_row, int64_t in_ld, int64_t M,
+                       bool may_be_same, const char *what)
+{
+    if (!out || !in || (may_be_same && out == in && out_row == in_row && (M == 1 || in_ld == in_row)))
+        return DGP_OK;
+    const uintptr_t o = (uintptr_t)out, i = (uintptr_t)in;
+    if (o < i + (uintptr_t)((M - 1) * in_ld + in_row) && i < o + (uintptr_t)(M * out_row))
+        return fail(DGP_ERR_SHAPE, "%s overlap", what);
+    return DGP_OK;
+}
+
+// Bytes of a row of codes and of its scales (0 where a row has none).
+int64_t code_row(int64_t K, int scale_mode)
+{
+    return scale_mode == DGP_SCALE_NONE ? 2 * K : scale_mode == DGP_SCALE_MX32 ? K / 2 : K;
+}
+int64_t scale_row(int64_t K, int scale_mode)
+{
+    return scale_mode == DGP_SCALE_BLOCK128 ? K / 128 * 4 : scale_mode == DGP_SCALE_MX128 ? K / 128
+           : scale_mode == DGP_SCALE_MX32 ? K / 32 : 0;
+}
+
+// Q and S of an operand against one of its strided inputs.
+dgp_status check_codes_apart(const void *Q, const void *S, int scale_mode, const void *X, int64_t ldx, int x_type,
+                             int64_t M, int64_t K, const char *what)
+{
+    const int64_t in = input_size(x_type);
+    DGP_TRY(check_apart(Q, code_row(K, scale_mode), X, K * in, ldx * in, M, x_type == DGP_BF16, what));
+    return check_apart(scale_row(K, scale_mode) ? S : nullptr, scale_row(K, scale_mode), X, K * in, ldx * in, M, false, what);
+}
+
 dgp_status check_amax_workspace(int64_t groups, const float *ws, size_t ws_bytes)
 {
     const size_t need = dgp_quantize_workspace_bytes(groups, DGP_SCALE_TENSOR);
@@ -912,6 +952,7 @@ dgp_status dgp_quantize(const void *X, int64_t ldx, int x_type, void *Q, void *S
     const bool measure = scale_mode == DGP_SCALE_TENSOR && !scale;
     if (measure)
         DGP_TRY(check_amax_workspace(1, ws, ws_bytes));
+    DGP_TRY(check_codes_apart(Q, S, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = X, a.Q = Q, a.S = S, a.scale = scale;
@@ -946,6 +987,7 @@ dgp_status dgp_quantize_b(const void *B, int x_type, void *Bs, void *sB, int64_t
     const bool measure = scale_mode == DGP_SCALE_TENSOR;
     if (measure)
         DGP_TRY(check_amax_workspace(E, ws, ws_bytes));
+    DGP_TRY(check_codes_apart(Bs, sB, scale_mode, B, K, x_type, E * N, K, "B and Bs or sB"));
     DGP_TRY(check_device_arch());
     WeightQuantArgs a{};
     a.B = B, a.Q = Bs, a.S = sB;
@@ -980,6 +1022,12 @@ dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64
     if (scale_mode == DGP_SCALE_TENSOR && !scale)
         return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
     DGP_TRY(check_codes(Q, S, scale, scale_mode));
+    DGP_TRY(check_codes_apart(Q, S, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
+    DGP_TRY(check_codes_apart(Q, S, scale_mode, R, ldr, x_type, M, K, "residual and Q or S"));
+    const int64_t in = input_size(x_type);
+    DGP_TRY(check_apart(H, K * in, X, K * in, ldx * in, M, true, "X and residual output"));
+    DGP_TRY(check_apart(H, K * in, R, K * in, ldr * in, M, true, "residual and residual output"));
+    DGP_TRY(check_apart(H, K * in, Q, code_row(K, scale_mode), code_row(K, scale_mode), M, false, "Q and residual output"));
     DGP_TRY(check_device_arch());
     NormArgs a{};
     a.X = X, a.R = R, a.W = W, a.Q = Q, a.S = S, a.H = H, a.scale = scale;
@@ -999,6 +1047,8 @@ dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_
     if (scale_mode == DGP_SCALE_TENSOR && !scale)
         return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
     DGP_TRY(check_codes(Q, S, scale, scale_mode));
+    DGP_TRY(check_codes_apart(Q, S, scale_mode, G, ldg, x_type, M, K, "gate and Q or S"));
+    DGP_TRY(check_codes_apart(Q, S, scale_mode, U, ldu, x_type, M, K, "up and Q or S"));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = G, a.U = U, a.Q = Q, a.S = S, a.scale = scale;

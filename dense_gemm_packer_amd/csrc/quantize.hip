@@ -730,22 +730,46 @@ hipError_t launch_quantize_b(const WeightQuantArgs &a, int x_type, int mode, hip
     }
 }
 
+template <int XT, int MODE, int T, int C>
+static void launch_norm_rows(const NormArgs &a, hipStream_t s)
+{
+    constexpr int kThreads = T < 256 ? 256 : T, kRows = kThreads / T;
+    constexpr int kIn = XT == kTypeF32 ? 4 : 2;
+    // Slabs of rows whose threads fit the 32 bits of a launch.
+    constexpr int64_t slab = (int64_t(1) << 31) / T;
+    const int64_t qrow = MODE == kScaleNone ? 2 * a.K : MODE == kScaleMx32 ? a.K / 2 : a.K;
+    const int64_t srow = MODE == kScaleBlock ? a.K / 128 * 4 : MODE == kScaleMx ? a.K / 128 : MODE == kScaleMx32 ? a.K / 32 : 0;
+    for (int64_t r = 0; r < a.M; r += slab) {
+        NormArgs b = a;
+        b.M = a.M - r < slab ? a.M - r : slab;
+        b.X = static_cast<const uint8_t *>(a.X) + r * a.ldx * kIn;
+        if (a.R)
+            b.R = static_cast<const uint8_t *>(a.R) + r * a.ldr * kIn;
+        if (a.H)
+            b.H = static_cast<uint8_t *>(a.H) + r * a.K * kIn;
+        b.Q = static_cast<uint8_t *>(a.Q) + r * qrow;
+        if (srow)
+            b.S = static_cast<uint8_t *>(a.S) + r * srow;
+        rmsnorm_kernel<XT, MODE, T, C><<<(unsigned)((b.M + kRows - 1) / kRows), kThreads, 0, s>>>(b);
+    }
+}
+
 template <int XT, int MODE>
 static void launch_norm(const NormArgs &a, hipStream_t s)
 {
     const int64_t k8 = a.K / 8;
     if (k8 <= 64)
-        rmsnorm_kernel<XT, MODE, 64, 1><<<(unsigned)((a.M + 3) / 4), 256, 0, s>>>(a);
+        launch_norm_rows<XT, MODE, 64, 1>(a, s);
     else if (k8 <= 256)
-        rmsnorm_kernel<XT, MODE, 64, 4><<<(unsigned)((a.M + 3) / 4), 256, 0, s>>>(a);
+        launch_norm_rows<XT, MODE, 64, 4>(a, s);
     else if (k8 <= 1024 && a.M > 512)
-        rmsnorm_kernel<XT, MODE, 256, 4><<<(unsigned)a.M, 256, 0, s>>>(a);
+        launch_norm_rows<XT, MODE, 256, 4>(a, s);
     else if (k8 <= 1024)
-        rmsnorm_kernel<XT, MODE, 1024, 1><<<(unsigned)a.M, 1024, 0, s>>>(a);
+        launch_norm_rows<XT, MODE, 1024, 1>(a, s);
     else if (k8 <= 4096)
-        rmsnorm_kernel<XT, MODE, 1024, 4><<<(unsigned)a.M, 1024, 0, s>>>(a);
+        launch_norm_rows<XT, MODE, 1024, 4>(a, s);
     else
-        rmsnorm_kernel<XT, MODE, 1024, 0><<<(unsigned)a.M, 1024, 0, s>>>(a);
+        launch_norm_rows<XT, MODE, 1024, 0>(a, s);
 }
 
 hipError_t launch_rmsnorm(const NormArgs &a, int x_type, int mode, hipStream_t s)

@@ -345,7 +345,9 @@ dgp_status dgp_gemm_preshuffle_grouped(const void *A, int64_t a_rows, const void
  * Inputs are rows ld* elements apart (ld* >= K), each 16-byte aligned; Q, S
  * and H are dense.  K as the product takes it: rows of Q a multiple of 128
  * bytes, at most 2^23.  M = 0 or K = 0 is a no-op (no scale is written: such
- * a product reads none).
+ * a product reads none).  Outputs that overlap an input are refused
+ * (DGP_ERR_SHAPE), but for an update in place: Q (bf16) or H that is an input
+ * itself, with dense rows of the same type.
  */
 
 /* Bytes of workspace that dgp_quantize (E = 1) and dgp_quantize_b need: 1 KiB
@@ -368,8 +370,8 @@ dgp_status dgp_quantize_b(const void *B, int x_type, void *Bs, void *sB, int64_t
 
 /* dgp_rmsnorm_quantize -- h = x + r (r: the residual's rows, or R NULL: h = x),
  * y = h / sqrt(mean(h^2) + eps) * w over each row; Q, S from y.  H, where not
- * NULL, receives h rounded to x_type ([M][K]; y comes from the unrounded sum);
- * it may be X or R itself where their rows are dense (an update in place).
+ * NULL, receives h rounded to x_type ([M][K]; y comes from the unrounded sum).
+ * The squares are summed in fp32: beyond 3.4e38 (values of about 1e19) y is 0.
  * w has K values of x_type or DGP_F32.  DGP_SCALE_TENSOR takes a given scale. */
 dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64_t ldr, int x_type, const void *W,
                                 int w_type, float eps, void *Q, void *S, const float *scale, void *H, int64_t M,

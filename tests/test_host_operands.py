@@ -193,6 +193,39 @@ def test_binding_follows_the_active_library(dgp):
     assert dgp._bound is dgp.lib()
 
 
+Z = 0x40000000       # a second one, far from the first
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(Q=P + 2032), dict(Q=Z, S=P + 2044), dict(Q=Z, S=Z + 4096, X=Z + 496, M=2, ldx=1024),
+])
+def test_quantize_refuses_overlap(L, kw):
+    """Q or S inside X's rows, from its first byte to its last."""
+    assert quantize(L, **kw) == SHAPE and b"overlap" in L.dgp_last_error()
+
+
+def test_quantize_b_refuses_overlap(L):
+    assert quantize_b(L, Bs=P, sB=Z) == SHAPE and quantize_b(L, Bs=Z, sB=P + 16) == SHAPE
+    assert b"overlap" in L.dgp_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(Q=P), dict(S=P + 64), dict(R=P + 0x8000, ldr=256, Q=P + 0x8000), dict(H=P + 512), dict(H=P, ldx=512),
+    dict(H=P, ldx=512, M=1, Q=P), dict(R=P + 0x8000, ldr=512, H=P + 0x8000), dict(H=Z + 512), dict(H=P, Q=P, mode=NONE),
+    dict(Q=P, mode=NONE, xt=F16, wt=F16), dict(Q=P + 512, mode=NONE),
+])
+def test_rmsnorm_refuses_overlap(L, kw):
+    """A shifted or differently strided output, the scales, or Q over the residual output."""
+    base = dict(X=P, W=Z + 0x100000, Q=Z, S=Z + 0x10000)
+    assert norm(L, **{**base, **kw}) == SHAPE and b"overlap" in L.dgp_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(Q=P), dict(Q=P, ldg=256, ldu=256, U=P + 512 * 4, M=5, mode=NONE), dict(S=P + 1024), dict(Q=P, mode=NONE)])
+def test_swiglu_refuses_overlap(L, kw):
+    base = dict(G=P, U=P + 512, Q=Z, S=Z + 0x10000)
+    assert swiglu(L, **{**base, **kw}) == SHAPE and b"overlap" in L.dgp_last_error()
+
+
 def grouped(L, A=P, a_rows=64, Bs=P, C=P, M=64, N=128, K=256, E=4, offsets=P, rows=None, dtype=FP8, mode=MX, sA=P, sB=P,
             cfg=None):
     return L.dgp_gemm_preshuffle_grouped(A, a_rows, Bs, C, M, N, K, E, offsets, rows, dtype, mode, sA, sB, cfg, None)
@@ -217,6 +250,11 @@ def test_grouped_configurations(L, dgp):
                 dict(tile_m=256, tile_n=256, tile_k=128, schedule=3), dict(tile_m=256, tile_n=256, tile_k=64)):
         c = dgp.Config(**cfg)
         assert grouped(L, cfg=ctypes.byref(c)) == CONFIG, cfg
+    # too many threads for one launch; too many tiles for the search's sums
+    small = ctypes.byref(dgp.Config(tile_m=16, tile_n=16))
+    assert grouped(L, M=1 << 22, a_rows=1 << 22, N=1 << 14, cfg=small) == SHAPE
+    assert grouped(L, M=1 << 29, a_rows=1 << 29, N=16, E=64, cfg=small) == SHAPE
+    assert b"tiles" in L.dgp_last_error()
     assert grouped(L, M=0, A=None, Bs=None, C=None, offsets=None) == OK
     assert grouped(L, E=0, A=None, Bs=None, C=None, offsets=None) == OK
 
