@@ -987,7 +987,10 @@ dgp_status dgp_quantize_b(const void *B, int x_type, void *Bs, void *sB, int64_t
     const bool measure = scale_mode == DGP_SCALE_TENSOR;
     if (measure)
         DGP_TRY(check_amax_workspace(E, ws, ws_bytes));
-    DGP_TRY(check_codes_apart(Bs, sB, scale_mode, B, K, x_type, E * N, K, "B and Bs or sB"));
+    const int64_t b_row = K * input_size(x_type), scales = scale_mode == DGP_SCALE_BLOCK128 ? E * (N / 128) * (K / 128) * 4
+                          : measure ? E * 4 : E * N * scale_row(K, scale_mode);
+    DGP_TRY(check_apart(Bs, code_row(K, scale_mode), B, b_row, b_row, E * N, false, "B and Bs"));
+    DGP_TRY(check_apart(sB, scales, B, E * N * b_row, E * N * b_row, 1, false, "B and sB"));
     DGP_TRY(check_device_arch());
     WeightQuantArgs a{};
     a.B = B, a.Q = Bs, a.S = sB;

@@ -3,13 +3,15 @@
 // __init__.py): argument checks, allocation of the outputs and the call of the
 // C ABI, in one step.  A decode step makes many of these calls on a few rows
 // each, where the kernel takes 2-4 us: with the checks and allocations in
-// Python a call cost 7-9 us on the host.
+// Python a call cost 7-9 us on the host.  Here quantize takes 4.0 us and the
+// norm, with its three outputs, 4.6, of which the launch is 2.9.
 //
 // The C ABI is called through addresses that bind() receives, so the module
 // follows a switch of the active library, and its status codes go to the
 // Python function that raises DgpError.
 #include <Python.h>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
@@ -211,9 +213,14 @@ private:
     void *handle_ = nullptr;
 };
 
+// From the allocator that at::empty takes for this kind of device, without the
+// dispatcher's way to it: 0.2 us an output, not 0.6 (the device and stream are
+// those Place has made current).
 Tensor empty(at::IntArrayRef shape, ScalarType dtype, const Tensor &X)
 {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(X.device()));
+    static c10::Allocator *const allocator =
+        at::empty({1}, at::TensorOptions().dtype(ScalarType::Byte).device(X.device())).storage().allocator();
+    return at::detail::empty_generic(shape, allocator, c10::DispatchKeySet(c10::DispatchKey::CUDA), dtype, std::nullopt);
 }
 
 template <class Fn, class... Args>

@@ -55,6 +55,25 @@ def test_gate_onto_its_input():
         assert same(Q, want)
 
 
+@pytest.mark.parametrize("mode", ["tensor", "block128", "mx128", "mx32"])
+def test_outputs_right_beside_the_input(mode):
+    """Codes and scales in one buffer with the input, on either side of it."""
+    e, n, k = 2, 128, 512
+    b = rows(e * n, k, torch.bfloat16, 80).to(DEV).view(e, n, k)
+    wq, ws = dgp.quantize_b(b, MODES[mode])
+    nq, ns, nb = (t.numel() * t.element_size() for t in (wq, ws, b))
+    pad = -ns % 16
+    buf = torch.zeros(nq + pad + ns + nb + nq + ns, dtype=torch.uint8, device=DEV)
+    start = nq + pad + ns
+    inside = buf[start:start + nb].view(torch.bfloat16).view(e, n, k)
+    inside.copy_(b)
+    for q0, s0 in ((0, nq + pad), (start + nb, start + nb + nq)):
+        q = buf[q0:q0 + nq].view(wq.dtype).view(wq.shape)
+        s = buf[s0:s0 + ns].view(ws.dtype).view(ws.shape)
+        dgp.quantize_b(inside, MODES[mode], out=q, scales=s)
+        assert same(q, wq) and same(s, ws) and same(inside, b)
+
+
 # ------------------------------------------------------ sizes past 32 bits
 
 def test_more_pieces_than_a_launch_counts():

@@ -206,6 +206,7 @@ def test_quantize_refuses_overlap(L, kw):
 
 def test_quantize_b_refuses_overlap(L):
     assert quantize_b(L, Bs=P, sB=Z) == SHAPE and quantize_b(L, Bs=Z, sB=P + 16) == SHAPE
+    assert quantize_b(L, Bs=Z, sB=P - 4) == SHAPE    # (two values)
     assert b"overlap" in L.dgp_last_error()
 
 
