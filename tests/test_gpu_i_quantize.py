@@ -229,6 +229,19 @@ def test_rmsnorm(x_type, mode, m, k, res, w32):
         assert len(got) == 2
 
 
+@pytest.mark.parametrize("mode", ["none", "mx128"])
+@pytest.mark.parametrize("m,k", [(3, 512), (5, 640), (8193, 1024), (9, 2048), (7, 4096), (1030, 3968), (384, 4224),
+                                 (385, 8192), (2, 8320)])
+def test_rmsnorm_row_splits(mode, m, k):
+    """Every split of a row over threads and pieces, full and with threads left over."""
+    x, r = (rows(m, k, torch.bfloat16, s, spread=1.0) for s in (27, 28))
+    w = (1 + 0.2 * torch.randn(k, generator=torch.Generator().manual_seed(29))).bfloat16()
+    Q, S, H = dgp.rmsnorm_quantize(x.to(DEV), w.to(DEV), MODES[mode], residual=r.to(DEV), eps=1e-5)
+    h, y = norm_reference(x, r, w, 1e-5)
+    check_operand(Q, S, y, mode, norm_delta(k))
+    assert bool(((H.cpu().double() - h).abs() <= h.abs() * (2.0 ** -8 + EPS) + 2.0 ** -133).all())
+
+
 @pytest.mark.parametrize("k", [256, 1024, 7168, 40960])
 def test_rmsnorm_in_place_and_strided(k):
     m = 4
