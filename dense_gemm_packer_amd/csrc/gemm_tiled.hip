@@ -409,12 +409,15 @@ gemm_tiled_kernel(const GemmArgs args)
         }
     };
 
-    auto step = [&](auto setc, int t) {
+    auto step = [&](auto setc, int t, auto tailc) {
         // This wave's A copy of tile t has landed once at most kAfter loads are
-        // outstanding, and every earlier LDS read has completed; the barrier
+        // outstanding (less the B reloads of the `tail` steps behind the loop
+        // before this one: nothing reads those sets, and the compiler drops
+        // the loads), and every earlier LDS read has completed; the barrier
         // certifies both for all waves, so tile t is readable and the buffer
         // of tile t-1 is free for tile t+DEPTH.
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAfter) : "memory");
+        constexpr int kWait = kAfter - decltype(tailc)::value * S::kBLoads;
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kWait) : "memory");
         const uint32_t knext = kofs(t + DEPTH);
         dma_a(nxt, knext);
         if constexpr (kWide)
@@ -520,24 +523,25 @@ gemm_tiled_kernel(const GemmArgs args)
     // Main loop, unrolled by DEPTH so that the B register set of every step is
     // a compile-time index; the remaining ntiles % DEPTH steps follow.
     int t = 0;
+    constexpr std::integral_constant<int, 0> kNone{};
     for (; t + DEPTH <= ntiles; t += DEPTH) {
-        step(std::integral_constant<int, 0>{}, t);
+        step(std::integral_constant<int, 0>{}, t, kNone);
         if constexpr (DEPTH > 1)
-            step(std::integral_constant<int, (DEPTH > 1 ? 1 : 0)>{}, t + 1);
+            step(std::integral_constant<int, (DEPTH > 1 ? 1 : 0)>{}, t + 1, kNone);
         if constexpr (DEPTH > 2)
-            step(std::integral_constant<int, (DEPTH > 2 ? 2 : 0)>{}, t + 2);
+            step(std::integral_constant<int, (DEPTH > 2 ? 2 : 0)>{}, t + 2, kNone);
         if constexpr (DEPTH > 3)
-            step(std::integral_constant<int, (DEPTH > 3 ? 3 : 0)>{}, t + 3);
+            step(std::integral_constant<int, (DEPTH > 3 ? 3 : 0)>{}, t + 3, kNone);
     }
     if constexpr (DEPTH > 1)
         if (t < ntiles)
-            step(std::integral_constant<int, 0>{}, t++);
+            step(std::integral_constant<int, 0>{}, t++, kNone);
     if constexpr (DEPTH > 2)
         if (t < ntiles)
-            step(std::integral_constant<int, (DEPTH > 2 ? 1 : 0)>{}, t++);
+            step(std::integral_constant<int, (DEPTH > 2 ? 1 : 0)>{}, t++, std::integral_constant<int, 1>{});
     if constexpr (DEPTH > 3)
         if (t < ntiles)
-            step(std::integral_constant<int, (DEPTH > 3 ? 2 : 0)>{}, t++);
+            step(std::integral_constant<int, (DEPTH > 3 ? 2 : 0)>{}, t++, std::integral_constant<int, 2>{});
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // Epilogue: scale once, round once.  The per-tensor scales are loaded

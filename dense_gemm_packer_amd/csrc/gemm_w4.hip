@@ -88,14 +88,17 @@ struct Plan {
     // Loads issued after the last copy of tile t+1 (in tile t+1-kDmaAhead)
     // up to the barrier of tile t+1 (tile t, fragment kBar).  Within a
     // fragment position the B reloads precede the copies.
-    static constexpr int vm_at_barrier()
+    // `tail`: the last `tail` k-tiles up to t (those behind the unrolled loop)
+    // reload no B: nothing reads those sets, so the compiler drops the loads.
+    static constexpr int vm_at_barrier(int tail)
     {
         int n = 0;
         for (int i = 0; i < kBLoads; ++i)   // the copies' tile, after its last copy
-            n += bload_pos(i) > dma_pos(kDma - 1) ? 1 : 0;
-        n += (kDmaAhead - 2) * (kDma + kBLoads);   // whole k-tiles in between
+            n += tail < kDmaAhead && bload_pos(i) > dma_pos(kDma - 1) ? 1 : 0;
+        for (int u = 1; u < kDmaAhead - 1; ++u)   // whole k-tiles in between: t - u
+            n += kDma + (tail <= u ? kBLoads : 0);
         for (int i = 0; i < kBLoads; ++i)   // tile t before the barrier
-            n += bload_pos(i) < kBar ? 1 : 0;
+            n += tail == 0 && bload_pos(i) < kBar ? 1 : 0;
         for (int j = 0; j < kDma; ++j)
             n += dma_pos(j) < kBar ? 1 : 0;
         return n;
@@ -233,7 +236,7 @@ gemm_w4_kernel(const GemmArgs args)
     // 2 (mxfp8) or 4 (mxfp4) more loads per k-tile (those of the barrier's
     // own tile precede its last A copy).
     constexpr int kXCopies = kWide ? 0 : kMx ? 2 : kMx4 ? 4 : 0;
-    constexpr int kVm = P::vm_at_barrier() + kXCopies * (kDmaAhead - 2);
+    constexpr int kVm = P::vm_at_barrier(0) + kXCopies * (kDmaAhead - 2);
     static_assert(kVm <= 63, "vmcnt field is 6 bits");
     // One LDS object (the A ring, then for mxfp8 the scale stages): the
     // compiler's wait insertion keeps the async copies and the LDS reads of
@@ -509,8 +512,10 @@ gemm_w4_kernel(const GemmArgs args)
     // One k-tile.  SET = t % kDB holds tile t's B (and receives tile t+kDB's
     // as it is consumed); the wrapped reloads at its start refill set
     // (t-1) % kDB with tile t-1+kDB.
-    auto tile = [&](auto setc, int t) {
+    auto tile = [&](auto setc, int t, auto tailc) {
         constexpr int SET = decltype(setc)::value;
+        constexpr int kWait = P::vm_at_barrier(decltype(tailc)::value) + kXCopies * (kDmaAhead - 2);
+        static_assert(kWait <= kVm, "");
         constexpr int PREV = (SET + kDB - 1) % kDB;
         const uint32_t cur = stage(t), nx1 = stage(t + 1), nx3 = stage(t + kDmaAhead);
         const uint32_t k_prev = kofs(t - 1 + kDB), k_this = kofs(t + kDB), k_dma = kofs(t + kDmaAhead);
@@ -540,7 +545,7 @@ gemm_w4_kernel(const GemmArgs args)
                 if constexpr (SYNC)   // this wave's LDS writes of tile t+1 (and earlier) are done
                     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 else                  // this wave's async copy of tile t+1 has landed
-                    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kVm) : "memory");
+                    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kWait) : "memory");
             }
             // The fragment's 4 MFMAs with one slot of other work between each
             // two (one wave per SIMD issues in order: work bunched between
@@ -667,22 +672,23 @@ gemm_w4_kernel(const GemmArgs args)
     // Main loop unrolled by DB (the B set of every k-tile is a compile-time
     // index); the remaining ntiles % DB k-tiles follow.
     int t = 0;
+    constexpr std::integral_constant<int, 0> kLoop{};
     for (; t + DB <= ntiles; t += DB) {
-        tile(std::integral_constant<int, 0>{}, t);
-        tile(std::integral_constant<int, 1>{}, t + 1);
+        tile(std::integral_constant<int, 0>{}, t, kLoop);
+        tile(std::integral_constant<int, 1>{}, t + 1, kLoop);
         if constexpr (DB > 2)
-            tile(std::integral_constant<int, (DB > 2 ? 2 : 0)>{}, t + 2);
+            tile(std::integral_constant<int, (DB > 2 ? 2 : 0)>{}, t + 2, kLoop);
         if constexpr (DB > 3)
-            tile(std::integral_constant<int, (DB > 3 ? 3 : 0)>{}, t + 3);
+            tile(std::integral_constant<int, (DB > 3 ? 3 : 0)>{}, t + 3, kLoop);
     }
     if (t < ntiles)
-        tile(std::integral_constant<int, 0>{}, t++);
+        tile(std::integral_constant<int, 0>{}, t++, std::integral_constant<int, 1>{});
     if constexpr (DB > 2)
         if (t < ntiles)
-            tile(std::integral_constant<int, 1>{}, t++);
+            tile(std::integral_constant<int, 1>{}, t++, std::integral_constant<int, 2>{});
     if constexpr (DB > 3)
         if (t < ntiles)
-            tile(std::integral_constant<int, (DB > 3 ? 2 : 0)>{}, t++);
+            tile(std::integral_constant<int, (DB > 3 ? 2 : 0)>{}, t++, std::integral_constant<int, 3>{});
     // Drain: outstanding copies write LDS; the last MFMAs must finish before
     // their accumulators are read (the compiler does not count these
     // instructions as MFMAs, so it inserts no wait states for them).
