@@ -291,16 +291,29 @@ __device__ inline __amdgpu_buffer_rsrc_t row_rsrc(const GemmArgs &p, const void 
                      clamp_bytes((int64_t)(p.M - m0) * row_bytes));
 }
 
+// In two steps: the row of A (with a row list: a load), and its offset.
+template <int GR>
+__device__ inline uint32_t row_index(const GemmArgs &p, int m0, int r)
+{
+    if constexpr (GR != 0) {
+        if (p.rows)
+            return m0 + r < p.M ? (uint32_t)p.rows[m0 + r] : 0xFFFFFFFFu;
+    }
+    return (uint32_t)r;
+}
+template <int GR>
+__device__ inline uint32_t index_offset(const GemmArgs &p, uint32_t i, uint32_t row_bytes)
+{
+    if constexpr (GR != 0) {
+        if (p.rows)
+            return i < (uint32_t)p.a_rows ? i * row_bytes : kNoRow;
+    }
+    return i * row_bytes;
+}
 template <int GR>
 __device__ inline uint32_t row_offset(const GemmArgs &p, int m0, int r, uint32_t row_bytes)
 {
-    if constexpr (GR != 0) {
-        if (p.rows) {
-            const uint32_t i = m0 + r < p.M ? (uint32_t)p.rows[m0 + r] : 0xFFFFFFFFu;
-            return i < (uint32_t)p.a_rows ? i * row_bytes : kNoRow;
-        }
-    }
-    return (uint32_t)r * row_bytes;
+    return index_offset<GR>(p, row_index<GR>(p, m0, r), row_bytes);
 }
 
 // ------------------------------------------------------------ load ring

@@ -211,6 +211,7 @@ gemm_w4_kernel(const GemmArgs args)
     static_assert(DB >= 2 && DB <= 4, "B sets");
     constexpr int kDB = DB;
     using namespace w4;
+    static_assert(GR == 0 || SWZ, "by expert: swizzled rows");
     static_assert(!SYNC || (SWZ && !kDmaLate), "the register copy: swizzled rows, copies after the barrier");
     constexpr bool kMx = SCALE == kScaleMx;
     constexpr bool kMx4 = SCALE == kScaleMx32;
@@ -287,7 +288,10 @@ gemm_w4_kernel(const GemmArgs args)
             // lands at row 8*blk + l/8, stored chunk l%8, so it fetches logical
             // chunk (l%8) ^ swizzle(row)
             const int r = 8 * blk + (lane >> 3);
-            dma_voff[j] = row_offset<GR>(p, m0, r, Kb) + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
+            if constexpr (GR != 0)
+                dma_voff[j] = row_index<GR>(p, m0, r);   // (its offset below, behind the loads of B)
+            else
+                dma_voff[j] = row_offset<GR>(p, m0, r, Kb) + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
         } else {
             dma_voff[j] = row_offset<GR>(p, m0, (blk / kCH) * 16 + (lane & 15), Kb) +
                           (uint32_t)((blk % kCH) * 64 + (lane >> 4) * 16);
@@ -345,8 +349,7 @@ gemm_w4_kernel(const GemmArgs args)
         for (int j = 0; j < kXWide; ++j) {
             const int e0 = (j * NW + wave) * 64, r0 = e0 / kPieces, r = (e0 + lane) / kPieces;
             xw_rsrc[j] = r0 < TM ? rXa : r0 < TM + TN ? rXb : make_rsrc(nullptr, 0);
-            xw_voff[j] = (r0 < TM ? row_offset<GR>(p, m0, r, (uint32_t)kblk) : (uint32_t)(r - TM) * (uint32_t)kblk) +
-                         16u * (uint32_t)(lane % kPieces);
+            xw_voff[j] = r0 < TM ? row_index<GR>(p, m0, r) : (uint32_t)(r - TM);
         }
     }
     [[maybe_unused]] auto copy_wide = [&](int c) {   // stage c: k-tiles c XG .. (bytes past a row's end: unread)
@@ -465,10 +468,44 @@ gemm_w4_kernel(const GemmArgs args)
         }
     };
 
-    copy_wide(0);
     // Prologue: copies of tiles 0..kDmaAhead-1, B of tiles 0..DB-1, all
     // landed; then the first kRA fragments of tile 0.  (The register copy
     // loads its last prologue tile into registers: tile 0 writes it.)
+    // By expert, B first: its loads need no row of the list.
+    auto prologue_b = [&](auto setc) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int ch = 0; ch < kCH; ++ch)
+                load_b(setc, nt, ch, kofs(decltype(setc)::value));
+    };
+    auto all_b = [&] {
+        prologue_b(std::integral_constant<int, 0>{});
+        prologue_b(std::integral_constant<int, 1>{});
+        if constexpr (DB > 2)
+            prologue_b(std::integral_constant<int, (DB > 2 ? 2 : 0)>{});
+        if constexpr (DB > 3)
+            prologue_b(std::integral_constant<int, (DB > 3 ? 3 : 0)>{});
+    };
+    if constexpr (GR != 0) {
+        all_b();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kDma; ++j) {
+            const int r = 8 * (j * NW + wave) + (lane >> 3);
+            dma_voff[j] = index_offset<GR>(p, dma_voff[j], Kb) + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
+        }
+    }
+    if constexpr (kWide) {
+        constexpr int kPieces = kXRow / 16;
+#pragma unroll
+        for (int j = 0; j < kXWide; ++j) {
+            const bool row = (j * NW + wave) * 64 / kPieces < TM;
+            xw_voff[j] = (row ? index_offset<GR>(p, xw_voff[j], (uint32_t)kblk) : xw_voff[j] * (uint32_t)kblk) +
+                         16u * (uint32_t)(lane % kPieces);
+        }
+    }
+    copy_wide(0);
 #pragma unroll
     for (int t = 0; t < kDmaAhead; ++t)
 #pragma unroll
@@ -483,19 +520,8 @@ gemm_w4_kernel(const GemmArgs args)
             if (j == 0)
                 dma_scales(t, kofs(t));
         }
-    auto prologue_b = [&](auto setc) {
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int ch = 0; ch < kCH; ++ch)
-                load_b(setc, nt, ch, kofs(decltype(setc)::value));
-    };
-    prologue_b(std::integral_constant<int, 0>{});
-    prologue_b(std::integral_constant<int, 1>{});
-    if constexpr (DB > 2)
-        prologue_b(std::integral_constant<int, (DB > 2 ? 2 : 0)>{});
-    if constexpr (DB > 3)
-        prologue_b(std::integral_constant<int, (DB > 3 ? 3 : 0)>{});
+    if constexpr (GR == 0)
+        all_b();
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     read_xb(0);
 #pragma unroll
