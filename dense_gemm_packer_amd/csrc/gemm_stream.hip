@@ -684,7 +684,11 @@ static const KernelSpec kStreamKernels[] = {
     DGP_KSPLIT_BOTH_OUT(kDtypeFp4, 16, 4, kScaleMx32, 32),
 };
 
-// Product grouped by expert: the 8-wave K-split tiles.
+// Product grouped by expert: the 8-wave K-split tiles, for experts with a row
+// tile or two.  Bound by reading the weights of the experts that have rows: 64
+// of 4096 x 7168 in blockscale with about 8 rows each take 302 us, 1.97 GB
+// fetched at 6.5 TB/s (16 x 32 tile; a streaming read reaches 7.2), one token
+// through 8 of them in bf16 69 us, 6.8 TB/s (16 x 64).
 #define DGP_KSPLITG(DT, DEPTH, SC, TN)                                                         \
     {kStream, DT, SC, kOutBf16, 16, TN, 0, 8, (TN >= 16 ? TN / 16 : 1), DEPTH, 0, 0, DEPTH, 0,      \
      &launch_ksplit<DT, 8, DEPTH, SC, kOutBf16, TN, 1>}
