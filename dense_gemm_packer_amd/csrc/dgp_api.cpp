@@ -738,6 +738,9 @@ dgp_status run_grouped(const GemmCall &c, const Experts &x, hipStream_t stream)
     a.tiles_m = (int)tiles_m, a.tiles_n = (int)tiles_n, a.splits = 1;
     const bool configured = c.cfg && c.cfg->tile_m > 0;
     a.remap = configured ? c.cfg->xcd_remap : 1;
+    // (8 row tiles side by side: within 3 % of the best of 4, 8, 16 and 32 for 1 to
+    // 32 experts in every mode; 2 and 1: 7 and 11 % slower on 16 experts of 1000
+    // rows, bf16, N 4096, K 8192)
     a.group_m = configured && c.cfg->group_m > 0 ? c.cfg->group_m : 8;
     a.offsets = x.offsets, a.rows = x.rows;
     a.groups = (int)x.E, a.a_rows = (int)(x.rows ? x.a_rows : 0);
