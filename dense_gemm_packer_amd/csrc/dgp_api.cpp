@@ -861,13 +861,20 @@ int64_t scale_row(int64_t K, int scale_mode)
            : scale_mode == DGP_SCALE_MX32 ? K / 32 : 0;
 }
 
-// Q and S of an operand against one of its strided inputs.
-dgp_status check_codes_apart(const void *Q, const void *S, int scale_mode, const void *X, int64_t ldx, int x_type,
-                             int64_t M, int64_t K, const char *what)
+// Bytes of scales that a call of M rows writes (a given per-tensor scale: none).
+int64_t scale_bytes(int64_t M, int64_t K, int scale_mode, const float *scale)
 {
-    const int64_t in = input_size(x_type);
+    return scale_mode == DGP_SCALE_TENSOR ? (scale ? 0 : 4) : M * scale_row(K, scale_mode);
+}
+
+// Q and S of an operand against one of its strided inputs.
+dgp_status check_codes_apart(const void *Q, const void *S, const float *scale, int scale_mode, const void *X, int64_t ldx,
+                             int x_type, int64_t M, int64_t K, const char *what)
+{
+    const int64_t in = input_size(x_type), s_bytes = scale_bytes(M, K, scale_mode, scale);
     DGP_TRY(check_apart(Q, code_row(K, scale_mode), X, K * in, ldx * in, M, x_type == DGP_BF16, what));
-    return check_apart(scale_row(K, scale_mode) ? S : nullptr, scale_row(K, scale_mode), X, K * in, ldx * in, M, false, what);
+    // (S as one dense row against all of X as another)
+    return check_apart(s_bytes ? S : nullptr, s_bytes, X, ((M - 1) * ldx + K) * in, 0, 1, false, what);
 }
 
 dgp_status check_amax_workspace(int64_t groups, const float *ws, size_t ws_bytes)
@@ -955,7 +962,7 @@ dgp_status dgp_quantize(const void *X, int64_t ldx, int x_type, void *Q, void *S
     const bool measure = scale_mode == DGP_SCALE_TENSOR && !scale;
     if (measure)
         DGP_TRY(check_amax_workspace(1, ws, ws_bytes));
-    DGP_TRY(check_codes_apart(Q, S, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
+    DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = X, a.Q = Q, a.S = S, a.scale = scale;
@@ -1028,8 +1035,8 @@ dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64
     if (scale_mode == DGP_SCALE_TENSOR && !scale)
         return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
     DGP_TRY(check_codes(Q, S, scale, scale_mode));
-    DGP_TRY(check_codes_apart(Q, S, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
-    DGP_TRY(check_codes_apart(Q, S, scale_mode, R, ldr, x_type, M, K, "residual and Q or S"));
+    DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
+    DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, R, ldr, x_type, M, K, "residual and Q or S"));
     const int64_t in = input_size(x_type);
     DGP_TRY(check_apart(H, K * in, X, K * in, ldx * in, M, true, "X and residual output"));
     DGP_TRY(check_apart(H, K * in, R, K * in, ldr * in, M, true, "residual and residual output"));
@@ -1053,8 +1060,8 @@ dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_
     if (scale_mode == DGP_SCALE_TENSOR && !scale)
         return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
     DGP_TRY(check_codes(Q, S, scale, scale_mode));
-    DGP_TRY(check_codes_apart(Q, S, scale_mode, G, ldg, x_type, M, K, "gate and Q or S"));
-    DGP_TRY(check_codes_apart(Q, S, scale_mode, U, ldu, x_type, M, K, "up and Q or S"));
+    DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, G, ldg, x_type, M, K, "gate and Q or S"));
+    DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, U, ldu, x_type, M, K, "up and Q or S"));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = G, a.U = U, a.Q = Q, a.S = S, a.scale = scale;
