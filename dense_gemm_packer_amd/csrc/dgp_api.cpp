@@ -877,6 +877,17 @@ dgp_status check_codes_apart(const void *Q, const void *S, const float *scale, i
     return check_apart(s_bytes ? S : nullptr, s_bytes, X, ((M - 1) * ldx + K) * in, 0, 1, false, what);
 }
 
+// Q, S and H (the norm's residual output, or NULL) against an input that every
+// row reads: the norm's weight, a given scale.
+dgp_status check_outputs_apart(const void *Q, const void *S, const void *H, const float *scale, int scale_mode, int x_type,
+                               int64_t M, int64_t K, const void *in, int64_t in_bytes, const char *what)
+{
+    const int64_t s_bytes = scale_bytes(M, K, scale_mode, scale);
+    DGP_TRY(check_apart(Q, M * code_row(K, scale_mode), in, in_bytes, 0, 1, false, what));
+    DGP_TRY(check_apart(s_bytes ? S : nullptr, s_bytes, in, in_bytes, 0, 1, false, what));
+    return check_apart(H, M * K * input_size(x_type), in, in_bytes, 0, 1, false, what);
+}
+
 dgp_status check_amax_workspace(int64_t groups, const float *ws, size_t ws_bytes)
 {
     const size_t need = dgp_quantize_workspace_bytes(groups, DGP_SCALE_TENSOR);
@@ -963,6 +974,7 @@ dgp_status dgp_quantize(const void *X, int64_t ldx, int x_type, void *Q, void *S
     if (measure)
         DGP_TRY(check_amax_workspace(1, ws, ws_bytes));
     DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
+    DGP_TRY(check_outputs_apart(Q, S, nullptr, scale, scale_mode, x_type, M, K, scale, 4, "Q and the given scale"));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = X, a.Q = Q, a.S = S, a.scale = scale;
@@ -1041,6 +1053,8 @@ dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64
     DGP_TRY(check_apart(H, K * in, X, K * in, ldx * in, M, true, "X and residual output"));
     DGP_TRY(check_apart(H, K * in, R, K * in, ldr * in, M, true, "residual and residual output"));
     DGP_TRY(check_apart(H, K * in, Q, code_row(K, scale_mode), code_row(K, scale_mode), M, false, "Q and residual output"));
+    DGP_TRY(check_outputs_apart(Q, S, H, scale, scale_mode, x_type, M, K, W, K * input_size(w_type), "weight and Q, S or residual output"));
+    DGP_TRY(check_outputs_apart(Q, S, H, scale, scale_mode, x_type, M, K, scale, 4, "the given scale and Q or residual output"));
     DGP_TRY(check_device_arch());
     NormArgs a{};
     a.X = X, a.R = R, a.W = W, a.Q = Q, a.S = S, a.H = H, a.scale = scale;
@@ -1062,6 +1076,7 @@ dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_
     DGP_TRY(check_codes(Q, S, scale, scale_mode));
     DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, G, ldg, x_type, M, K, "gate and Q or S"));
     DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, U, ldu, x_type, M, K, "up and Q or S"));
+    DGP_TRY(check_outputs_apart(Q, S, nullptr, scale, scale_mode, x_type, M, K, scale, 4, "Q and the given scale"));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = G, a.U = U, a.Q = Q, a.S = S, a.scale = scale;
