@@ -888,6 +888,17 @@ dgp_status check_outputs_apart(const void *Q, const void *S, const void *H, cons
     return check_apart(H, M * K * input_size(x_type), in, in_bytes, 0, 1, false, what);
 }
 
+// The scales against the codes, and (the norm) the residual output.
+dgp_status check_scales_apart(const void *Q, const void *S, const void *H, const float *scale, int scale_mode, int x_type,
+                              int64_t M, int64_t K)
+{
+    const int64_t s_bytes = scale_bytes(M, K, scale_mode, scale);
+    if (s_bytes == 0)
+        return DGP_OK;
+    DGP_TRY(check_apart(S, s_bytes, Q, M * code_row(K, scale_mode), 0, 1, false, "Q and S"));
+    return check_apart(S, s_bytes, H, M * K * input_size(x_type), 0, 1, false, "S and residual output");
+}
+
 dgp_status check_amax_workspace(int64_t groups, const float *ws, size_t ws_bytes)
 {
     const size_t need = dgp_quantize_workspace_bytes(groups, DGP_SCALE_TENSOR);
@@ -975,6 +986,7 @@ dgp_status dgp_quantize(const void *X, int64_t ldx, int x_type, void *Q, void *S
         DGP_TRY(check_amax_workspace(1, ws, ws_bytes));
     DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
     DGP_TRY(check_outputs_apart(Q, S, nullptr, scale, scale_mode, x_type, M, K, scale, 4, "Q and the given scale"));
+    DGP_TRY(check_scales_apart(Q, S, nullptr, scale, scale_mode, x_type, M, K));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = X, a.Q = Q, a.S = S, a.scale = scale;
@@ -1013,6 +1025,7 @@ dgp_status dgp_quantize_b(const void *B, int x_type, void *Bs, void *sB, int64_t
                           : measure ? E * 4 : E * N * scale_row(K, scale_mode);
     DGP_TRY(check_apart(Bs, code_row(K, scale_mode), B, b_row, b_row, E * N, false, "B and Bs"));
     DGP_TRY(check_apart(sB, scales, B, E * N * b_row, E * N * b_row, 1, false, "B and sB"));
+    DGP_TRY(check_apart(sB, scales, Bs, E * N * code_row(K, scale_mode), 0, 1, false, "Bs and sB"));
     DGP_TRY(check_device_arch());
     WeightQuantArgs a{};
     a.B = B, a.Q = Bs, a.S = sB;
@@ -1055,6 +1068,7 @@ dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64
     DGP_TRY(check_apart(H, K * in, Q, code_row(K, scale_mode), code_row(K, scale_mode), M, false, "Q and residual output"));
     DGP_TRY(check_outputs_apart(Q, S, H, scale, scale_mode, x_type, M, K, W, K * input_size(w_type), "weight and Q, S or residual output"));
     DGP_TRY(check_outputs_apart(Q, S, H, scale, scale_mode, x_type, M, K, scale, 4, "the given scale and Q or residual output"));
+    DGP_TRY(check_scales_apart(Q, S, H, scale, scale_mode, x_type, M, K));
     DGP_TRY(check_device_arch());
     NormArgs a{};
     a.X = X, a.R = R, a.W = W, a.Q = Q, a.S = S, a.H = H, a.scale = scale;
@@ -1077,6 +1091,7 @@ dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_
     DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, G, ldg, x_type, M, K, "gate and Q or S"));
     DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, U, ldu, x_type, M, K, "up and Q or S"));
     DGP_TRY(check_outputs_apart(Q, S, nullptr, scale, scale_mode, x_type, M, K, scale, 4, "Q and the given scale"));
+    DGP_TRY(check_scales_apart(Q, S, nullptr, scale, scale_mode, x_type, M, K));
     DGP_TRY(check_device_arch());
     RowQuantArgs a{};
     a.X = G, a.U = U, a.Q = Q, a.S = S, a.scale = scale;

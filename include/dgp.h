@@ -345,9 +345,10 @@ dgp_status dgp_gemm_preshuffle_grouped(const void *A, int64_t a_rows, const void
  * Inputs are rows ld* elements apart (ld* >= K), each 16-byte aligned; Q, S
  * and H are dense.  K as the product takes it: rows of Q a multiple of 128
  * bytes, at most 2^23.  M = 0 or K = 0 is a no-op (no scale is written: such
- * a product reads none).  Outputs that overlap an input are refused
- * (DGP_ERR_SHAPE), but for an update in place: Q (bf16) or H that is an input
- * itself, with dense rows of the same type.
+ * a product reads none).  Outputs that overlap each other or an input (the
+ * norm's weight and a given scale among them) are refused (DGP_ERR_SHAPE), but
+ * for an update in place: Q (bf16) or H that is X, the residual, the gate or
+ * the other factor itself, with dense rows of the same type.
  */
 
 /* Bytes of workspace that dgp_quantize (E = 1) and dgp_quantize_b need: 1 KiB

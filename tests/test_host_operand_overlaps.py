@@ -45,3 +45,37 @@ def test_codes_over_a_given_scale(L, at):
 
 def test_residual_stream_over_a_given_scale(L):
     assert refused(L, ops.norm(L, X=X, W=W, R=R, ldr=256, H=H, Q=Q, S=None, scale=H + 2044, mode=ops.TENSOR))
+
+
+# Outputs on each other.
+
+@pytest.mark.parametrize("kw", [
+    dict(S=Q), dict(S=Q + 4 * 256 - 4), dict(S=Q - 28), dict(S=Q, mode=ops.MX), dict(S=Q - 7, mode=ops.MX),
+    dict(S=Q + 4 * 128 - 1, mode=ops.MX32), dict(S=Q - 31, mode=ops.MX32),
+])
+def test_scales_over_codes(L, kw):
+    """4 rows of 256: 1024 bytes of e4m3 codes and 8 fp32 or 8 E8M0 scales, or
+    512 bytes of E2M1 codes and 32 scales."""
+    kw = {**dict(Q=Q, S=S), **kw}
+    assert refused(L, ops.quantize(L, X=X, **kw))
+    assert refused(L, ops.norm(L, X=X, W=W, **kw))
+    assert refused(L, ops.swiglu(L, G=X, U=X + 512, **kw))
+
+
+@pytest.mark.parametrize("at", [0, 1020])
+def test_measured_tensor_scale_over_codes(L, at):
+    assert refused(L, ops.quantize(L, X=X, Q=Q, S=Q + at, mode=ops.TENSOR, ws=W, wsb=1024))
+
+
+@pytest.mark.parametrize("kw", [dict(S=H), dict(S=H - 28), dict(S=H + 2044), dict(S=H + 2047, mode=ops.MX)])
+def test_scales_over_the_residual_stream(L, kw):
+    assert refused(L, ops.norm(L, **{**dict(X=X, W=W, R=R, ldr=256, H=H, Q=Q), **kw}))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(sB=Q), dict(sB=Q + 3 * 128 * 256 - 4), dict(sB=Q - 20), dict(sB=Q - 3 * 256 + 1, mode=ops.MX),
+    dict(sB=Q + 3 * 128 * 128 - 1, mode=ops.MX32), dict(sB=Q - 8, mode=ops.TENSOR, ws=W, wsb=3072),
+])
+def test_weight_scales_over_weight_codes(L, kw):
+    """3 weights of 128 x 256."""
+    assert refused(L, ops.quantize_b(L, **{**dict(B=X, Bs=Q, E=3), **kw}))
