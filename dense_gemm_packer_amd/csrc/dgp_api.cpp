@@ -154,6 +154,7 @@ struct Query {
     int family, dtype, scale, out, tm, tn;
     int kt = -1, wm = -1, depth = -1, pv = -1, pd = -1, sched = -1, lay = -1, copy = -1;
     int64_t K = 0;   // for kernels that need K to be a multiple of something
+    bool dwords = true;   // the scales start at whole dwords, which those kernels need too
 };
 
 const KernelSpec *find_spec(const Query &q, const KernelSpec *(*table)(int *) = kernel_table)
@@ -167,7 +168,7 @@ const KernelSpec *find_spec(const Query &q, const KernelSpec *(*table)(int *) = 
             k.tn == q.tn && (q.kt < 0 || k.kt == q.kt) && (q.wm < 0 || wm == q.wm) &&
             (q.depth < 0 || k.depth == q.depth) && (q.pv < 0 || k.pv == q.pv) && (q.pd < 0 || k.pd == q.pd) &&
             (q.sched < 0 || k.sched == q.sched) && (q.lay < 0 || (k.family == kTiled && k.lay == q.lay)) &&
-            (q.copy < 0 || (k.family == kTiled && k.copy == q.copy)) && (k.k_mult == 0 || q.K % k.k_mult == 0))
+            (q.copy < 0 || (k.family == kTiled && k.copy == q.copy)) && (k.k_mult == 0 || (q.dwords && q.K % k.k_mult == 0)))
             return &k;
     }
     return nullptr;
@@ -362,6 +363,10 @@ struct GemmCall {
     bool lib_scratch = false;   // split-K partials go to the library's fixed array (ws unused)
 };
 
+// Scales that start at whole dwords.  (E8M0 bytes of 128 blocks need not: the
+// kernels that copy them many bytes at a time are then left out.)
+bool dword_scales(const GemmCall &c) { return (((uintptr_t)c.sA | (uintptr_t)c.sB) & 3u) == 0; }
+
 // The kernel of `table` that the call's configuration names.
 dgp_status configured_spec(const GemmCall &c, int64_t Ks, const KernelSpec *(*table)(int *), const KernelSpec **out_spec)
 {
@@ -401,6 +406,7 @@ dgp_status configured_spec(const GemmCall &c, int64_t Ks, const KernelSpec *(*ta
         q.depth = c.cfg->prefetch > 0 ? c.cfg->prefetch : -1;
     }
     q.K = c.K;
+    q.dwords = dword_scales(c);
     const KernelSpec *spec = find_spec(q, table);
     if (!spec)
         return fail(DGP_ERR_CONFIG,
@@ -669,20 +675,22 @@ double expected_row_tiles(int64_t M, int64_t E, int tm)
     return 2 * M > live * tm ? std::max((double)live, (double)M / tm + 0.5 * live) : (double)live;
 }
 
-const KernelSpec *default_grouped_spec(int dtype, int scale, int64_t M, int64_t N, int64_t K, int64_t Kb, int64_t E)
+const KernelSpec *default_grouped_spec(const GemmCall &call, int64_t Kb, int64_t E)
 {
+    const int64_t M = call.M, N = call.N;
     const GroupedTile *best = nullptr;
     double least = 0;
     const double weights = (double)(E < M ? E : M) * (double)N * (double)Kb * 1e-6;
-    for (const GroupedTile &t : kGroupedCost[scale]) {
+    for (const GroupedTile &t : kGroupedCost[call.scale]) {
         const double x = std::ceil(expected_row_tiles(M, E, t.tm) * (double)((N + t.tn - 1) / t.tn) / kNumCu);
         const double c = (t.a + t.b * (double)(Kb / 128)) * (1 + t.s * (x - 1)), m = t.a + weights / t.w;
         const double us4 = c * c * c * c + m * m * m * m;
         if (!best || us4 < least)
             best = &t, least = us4;
     }
-    Query q{best->tm == 16 ? kStream : kTiled, dtype, scale, kOutBf16, best->tm, best->tn};
-    q.K = K;
+    Query q{best->tm == 16 ? kStream : kTiled, call.dtype, call.scale, kOutBf16, best->tm, best->tn};
+    q.K = call.K;
+    q.dwords = dword_scales(call);
     return find_spec(q, grouped_table);
 }
 
@@ -718,7 +726,7 @@ dgp_status run_grouped(const GemmCall &c, const Experts &x, hipStream_t stream)
     if (c.cfg && c.cfg->tile_m > 0)
         DGP_TRY(configured_spec(c, Kb, grouped_table, &spec));
     else
-        spec = default_grouped_spec(c.dtype, c.scale, c.M, c.N, c.K, Kb, x.E);
+        spec = default_grouped_spec(c, Kb, x.E);
     if (!spec)
         return fail(DGP_ERR_CONFIG, "no compiled grouped kernel fits this shape");
     const int64_t tiles_m = most_row_tiles(c.M, x.E, spec->tm), tiles_n = (c.N + spec->tn - 1) / spec->tn;

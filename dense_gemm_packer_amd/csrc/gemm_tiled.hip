@@ -34,7 +34,8 @@ namespace dgp {
 // (12 copies of up to 64 lines against 40 of 16).  Staged for 16 (mxfp8) or 4
 // (mxfp4) k-tiles, a row's 16 or 32 bytes come in one or two pieces, into one
 // of two LDS areas behind the A ring, while the k-tiles before them run.  Rows
-// of the scale arrays have to be whole dwords (mxfp8: K % 512 == 0).
+// of the scale arrays have to be whole dwords and start at one (mxfp8: K % 512
+// == 0 and aligned pointers).
 template <int DT, int TM, int TN, int WM, int WN, int KT, int DEPTH, int SCALE, int OUT, int PV, int PD, int GR, int XG>
 __global__ void __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
                                amdgpu_waves_per_eu((WM * WN + 3) / 4, (WM * WN + 3) / 4)))

@@ -62,7 +62,7 @@ struct KernelSpec {
     void (*launch)(const GemmArgs &, dim3 grid, hipStream_t);
     int lay = 0;    // tiled: A's LDS layout, kLayBlocks or kLaySwizzled
     int copy = 0;   // tiled: A's global -> LDS path, kCopyAsync or kCopyRegs
-    int k_mult = 0; // K is a multiple of this (0: any K that the mode takes)
+    int k_mult = 0; // K is a multiple of this and the scales start at whole dwords (0: any that the mode takes)
 };
 
 // The compiled GEMM kernels: the tiled family (gemm_tiled.hip), its

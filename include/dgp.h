@@ -34,13 +34,15 @@
  *   - No input needs padding past its last element.  The kernels read
  *     through gfx950 buffer resources whose range ends at the input's last
  *     byte; a load at or past that end returns zero and touches no memory.
- *     One kernel relies on a finer form of this rule: the 16-row K-split
- *     decode tiles read mxfp4 (DGP_SCALE_MX32) scale bytes 16 at a time,
- *     and such a 16-byte load near the end of sA or sB may run past it.  The
- *     buffer unit range-checks each dword of an aligned multi-dword buffer
- *     load on its own, so the dwords inside the range carry data and the
- *     dwords past it read as zero.  (The compiler merges adjacent aligned
- *     dword buffer loads into one wider load on the same rule.)
+ *     Some kernels rely on a finer form of this rule: the 16-row K-split
+ *     decode tiles read mxfp4 (DGP_SCALE_MX32) scale bytes 16 at a time, and
+ *     the larger tiles of dgp_gemm_preshuffle_grouped copy mxfp4 and mxfp8
+ *     (DGP_SCALE_MX128; K a multiple of 512 and scales at whole dwords) scale
+ *     bytes 16 at a time, and such a 16-byte load near the end of sA or sB
+ *     may run past it.  The buffer unit range-checks each dword of an aligned
+ *     multi-dword buffer load on its own, so the dwords inside the range
+ *     carry data and the dwords past it read as zero.  (The compiler merges
+ *     adjacent aligned dword buffer loads into one wider load on the same rule.)
  */
 #ifndef DGP_H
 #define DGP_H
@@ -88,7 +90,8 @@ typedef enum dgp_dtype { DGP_BF16 = 0, DGP_FP8_E4M3 = 1, DGP_FP4_E2M1 = 2, DGP_F
  * the hardware-scaled MFMA).  DGP_SCALE_MX32 (mxfp4): the only mode of
  * DGP_FP4_E2M1, and only for it; as MX128 but one E8M0 byte per 32-element
  * block, sA [M][K/32], sB [N][K/32] ([P3] "What's included": mxfp4, 4-bit
- * packed with 32-element E8M0 blocks).  fp32 scales must be 4-byte aligned. */
+ * packed with 32-element E8M0 blocks).  fp32 scales and those of MX32 must be
+ * 4-byte aligned; MX128's may start at any byte. */
 typedef enum dgp_scale_mode {
     DGP_SCALE_NONE = 0,
     DGP_SCALE_TENSOR = 1,
