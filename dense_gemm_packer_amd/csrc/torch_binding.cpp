@@ -173,14 +173,18 @@ ScalarType scale_type(int mode)
 
 // Where a call runs: the given stream, or the current one of X's device; X's
 // device is current, and outputs are allocated on that stream, while this lives.
+// A call that allocates nothing also takes any object with a cuda_stream handle.
 class Place {
 public:
-    Place(const Tensor &X, PyObject *stream)
+    Place(const Tensor &X, PyObject *stream, bool allocates = true)
     {
         if (stream == Py_None) {
             device_.emplace(X.device());
             PyObject *h = PyObject_CallFunction(current_stream, "i", (int)X.device().index());
             handle_ = take(h);
+        } else if (!allocates && !THPStream_Check(stream)) {
+            device_.emplace(X.device());
+            handle_ = take(PyObject_GetAttrString(stream, "cuda_stream"));
         } else {
             if (!THPStream_Check(stream)) {
                 PyErr_SetString(PyExc_TypeError, "stream must be a torch stream");
@@ -505,7 +509,7 @@ PyObject *gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (C.defined())
         dense(C, ScalarType::BFloat16, shape_c, A, "out");
     check_all_scales(sA, sB, (int)mode, M, 1, N, K, A);
-    Place place(A, a[7]);
+    Place place(A, a[7], !C.defined());
     if (!C.defined())
         C = empty(shape_c, ScalarType::BFloat16, A);
     call(abi.gemm, (const void *)A.data_ptr(), (const void *)Bs.data_ptr(), C.data_ptr(), M, N, K, dtype, (int)mode,
