@@ -2,11 +2,12 @@
 
 Argument marshalling only, through ctypes; the one-pass products and the
 operators that write their operands go through a small native module
-(csrc/torch_binding.cpp, _binding.so), whose calls cost less on the host: every computation runs in the HIP kernels behind
-the C ABI declared in include/dgp.h.  torch supplies device memory (outputs
-are allocated as torch tensors when not given) and the stream (the current
-torch stream unless one is passed).  There is no fallback: if the compiled
-library is missing, every call raises.
+(csrc/torch_binding.cpp, _binding.so), whose calls cost less on the host.
+Every computation runs in the HIP kernels behind the C ABI declared in
+include/dgp.h.  torch supplies device memory (outputs are allocated as torch
+tensors when not given) and the stream (the current torch stream unless one is
+passed).  There is no fallback: if the compiled library or the native module is
+missing, the calls that need it raise.
 
 Element types follow the torch dtype of the operands: torch.bfloat16 ->
 DGP_BF16, torch.float8_e4m3fn -> DGP_FP8_E4M3, torch.float4_e2m1fn_x2 (two
@@ -424,9 +425,9 @@ def gemm_preshuffle_grouped(A: torch.Tensor, Bs: torch.Tensor, offsets: torch.Te
     """The product grouped by expert (dgp_gemm_preshuffle_grouped): rows
     offsets[e]..offsets[e+1] of C are rows of A times weight e, transposed.  Bs
     is [E][N][K] preshuffled (quantize_b of a stack, or preshuffle_b of each
-    weight: preshuffle_b(B.view(E * N, K)).view(E, N, K)), offsets int32 [E+1] on the device; rows (int32) names the row of A
-    for each row of C.  Rows of C that no expert owns keep what `out` holds
-    (unspecified without it)."""
+    weight: preshuffle_b(B.view(E * N, K)).view(E, N, K)), offsets int32 [E+1]
+    on the device; rows (int32) names the row of A for each row of C.  Rows of C
+    that no expert owns keep what `out` holds (unspecified without it)."""
     if scale_mode is None:
         scale_mode = _scale_mode(A, sA, sB, None)
     cfg = None if config is None else config if isinstance(config, Config) else Config(**config)
@@ -463,8 +464,8 @@ def gemm_preshuffle_splitk_noalloc(A: torch.Tensor, Bs: torch.Tensor, split_k: i
 
 def quantize(X: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
              scales: torch.Tensor | None = None, stream=None):
-    """(Q, S): the rows of X ([M][K] bfloat16, float16 or float32; the row
-    stride is free) as the A operand of a quantised product (dgp_quantize).
+    """(Q, S): the rows of X ([M][K] bfloat16, float16 or float32; any row
+    stride of whole 16 bytes) as the A operand of a quantised product (dgp_quantize).
     SCALE_TENSOR measures the scale, or takes the given one (then S is it)."""
     return _native().quantize(X, scale_mode, scale, out, scales, stream)
 
@@ -492,8 +493,8 @@ def rmsnorm_quantize(X: torch.Tensor, weight: torch.Tensor, scale_mode: int, res
 def swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, scale_mode: int, scale: torch.Tensor | None = None,
                     out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
     """(Q, S): gate / (1 + exp(-gate)) * up written as a product's A operand
-    (dgp_swiglu_quantize).  gate and up are [M][K] with free row strides: the
-    two halves of one product's columns are C[:, :K] and C[:, K:].  SCALE_NONE:
+    (dgp_swiglu_quantize).  gate and up are [M][K] with any row strides of whole
+    16 bytes: the two halves of one product's columns are C[:, :K] and C[:, K:].  SCALE_NONE:
     Q is bfloat16 and S None; SCALE_TENSOR takes a given scale."""
     return _native().swiglu_quantize(gate, up, scale_mode, scale, out, scales, stream)
 

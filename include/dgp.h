@@ -24,13 +24,15 @@
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The
  *     library never allocates, frees, synchronises or keeps a pointer past the
  *     call (one entry point, dgp_gemm_preshuffle_splitk_noalloc, uses a fixed
- *     array of the library's own instead of a caller workspace).  Work is enqueued on `stream` (a hipStream_t; NULL = the null
- *     stream) and runs asynchronously: outputs are ready when the stream is.
+ *     array of the library's own instead of a caller workspace).  Work is
+ *     enqueued on `stream` (a hipStream_t; NULL = the null stream) and runs
+ *     asynchronously: outputs are ready when the stream is.
  *   - Scales are device pointers to fp32 as well (so a launch never needs a
  *     host synchronisation).
  *   - Every argument is validated on the host before any HIP call.  On a bad
  *     argument the call returns a status != DGP_OK and enqueues nothing.
- *   - Aliasing between an output and any input is not supported.
+ *   - Aliasing between an output and any input is not supported (the operators
+ *     that write an operand say where they update in place).
  *   - No input needs padding past its last element.  The kernels read
  *     through gfx950 buffer resources whose range ends at the input's last
  *     byte; a load at or past that end returns zero and touches no memory.
@@ -319,8 +321,8 @@ dgp_status dgp_gemm_preshuffle_splitk_noalloc(const void *A, const void *Bs, voi
  *
  * The tile is chosen from M, N, K and E by estimated time; cfg names another
  * compiled one (every mode: 16x16, 16x32 and 16x64 K-split tiles of 8 waves;
- * 64x64, 64x128, 64x256, 128x256 and 256x256 with tile_k = 128).  K > 0; M = 0, N = 0 or E = 0 is a no-op; E <=
- * 65535.  One launch, no workspace.
+ * 64x64, 64x128, 64x256, 128x256 and 256x256 with tile_k = 128).  K > 0; M = 0,
+ * N = 0 or E = 0 is a no-op; E <= 65535.  One launch, no workspace.
  */
 dgp_status dgp_gemm_preshuffle_grouped(const void *A, int64_t a_rows, const void *Bs, void *C, int64_t M, int64_t N,
                                        int64_t K, int64_t E, const int32_t *offsets, const int32_t *rows, int dtype,
@@ -378,13 +380,16 @@ dgp_status dgp_quantize_b(const void *B, int x_type, void *Bs, void *sB, int64_t
 /* dgp_rmsnorm_quantize -- h = x + r (r: the residual's rows, or R NULL: h = x),
  * y = h / sqrt(mean(h^2) + eps) * w over each row; Q, S from y.  H, where not
  * NULL, receives h rounded to x_type ([M][K]; y comes from the unrounded sum).
- * The squares are summed in fp32: beyond 3.4e38 (values of about 1e19) y is 0.
+ * The squares are summed in fp32: beyond 3.4e38 (values of about 1e19) y is 0;
+ * with eps = 0 rows of values below about 1e-19 lose bits and below 1e-23 are
+ * divided by 0.
  * w has K values of x_type or DGP_F32.  DGP_SCALE_TENSOR takes a given scale. */
 dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64_t ldr, int x_type, const void *W,
                                 int w_type, float eps, void *Q, void *S, const float *scale, void *H, int64_t M,
                                 int64_t K, int scale_mode, void *stream);
 
-/* dgp_swiglu_quantize -- y = g / (1 + exp(-g)) * u elementwise; Q, S from y.
+/* dgp_swiglu_quantize -- y = g / (1 + exp(-g)) * u elementwise, to 2 |g| + 8 half
+ * steps of fp32 before the output's rounding; Q, S from y.
  * The two halves of one product's columns are g and u with ldg = ldu = 2 K.
  * DGP_SCALE_TENSOR takes a given scale. */
 dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_t ldu, int x_type, void *Q, void *S,
