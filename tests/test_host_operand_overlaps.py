@@ -74,7 +74,7 @@ def test_scales_over_the_residual_stream(L, kw):
 
 @pytest.mark.parametrize("kw", [
     dict(sB=Q), dict(sB=Q + 3 * 128 * 256 - 4), dict(sB=Q - 20), dict(sB=Q - 3 * 256 + 1, mode=ops.MX),
-    dict(sB=Q + 3 * 128 * 128 - 1, mode=ops.MX32), dict(sB=Q - 8, mode=ops.TENSOR, ws=W, wsb=3072),
+    dict(sB=Q + 3 * 128 * 128 - 1, mode=ops.MX32), dict(sB=Q - 8, mode=ops.TENSOR, ws=W, wsb=4096),
 ])
 def test_weight_scales_over_weight_codes(L, kw):
     """3 weights of 128 x 256."""
