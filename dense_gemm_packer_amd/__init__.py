@@ -68,7 +68,9 @@ class Config(ctypes.Structure):
 EXPORTS = ("dgp_preshuffle_b", "dgp_unshuffle_b", "dgp_gemm_preshuffle", "dgp_splitk_workspace_bytes",
            "dgp_gemm_preshuffle_splitk", "dgp_gemm_preshuffle_splitk_noalloc",
            "dgp_quantize_workspace_bytes", "dgp_quantize", "dgp_quantize_b", "dgp_rmsnorm_quantize",
-           "dgp_swiglu_quantize", "dgp_gemm_preshuffle_grouped", "dgp_check_arch", "dgp_status_string", "dgp_last_error",
+           "dgp_swiglu_quantize", "dgp_layernorm_quantize", "dgp_norm_backward_workspace_bytes", "dgp_layernorm_backward",
+           "dgp_rmsnorm_backward", "dgp_swiglu_backward", "dgp_wgrad_workspace_bytes", "dgp_gemm_wgrad",
+           "dgp_gemm_preshuffle_grouped", "dgp_check_arch", "dgp_status_string", "dgp_last_error",
            "dgp_tile_of_workgroup", "dgp_tile_map", "dgp_kernel_count", "dgp_kernel_info", "dgp_select_kernel",
            "dgp_probe_mfma_layout", "dgp_probe_mfma_scaled", "dgp_probe_lds_dma", "dgp_probe_lds_dma_narrow", "dgp_probe_copy",
            "dgp_probe_stream_read", "dgp_probe_mfma_peak", "dgp_lds_poison")
@@ -132,6 +134,15 @@ def _load(path: str) -> ctypes.CDLL:
         "dgp_rmsnorm_quantize": [_vp, _i64, _vp, _i64, _int, _vp, _int, ctypes.c_float, _vp, _vp, _vp, _vp, _i64,
                                  _i64, _int, _vp],
         "dgp_swiglu_quantize": [_vp, _i64, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _int, _vp],
+        "dgp_layernorm_quantize": [_vp, _i64, _vp, _i64, _int, _vp, _vp, _int, ctypes.c_float, _vp, _vp, _vp, _vp, _i64,
+                                   _i64, _int, _vp],
+        "dgp_layernorm_backward": [_vp, _i64, _int, _vp, _i64, _vp, _int, _vp, _int, _vp, _i64, ctypes.c_float, _vp, _vp,
+                                   _vp, _i64, _i64, _vp, _sz, _vp],
+        "dgp_rmsnorm_backward": [_vp, _i64, _int, _vp, _i64, _vp, _int, _vp, _int, _vp, _i64, ctypes.c_float, _vp, _vp,
+                                 _i64, _i64, _vp, _sz, _vp],
+        "dgp_swiglu_backward": [_vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _i64, _vp],
+        "dgp_gemm_wgrad": [_vp, _i64, _vp, _i64, _int, _vp, _int, _vp, _int, _int, _i64, _i64, _i64, _i64, _vp, _vp, _vp,
+                           _sz, _vp],
         "dgp_check_arch": [ctypes.c_char_p],
         "dgp_tile_of_workgroup": [_i64, _i64, _i64, _i64, _int, _int, ctypes.POINTER(_i64)],
         "dgp_tile_map": [_i64, _i64, _i64, _int, _int, _vp, _i64],
@@ -155,6 +166,10 @@ def _load(path: str) -> ctypes.CDLL:
     L.dgp_splitk_workspace_bytes.restype = _sz
     L.dgp_quantize_workspace_bytes.argtypes = [_i64, _int]
     L.dgp_quantize_workspace_bytes.restype = _sz
+    L.dgp_norm_backward_workspace_bytes.argtypes = [_i64, _i64, _int]
+    L.dgp_norm_backward_workspace_bytes.restype = _sz
+    L.dgp_wgrad_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+    L.dgp_wgrad_workspace_bytes.restype = _sz
     L.dgp_status_string.argtypes = [_int]
     L.dgp_status_string.restype = ctypes.c_char_p
     L.dgp_last_error.argtypes = []
@@ -188,7 +203,9 @@ def _native():
             loader.exec_module(module)
             _module = module
         names = ("dgp_quantize_workspace_bytes", "dgp_quantize", "dgp_quantize_b", "dgp_rmsnorm_quantize",
-                 "dgp_swiglu_quantize", "dgp_gemm_preshuffle_grouped", "dgp_gemm_preshuffle")
+                 "dgp_swiglu_quantize", "dgp_gemm_preshuffle_grouped", "dgp_gemm_preshuffle", "dgp_layernorm_quantize",
+                 "dgp_norm_backward_workspace_bytes", "dgp_layernorm_backward", "dgp_rmsnorm_backward",
+                 "dgp_swiglu_backward", "dgp_wgrad_workspace_bytes", "dgp_gemm_wgrad")
         _module.bind(tuple(ctypes.cast(getattr(L, n), _vp).value for n in names), _check, _refuse_mode, _raw_stream)
         _bound = L
     return _module
@@ -497,6 +514,68 @@ def swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, scale_mode: int, scale
     16 bytes: the two halves of one product's columns are C[:, :K] and C[:, K:].  SCALE_NONE:
     Q is bfloat16 and S None; SCALE_TENSOR takes a given scale."""
     return _native().swiglu_quantize(gate, up, scale_mode, scale, out, scales, stream)
+
+
+def layernorm_quantize(X: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, scale_mode: int,
+                       residual: torch.Tensor | None = None, eps: float = 1e-5, scale: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                       residual_out: torch.Tensor | None = None, stream=None):
+    """Layer norm of h = X (+ residual) over each row, times weight plus bias
+    (None: no bias; else of weight's type), written as a product's A operand
+    (dgp_layernorm_quantize).  Returns as rmsnorm_quantize does."""
+    return _native().layernorm_quantize(X, weight, bias, scale_mode, residual, eps, scale, out, scales, residual_out, stream)
+
+
+# ------------------------------------------------------------------ gradients
+#
+# What a forward pass kept of an activation comes as that activation
+# (SCALE_NONE) or as codes and scales: what quantize wrote, or the operand that
+# the forward product took (SCALE_TENSOR, SCALE_BLOCK128, SCALE_MX128).
+
+def layernorm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor, scale_mode: int = SCALE_NONE,
+                       scales: torch.Tensor | None = None, residual_grad: torch.Tensor | None = None, eps: float = 1e-5,
+                       dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                       dbias: torch.Tensor | None = None, stream=None):
+    """(dX, dweight, dbias) of the layer norm (dgp_layernorm_backward): dX in
+    dY's type, the sums over rows in float32.  X is the norm's input h (with a
+    residual: the stream's new value) in dY's type, or its checkpoint.
+    residual_grad, the gradient of the residual stream, is added to dX."""
+    return _native().layernorm_backward(dY, X, weight, scale_mode, scales, residual_grad, eps, dx, dweight, dbias, stream)
+
+
+def rmsnorm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor, scale_mode: int = SCALE_NONE,
+                     scales: torch.Tensor | None = None, residual_grad: torch.Tensor | None = None, eps: float = 1e-6,
+                     dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None, stream=None):
+    """(dX, dweight) of the root-mean-square norm (dgp_rmsnorm_backward);
+    arguments as for layernorm_backward."""
+    return _native().rmsnorm_backward(dY, X, weight, scale_mode, scales, residual_grad, eps, dx, dweight, stream)
+
+
+def swiglu_backward(dY: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, scale_mode: int = SCALE_NONE,
+                    gate_scales: torch.Tensor | None = None, up_scales: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """[M][2 K]: the gradients of gate and of up side by side, in dY's type
+    (dgp_swiglu_backward).  gate and up are [M][K] with any row strides of whole
+    16 bytes, in dY's type or as checkpoints; the halves of one checkpoint Q, S
+    of [M][2 K] are Q[:, :K], Q[:, K:] and S[:, :K // 128], S[:, K // 128:]
+    (SCALE_TENSOR: S for both).  out may be the tensor whose halves gate and up are."""
+    return _native().swiglu_backward(dY, gate, up, scale_mode, gate_scales, up_scales, out, stream)
+
+
+def gemm_wgrad(dC: torch.Tensor, X: torch.Tensor, sX: torch.Tensor | None = None, scale_mode: int = SCALE_NONE,
+               offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               out_dtype: torch.dtype | None = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Gradient of a product's weight (dgp_gemm_wgrad): dC^T x, [N][K] row-major,
+    where C = x B^T had the operand X (and sX) and dC is [M][N] bfloat16 (any
+    row stride of whole 16 bytes).  With offsets (int32 [E + 1] on the device,
+    as gemm_preshuffle_grouped takes them) one gradient per expert, [E][N][K];
+    rows (int32 [M]) names the row of X for each row of dC.  out_dtype is
+    float32 (default, or out's) or bfloat16; accumulate adds to `out` (float32)."""
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
+    return _native().wgrad(dC, X, sX, scale_mode, offsets, rows, out, out_dtype == torch.bfloat16, accumulate, stream)
 
 
 def check_arch(name: str) -> bool:

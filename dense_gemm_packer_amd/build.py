@@ -22,8 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdgp.so")
 POISON_LIB = os.path.join(HERE, "libdgp_lds_poison.so")
 SOURCES = ["dgp_api.cpp", "packer.hip", "gemm_tiled.hip", "gemm_lds.hip", "gemm_stream.hip", "reduce.hip", "probe.hip", "noalloc.hip", "gemm_w4.hip", "gemm_wave.hip",
-           "quantize.hip"]
-HEADERS = ["common.h", "launch.h", "gemm_common.h"]
+           "quantize.hip", "layernorm.hip", "norm_backward.hip", "swiglu_backward.hip", "wgrad.hip"]
+HEADERS = ["common.h", "launch.h", "gemm_common.h", "operand.h", "norm.h"]
 ARCH = "gfx950"
 
 BINDING = os.path.join(HERE, "_binding.so")
@@ -37,7 +37,7 @@ CFLAGS = [
 # Keep MFMA accumulators in arch VGPRs (avoids accumulator copies at loop
 # latches) everywhere except in the kernels that need the AGPRs for them.
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-AGPR_ACC_SOURCES = {"gemm_lds.hip", "gemm_w4.hip"}
+AGPR_ACC_SOURCES = {"gemm_lds.hip", "gemm_w4.hip", "wgrad.hip"}
 
 
 def flags(src):

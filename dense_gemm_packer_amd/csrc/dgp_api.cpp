@@ -927,6 +927,149 @@ int amax_parts(int64_t M, int64_t K)
     return (int)(n < 1 ? 1 : n > kAmaxParts ? kAmaxParts : n);
 }
 
+// A norm's arguments (the layer norm's bias apart).
+dgp_status check_norm(const NormArgs &a, int x_type, int scale_mode)
+{
+    const int64_t M = a.M, K = a.K;
+    DGP_TRY(check_operand(x_type, M, K, scale_mode, true));
+    if (a.wt != x_type && a.wt != DGP_F32)
+        return fail(DGP_ERR_DTYPE, "weight type %d is neither X's type nor DGP_F32", a.wt);
+    if (!(a.eps >= 0.0f) || !(a.eps <= 3.0e38f))
+        return fail(DGP_ERR_SHAPE, "eps must be finite and not negative");
+    if (M == 0 || K == 0)
+        return DGP_OK;
+    DGP_TRY(check_rows(a.X, a.ldx, K, x_type, "X"));
+    if (a.R)
+        DGP_TRY(check_rows(a.R, a.ldr, K, x_type, "residual"));
+    if (!a.W)
+        return fail(DGP_ERR_NULL, "weight is NULL");
+    if (!aligned16(a.W) || !aligned16(a.H))
+        return fail(DGP_ERR_ALIGN, "weight and residual output must be 16-byte aligned");
+    if (scale_mode == DGP_SCALE_TENSOR && !a.scale)
+        return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
+    DGP_TRY(check_codes(a.Q, a.S, a.scale, scale_mode));
+    DGP_TRY(check_codes_apart(a.Q, a.S, a.scale, scale_mode, a.X, a.ldx, x_type, M, K, "X and Q or S"));
+    DGP_TRY(check_codes_apart(a.Q, a.S, a.scale, scale_mode, a.R, a.ldr, x_type, M, K, "residual and Q or S"));
+    const int64_t in = input_size(x_type);
+    DGP_TRY(check_apart(a.H, K * in, a.X, K * in, a.ldx * in, M, true, "X and residual output"));
+    DGP_TRY(check_apart(a.H, K * in, a.R, K * in, a.ldr * in, M, true, "residual and residual output"));
+    DGP_TRY(check_apart(a.H, K * in, a.Q, code_row(K, scale_mode), code_row(K, scale_mode), M, false, "Q and residual output"));
+    DGP_TRY(check_outputs_apart(a.Q, a.S, a.H, a.scale, scale_mode, x_type, M, K, a.W, K * input_size(a.wt), "weight and Q, S or residual output"));
+    DGP_TRY(check_outputs_apart(a.Q, a.S, a.H, a.scale, scale_mode, x_type, M, K, a.scale, 4, "the given scale and Q or residual output"));
+    return check_scales_apart(a.Q, a.S, a.H, a.scale, scale_mode, x_type, M, K);
+}
+
+// ------------------------------------------------------------- gradients
+
+// Types and sizes of a gradient whose kept activations have the form `mode`.
+dgp_status check_gradient(int type, int mode, int64_t M, int64_t K)
+{
+    if (!input_size(type))
+        return fail(DGP_ERR_DTYPE, "gradient type %d is not DGP_BF16, DGP_F16 or DGP_F32", type);
+    if (mode < DGP_SCALE_NONE || mode > DGP_SCALE_MX128)
+        return fail(DGP_ERR_SCALE_MODE, "scale mode %d is not one that a gradient reads", mode);
+    if (M < 0 || K < 0 || M > INT32_MAX / 2)
+        return fail(DGP_ERR_SHAPE, "M=%lld K=%lld", (long long)M, (long long)K);
+    if (K % (mode == DGP_SCALE_NONE ? 64 : 128) != 0)
+        return fail(DGP_ERR_SHAPE, "K=%lld is not a multiple of %d", (long long)K, mode == DGP_SCALE_NONE ? 64 : 128);
+    if (K * input_size(type) > kMaxRowBytes)
+        return fail(DGP_ERR_SHAPE, "rows of %lld bytes exceed %lld", (long long)(K * input_size(type)), (long long)kMaxRowBytes);
+    return DGP_OK;
+}
+
+// Bytes of an element of a kept activation, and of a row of its scales.
+int64_t kept_size(int type, int mode) { return mode == DGP_SCALE_NONE ? input_size(type) : 1; }
+
+// A kept activation: rows and, by mode, scales.
+dgp_status check_kept(const void *X, int64_t ldx, const void *S, int64_t lds, int type, int mode, int64_t K, const char *what)
+{
+    if (!X)
+        return fail(DGP_ERR_NULL, "%s is NULL", what);
+    if (ldx < K)
+        return fail(DGP_ERR_SHAPE, "%s: row stride %lld below K=%lld", what, (long long)ldx, (long long)K);
+    if (!aligned16(X) || (ldx * kept_size(type, mode)) % 16 != 0)
+        return fail(DGP_ERR_ALIGN, "%s: rows must be 16-byte aligned", what);
+    if (mode == DGP_SCALE_NONE)
+        return DGP_OK;
+    if (!S)
+        return fail(DGP_ERR_NULL, "%s: scales are NULL", what);
+    if (mode != DGP_SCALE_TENSOR && lds < K / 128)
+        return fail(DGP_ERR_SHAPE, "%s: scale stride %lld below K/128=%lld", what, (long long)lds, (long long)(K / 128));
+    if (mode != DGP_SCALE_MX128 && ((uintptr_t)S & 3u))
+        return fail(DGP_ERR_ALIGN, "%s: fp32 scales must be 4-byte aligned", what);
+    return DGP_OK;
+}
+
+// Bytes from the first scale of a kept activation to its last one's end.
+int64_t kept_scale_bytes(int64_t lds, int mode, int64_t M, int64_t K)
+{
+    return mode == DGP_SCALE_NONE ? 0 : mode == DGP_SCALE_TENSOR ? 4 : ((M - 1) * lds + K / 128) * (mode == DGP_SCALE_BLOCK128 ? 4 : 1);
+}
+
+// [out, out + out_bytes) against [in, in + in_bytes).
+dgp_status check_spans(const void *out, int64_t out_bytes, const void *in, int64_t in_bytes, const char *what)
+{
+    return check_apart(out_bytes ? out : nullptr, out_bytes, in_bytes ? in : nullptr, in_bytes, 0, 1, false, what);
+}
+
+dgp_status norm_backward(const NormGradArgs &a, int type, int mode, bool layer, size_t ws_bytes, hipStream_t stream)
+{
+    const int64_t M = a.M, K = a.K, size = input_size(type);
+    DGP_TRY(check_gradient(type, mode, M, K));
+    if (a.wt != type && a.wt != DGP_F32)
+        return fail(DGP_ERR_DTYPE, "weight type %d is neither the gradients' type nor DGP_F32", a.wt);
+    if (!(a.eps >= 0.0f) || !(a.eps <= 3.0e38f))
+        return fail(DGP_ERR_SHAPE, "eps must be finite and not negative");
+    if (K == 0)
+        return ok();
+    if (!a.dW)
+        return fail(DGP_ERR_NULL, "dW is NULL");
+    if (!aligned16(a.dW) || !aligned16(a.dB))
+        return fail(DGP_ERR_ALIGN, "dW and dB must be 16-byte aligned");
+    DGP_TRY(check_spans(a.dW, K * 4, a.dB, K * 4, "dW and dB"));
+    const size_t need = dgp_norm_backward_workspace_bytes(M, K, layer);
+    if (M > 0) {
+        DGP_TRY(check_rows(a.Y, a.ldy, K, type, "dY"));
+        DGP_TRY(check_kept(a.X, a.ldx, a.S, K / 128, type, mode, K, "X"));
+        if (a.R)
+            DGP_TRY(check_rows(a.R, a.ldr, K, type, "residual gradient"));
+        if (!a.W || !a.D)
+            return fail(DGP_ERR_NULL, "weight or dX is NULL");
+        if (!aligned16(a.W) || !aligned16(a.D))
+            return fail(DGP_ERR_ALIGN, "weight and dX must be 16-byte aligned");
+        if (need && !a.ws)
+            return fail(DGP_ERR_WORKSPACE, "a workspace of %zu bytes is needed", need);
+        if (!aligned16(a.ws))
+            return fail(DGP_ERR_ALIGN, "workspace is not 16-byte aligned");
+        if (ws_bytes < need)
+            return fail(DGP_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+        const int64_t row = K * size, kept = kept_size(type, mode);
+        // dX in place of dY, R or X: rows that are read whole before they are written
+        // (rows too long for that are read again)
+        DGP_TRY(check_apart(a.D, row, a.Y, row, a.ldy * size, M, norm_grad_in_place(K), "dY and dX"));
+        DGP_TRY(check_apart(a.D, row, a.R, row, a.ldr * size, M, true, "residual gradient and dX"));
+        DGP_TRY(check_apart(a.D, row, a.X, K * kept, a.ldx * kept, M, mode == DGP_SCALE_NONE && norm_grad_in_place(K), "X and dX"));
+        struct Span {
+            const void *p;
+            int64_t bytes;
+        };
+        const Span outs[] = {{a.D, M * row}, {a.dW, K * 4}, {a.dB, K * 4}, {a.ws, (int64_t)need}};
+        const Span ins[] = {{a.S, kept_scale_bytes(K / 128, mode, M, K)}, {a.W, K * input_size(a.wt)}};
+        const Span big[] = {{a.Y, ((M - 1) * a.ldy + K) * size}, {a.X, ((M - 1) * a.ldx + K) * kept}, {a.R, ((M - 1) * a.ldr + K) * size}};
+        for (const Span &o : outs)
+            for (const Span &i : ins)
+                DGP_TRY(check_spans(o.p, o.bytes, i.p, i.bytes, "an output and the weight or the scales"));
+        for (int o = 1; o < 4; ++o) {
+            for (const Span &i : big)
+                DGP_TRY(check_spans(outs[o].p, outs[o].bytes, i.p, i.bytes, "dW, dB or the workspace and an input"));
+            for (int q = 0; q < o; ++q)
+                DGP_TRY(check_spans(outs[o].p, outs[o].bytes, outs[q].p, outs[q].bytes, "two outputs, or one and the workspace,"));
+        }
+    }
+    DGP_TRY(check_device_arch());
+    return hip_status(launch_norm_grad(a, type, mode, layer, stream), "norm gradient launch");
+}
+
 }  // namespace
 
 // ====================================================================== ABI
@@ -1051,38 +1194,27 @@ dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64
                                 int w_type, float eps, void *Q, void *S, const float *scale, void *H, int64_t M,
                                 int64_t K, int scale_mode, void *stream)
 {
-    DGP_TRY(check_operand(x_type, M, K, scale_mode, true));
-    if (w_type != x_type && w_type != DGP_F32)
-        return fail(DGP_ERR_DTYPE, "weight type %d is neither X's type nor DGP_F32", w_type);
-    if (!(eps >= 0.0f) || !(eps <= 3.0e38f))
-        return fail(DGP_ERR_SHAPE, "eps must be finite and not negative");
+    const NormArgs a{X, R, W, nullptr, Q, S, H, scale, ldx, ldr, M, K, eps, w_type};
+    DGP_TRY(check_norm(a, x_type, scale_mode));
     if (M == 0 || K == 0)
         return ok();
-    DGP_TRY(check_rows(X, ldx, K, x_type, "X"));
-    if (R)
-        DGP_TRY(check_rows(R, ldr, K, x_type, "residual"));
-    if (!W)
-        return fail(DGP_ERR_NULL, "weight is NULL");
-    if (!aligned16(W) || !aligned16(H))
-        return fail(DGP_ERR_ALIGN, "weight and residual output must be 16-byte aligned");
-    if (scale_mode == DGP_SCALE_TENSOR && !scale)
-        return fail(DGP_ERR_NULL, "DGP_SCALE_TENSOR needs a given scale here");
-    DGP_TRY(check_codes(Q, S, scale, scale_mode));
-    DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, X, ldx, x_type, M, K, "X and Q or S"));
-    DGP_TRY(check_codes_apart(Q, S, scale, scale_mode, R, ldr, x_type, M, K, "residual and Q or S"));
-    const int64_t in = input_size(x_type);
-    DGP_TRY(check_apart(H, K * in, X, K * in, ldx * in, M, true, "X and residual output"));
-    DGP_TRY(check_apart(H, K * in, R, K * in, ldr * in, M, true, "residual and residual output"));
-    DGP_TRY(check_apart(H, K * in, Q, code_row(K, scale_mode), code_row(K, scale_mode), M, false, "Q and residual output"));
-    DGP_TRY(check_outputs_apart(Q, S, H, scale, scale_mode, x_type, M, K, W, K * input_size(w_type), "weight and Q, S or residual output"));
-    DGP_TRY(check_outputs_apart(Q, S, H, scale, scale_mode, x_type, M, K, scale, 4, "the given scale and Q or residual output"));
-    DGP_TRY(check_scales_apart(Q, S, H, scale, scale_mode, x_type, M, K));
     DGP_TRY(check_device_arch());
-    NormArgs a{};
-    a.X = X, a.R = R, a.W = W, a.Q = Q, a.S = S, a.H = H, a.scale = scale;
-    a.ldx = ldx, a.ldr = ldr, a.M = M, a.K = K;
-    a.eps = eps, a.wt = w_type;
     return hip_status(launch_rmsnorm(a, x_type, scale_mode, (hipStream_t)stream), "norm launch");
+}
+
+dgp_status dgp_layernorm_quantize(const void *X, int64_t ldx, const void *R, int64_t ldr, int x_type, const void *W,
+                                  const void *B, int w_type, float eps, void *Q, void *S, const float *scale, void *H,
+                                  int64_t M, int64_t K, int scale_mode, void *stream)
+{
+    const NormArgs a{X, R, W, B, Q, S, H, scale, ldx, ldr, M, K, eps, w_type};
+    DGP_TRY(check_norm(a, x_type, scale_mode));
+    if (M == 0 || K == 0)
+        return ok();
+    if (!aligned16(B))
+        return fail(DGP_ERR_ALIGN, "bias must be 16-byte aligned");
+    DGP_TRY(check_outputs_apart(Q, S, H, scale, scale_mode, x_type, M, K, B, K * input_size(w_type), "bias and Q, S or residual output"));
+    DGP_TRY(check_device_arch());
+    return hip_status(launch_layernorm(a, x_type, scale_mode, (hipStream_t)stream), "layer norm launch");
 }
 
 dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_t ldu, int x_type, void *Q, void *S,
@@ -1105,6 +1237,146 @@ dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_
     a.X = G, a.U = U, a.Q = Q, a.S = S, a.scale = scale;
     a.ldx = ldg, a.ldu = ldu, a.M = M, a.K = K;
     return hip_status(launch_row_quant(a, x_type, scale_mode, true, (hipStream_t)stream), "gated activation launch");
+}
+
+size_t dgp_norm_backward_workspace_bytes(int64_t M, int64_t K, int layer)
+{
+    return M > 0 && K > 0 ? norm_grad_workspace_bytes(M, K, layer != 0) : 0;
+}
+
+dgp_status dgp_layernorm_backward(const void *dY, int64_t ldy, int type, const void *X, int64_t ldx, const void *S,
+                                  int scale_mode, const void *W, int w_type, const void *R, int64_t ldr, float eps,
+                                  void *dX, float *dW, float *dB, int64_t M, int64_t K, float *ws, size_t ws_bytes,
+                                  void *stream)
+{
+    const NormGradArgs a{dY, X, S, W, R, dX, dW, dB, ws, ldy, ldx, ldr, M, K, eps, w_type};
+    return norm_backward(a, type, scale_mode, true, ws_bytes, (hipStream_t)stream);
+}
+
+dgp_status dgp_rmsnorm_backward(const void *dY, int64_t ldy, int type, const void *X, int64_t ldx, const void *S,
+                                int scale_mode, const void *W, int w_type, const void *R, int64_t ldr, float eps,
+                                void *dX, float *dW, int64_t M, int64_t K, float *ws, size_t ws_bytes, void *stream)
+{
+    const NormGradArgs a{dY, X, S, W, R, dX, dW, nullptr, ws, ldy, ldx, ldr, M, K, eps, w_type};
+    return norm_backward(a, type, scale_mode, false, ws_bytes, (hipStream_t)stream);
+}
+
+dgp_status dgp_swiglu_backward(const void *dY, int64_t ldy, int type, const void *G, int64_t ldg, const void *U, int64_t ldu,
+                               const void *SG, int64_t ldsg, const void *SU, int64_t ldsu, int scale_mode, void *D,
+                               int64_t M, int64_t K, void *stream)
+{
+    DGP_TRY(check_gradient(type, scale_mode, M, K));
+    if (M == 0 || K == 0)
+        return ok();
+    DGP_TRY(check_rows(dY, ldy, K, type, "dY"));
+    DGP_TRY(check_kept(G, ldg, SG, ldsg, type, scale_mode, K, "gate"));
+    DGP_TRY(check_kept(U, ldu, SU, ldsu, type, scale_mode, K, "up"));
+    if (!D)
+        return fail(DGP_ERR_NULL, "D is NULL");
+    if (!aligned16(D))
+        return fail(DGP_ERR_ALIGN, "D is not 16-byte aligned");
+    const int64_t size = input_size(type), kept = kept_size(type, scale_mode), out = M * 2 * K * size;
+    // gate and up side by side, replaced by their gradients: every thread reads what it writes over
+    const bool same = scale_mode == DGP_SCALE_NONE && D == G && U == (const uint8_t *)G + K * size && (M == 1 || (ldg == 2 * K && ldu == 2 * K));
+    if (!same) {
+        DGP_TRY(check_spans(D, out, G, ((M - 1) * ldg + K) * kept, "gate and D"));
+        DGP_TRY(check_spans(D, out, U, ((M - 1) * ldu + K) * kept, "up and D"));
+    }
+    DGP_TRY(check_spans(D, out, dY, ((M - 1) * ldy + K) * size, "dY and D"));
+    DGP_TRY(check_spans(D, out, SG, kept_scale_bytes(ldsg, scale_mode, M, K), "the gate's scales and D"));
+    DGP_TRY(check_spans(D, out, SU, kept_scale_bytes(ldsu, scale_mode, M, K), "up's scales and D"));
+    DGP_TRY(check_device_arch());
+    const SwigluGradArgs a{dY, G, U, SG, SU, D, ldy, ldg, ldu, ldsg, ldsu, M, K};
+    return hip_status(launch_swiglu_grad(a, type, scale_mode, (hipStream_t)stream), "gated activation gradient launch");
+}
+
+size_t dgp_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || E <= 0)
+        return 0;
+    const int splits = wgrad_plan(M, N, K, E).splits;
+    return splits > 1 ? (size_t)splits * (size_t)E * (size_t)N * (size_t)K * sizeof(float) : 0;
+}
+
+dgp_status dgp_gemm_wgrad(const void *dC, int64_t ldc, const void *X, int64_t x_rows, int dtype, const void *S,
+                          int scale_mode, void *dB, int out_type, int accumulate, int64_t M, int64_t N, int64_t K,
+                          int64_t E, const int32_t *offsets, const int32_t *rows, float *ws, size_t ws_bytes,
+                          void *stream)
+{
+    if (dtype != DGP_BF16 && dtype != DGP_FP8_E4M3)
+        return fail(DGP_ERR_DTYPE, "dtype %d is not DGP_BF16 or DGP_FP8_E4M3", dtype);
+    if (out_type != DGP_BF16 && out_type != DGP_F32)
+        return fail(DGP_ERR_DTYPE, "output type %d is not DGP_BF16 or DGP_F32", out_type);
+    if (scale_mode < DGP_SCALE_NONE || scale_mode > DGP_SCALE_MX128 || (scale_mode == DGP_SCALE_NONE) != (dtype == DGP_BF16))
+        return fail(DGP_ERR_SCALE_MODE, "scale mode %d does not go with dtype %d here", scale_mode, dtype);
+    if (accumulate != 0 && (accumulate != 1 || out_type != DGP_F32))
+        return fail(DGP_ERR_DTYPE, "accumulate is 0, or 1 with DGP_F32");
+    const int64_t step = dtype == DGP_BF16 ? 64 : 128, size = dtype == DGP_BF16 ? 2 : 1, csize = out_type == DGP_F32 ? 4 : 2;
+    if (M < 0 || N < 0 || K < 0 || E < 0 || x_rows < 0 || M > INT32_MAX / 2 || N > (1 << 22) || K > (1 << 22) || E > 65535)
+        return fail(DGP_ERR_SHAPE, "M=%lld N=%lld K=%lld E=%lld", (long long)M, (long long)N, (long long)K, (long long)E);
+    if (N % 16 != 0 || K % step != 0)
+        return fail(DGP_ERR_SHAPE, "N=%lld is not a multiple of 16, or K=%lld of %lld", (long long)N, (long long)K, (long long)step);
+    if (N == 0 || K == 0 || E == 0)
+        return ok();
+    if (!offsets && E != 1)
+        return fail(DGP_ERR_NULL, "E=%lld weights need offsets", (long long)E);
+    if (rows && !offsets)
+        return fail(DGP_ERR_NULL, "a row list needs offsets");
+    if (((uintptr_t)offsets | (uintptr_t)rows) & 3u)
+        return fail(DGP_ERR_ALIGN, "offsets and rows must be 4-byte aligned");
+    if (!dB)
+        return fail(DGP_ERR_NULL, "dB is NULL");
+    if (!aligned16(dB))
+        return fail(DGP_ERR_ALIGN, "dB is not 16-byte aligned");
+    if (M > 0) {
+        if (!dC || !X)
+            return fail(DGP_ERR_NULL, "dC or X is NULL");
+        if (ldc < N || ldc > (1 << 25))
+            return fail(DGP_ERR_SHAPE, "row stride %lld of dC, N=%lld", (long long)ldc, (long long)N);
+        if (!aligned16(dC) || !aligned16(X) || ldc % 8 != 0)
+            return fail(DGP_ERR_ALIGN, "rows of dC and X must be 16-byte aligned");
+        if (rows ? x_rows < 1 : x_rows < M)
+            return fail(DGP_ERR_SHAPE, "X has %lld rows, dC %lld", (long long)x_rows, (long long)M);
+        if (rows && (x_rows > INT32_MAX / 2 || x_rows * K * size > (int64_t)0xFF000000))
+            return fail(DGP_ERR_SHAPE, "with a row list X must be at most %lld bytes", (long long)0xFF000000);
+        if (scale_mode != DGP_SCALE_NONE && !S)
+            return fail(DGP_ERR_NULL, "scales are NULL");
+        if ((scale_mode == DGP_SCALE_TENSOR || scale_mode == DGP_SCALE_BLOCK128) && ((uintptr_t)S & 3u))
+            return fail(DGP_ERR_ALIGN, "fp32 scales must be 4-byte aligned");
+    }
+    const WgradPlan plan = M > 0 ? wgrad_plan(M, N, K, E) : WgradPlan{128, 1};
+    const size_t need = dgp_wgrad_workspace_bytes(M, N, K, E);
+    if (need && !ws)
+        return fail(DGP_ERR_WORKSPACE, "a workspace of %zu bytes is needed", need);
+    if (!aligned16(ws))
+        return fail(DGP_ERR_ALIGN, "workspace is not 16-byte aligned");
+    if (ws_bytes < need)
+        return fail(DGP_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+    const int64_t tiles = ((N + plan.tile - 1) / plan.tile) * ((K + plan.tile - 1) / plan.tile) * E * plan.splits;
+    if (tiles > UINT32_MAX / 256)
+        return fail(DGP_ERR_SHAPE, "too many %d x %d tiles", plan.tile, plan.tile);
+    const int64_t out = E * N * K * csize, used = rows ? x_rows : M;
+    struct Span {
+        const void *p;
+        int64_t bytes;
+    };
+    const Span ins[] = {{M > 0 ? dC : nullptr, M > 0 ? ((M - 1) * ldc + N) * 2 : 0},
+                        {X, used * K * size},
+                        {S, used > 0 ? kept_scale_bytes(K / 128, scale_mode, used, K) : 0},
+                        {offsets, (E + 1) * 4},
+                        {rows, M * 4}};
+    for (const Span &i : ins) {
+        DGP_TRY(check_spans(dB, out, i.p, i.bytes, "dB and an input"));
+        DGP_TRY(check_spans(ws, (int64_t)need, i.p, i.bytes, "the workspace and an input"));
+    }
+    DGP_TRY(check_spans(ws, (int64_t)need, dB, out, "the workspace and dB"));
+    DGP_TRY(check_device_arch());
+    WgradArgs a{};
+    a.Y = dC, a.X = X, a.S = S, a.C = dB, a.ws = ws;
+    a.offsets = offsets, a.rows = M > 0 ? rows : nullptr;
+    a.ldy = ldc, a.M = M, a.N = N, a.K = K, a.E = E, a.x_rows = x_rows;
+    a.accumulate = accumulate;
+    return hip_status(launch_wgrad(a, scale_mode, out_type == DGP_BF16, plan, (hipStream_t)stream), "weight gradient launch");
 }
 
 dgp_status dgp_gemm_preshuffle_grouped(const void *A, int64_t a_rows, const void *Bs, void *C, int64_t M, int64_t N,

@@ -117,12 +117,59 @@ struct WeightQuantArgs {
 };
 struct NormArgs {
     const void *X, *R, *W;  // R: residual or NULL, rows ldr apart
+    const void *B;          // the layer norm's bias (W's type) or NULL
     void *Q, *S, *H;        // H: the residual stream's new value ([M][K]) or NULL
     const float *scale;
     int64_t ldx, ldr, M, K;
     float eps;
     int wt;                 // W's type: X's or kTypeF32
 };
+
+// Gradients (norm_backward.hip, swiglu_backward.hip).  Types are kDtypeBf16,
+// kTypeF16 or kTypeF32; a kept input X has the gradients' type (mode
+// kScaleNone) or e4m3 codes with the scales of its mode.
+struct NormGradArgs {
+    const void *Y;          // the output's gradient, rows ldy apart
+    const void *X, *S;      // the norm's input, rows ldx apart, and its scales
+    const void *W;
+    const void *R;          // a gradient to add (rows ldr apart) or NULL
+    void *D;                // [M][K]
+    float *dW, *dB;         // [K]; dB (layer norm) or NULL
+    float *ws;              // norm_grad_workspace_bytes
+    int64_t ldy, ldx, ldr, M, K;
+    float eps;
+    int wt;                 // W's type: Y's or kTypeF32
+};
+struct SwigluGradArgs {
+    const void *Y;          // the output's gradient, rows ldy apart
+    const void *G, *U;      // gate and up, rows ldg and ldu apart
+    const void *SG, *SU;    // their scales, block rows ldsg and ldsu apart
+    void *D;                // [M][2 K]: the gate's gradient, then up's
+    int64_t ldy, ldg, ldu, ldsg, ldsu, M, K;
+};
+size_t norm_grad_workspace_bytes(int64_t M, int64_t K, bool layer);
+bool norm_grad_in_place(int64_t K);   // a row is read once, before it is written
+hipError_t launch_norm_grad(const NormGradArgs &a, int type, int mode, bool layer, hipStream_t s);
+hipError_t launch_swiglu_grad(const SwigluGradArgs &a, int type, int mode, hipStream_t s);
+
+// A weight's gradient (wgrad.hip): C[e] = Y[rows of e]^T X[rows of e].
+struct WgradArgs {
+    const void *Y;          // [M][N] bf16, rows ldy elements apart
+    const void *X;          // [x_rows][K] bf16 or e4m3
+    const void *S;          // X's scales
+    void *C;                // [E][N][K], fp32 or bf16
+    float *ws;              // splits > 1: [splits][E][N][K]
+    const int32_t *offsets; // [E + 1] or NULL (one group of M rows)
+    const int32_t *rows;    // row of X of each row of Y, or NULL (row m takes row m)
+    int64_t ldy, M, N, K, E, x_rows;
+    int splits, accumulate;
+};
+struct WgradPlan {
+    int tile;               // n and k of a workgroup's tile: 256 or 128
+    int splits;             // parts of a group's rows
+};
+WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K, int64_t E);
+hipError_t launch_wgrad(const WgradArgs &a, int mode, bool out_bf16, const WgradPlan &plan, hipStream_t s);
 constexpr int kAmaxParts = 256;   // most partial maxima per matrix
 hipError_t launch_row_quant(const RowQuantArgs &a, int x_type, int mode, bool gated, hipStream_t s);
 bool small_tensor(int64_t M, int64_t K);   // measured per-tensor scale in one launch
@@ -131,6 +178,7 @@ hipError_t launch_amax(const void *X, int64_t ldx, int x_type, int64_t groups, i
                        uint32_t *parts, hipStream_t s);
 hipError_t launch_quantize_b(const WeightQuantArgs &a, int x_type, int mode, hipStream_t s);
 hipError_t launch_rmsnorm(const NormArgs &a, int x_type, int mode, hipStream_t s);
+hipError_t launch_layernorm(const NormArgs &a, int x_type, int mode, hipStream_t s);
 
 // Probes (probe.hip).
 hipError_t launch_probe_mfma(int which, const void *a, const void *b, float *out, hipStream_t s);

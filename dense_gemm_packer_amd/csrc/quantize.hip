@@ -22,226 +22,12 @@
 // above every finite value.
 #include "common.h"
 #include "launch.h"
+#include "norm.h"
+#include "operand.h"
 
 namespace dgp {
 
 namespace {
-
-constexpr float kTop = 448.0f;                 // largest e4m3 value
-constexpr uint32_t kInfBits = 0x7F800000u;
-
-// ------------------------------------------------------------ input loads
-
-// 8 consecutive elements in flight: their 16 (bf16, fp16) or 32 (fp32) bytes.
-template <int XT>
-struct Raw8 {
-    i32x4 v[XT == kTypeF32 ? 2 : 1];
-};
-
-template <int XT>
-__device__ inline Raw8<XT> load_raw8(const void *base, int64_t elem)
-{
-    Raw8<XT> r;
-    const i32x4 *p = reinterpret_cast<const i32x4 *>(static_cast<const uint8_t *>(base) + elem * (XT == kTypeF32 ? 4 : 2));
-    r.v[0] = p[0];
-    if constexpr (XT == kTypeF32)
-        r.v[1] = p[1];
-    return r;
-}
-
-template <int XT>
-__device__ inline void to_float8(const Raw8<XT> &r, float (&x)[8])
-{
-    if constexpr (XT == kTypeF32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = __builtin_bit_cast(float, (int)r.v[i / 4][i % 4]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = (uint32_t)r.v[0][i];
-            if constexpr (XT == kDtypeBf16) {
-                x[2 * i] = __builtin_bit_cast(float, w << 16);
-                x[2 * i + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
-            } else {
-                x[2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)w);
-                x[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
-            }
-        }
-    }
-}
-
-template <int XT>
-__device__ inline void store8(void *base, int64_t elem, const float (&x)[8])
-{
-    i32x4 *p = reinterpret_cast<i32x4 *>(static_cast<uint8_t *>(base) + elem * (XT == kTypeF32 ? 4 : 2));
-    if constexpr (XT == kTypeF32) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            p[h] = __builtin_bit_cast(i32x4, f32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]});
-    } else {
-        i32x4 v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (XT == kDtypeBf16) {
-                v[i] = (int)pack_bf16x2(x[2 * i], x[2 * i + 1]);
-            } else {
-                const uint16_t lo = __builtin_bit_cast(uint16_t, (_Float16)x[2 * i]);
-                const uint16_t hi = __builtin_bit_cast(uint16_t, (_Float16)x[2 * i + 1]);
-                v[i] = (int)((uint32_t)lo | ((uint32_t)hi << 16));
-            }
-        }
-        *p = v;
-    }
-}
-
-// ------------------------------------------------------- block reductions
-
-__device__ inline uint32_t mag_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu; }
-__device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
-template <int N>
-__device__ inline uint32_t amax_bits(const float (&x)[N])
-{
-    uint32_t m = mag_bits(x[0]);
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-        m = umax(m, mag_bits(x[i]));
-    return m;
-}
-
-template <int CTRL>
-__device__ inline uint32_t dpp(uint32_t v)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
-}
-constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kRowHalfMirror = 0x141, kRowMirror = 0x140;
-
-// Maximum over groups of 4 or 16 consecutive lanes, in every lane of them.
-__device__ inline uint32_t max4(uint32_t m)
-{
-    m = umax(m, dpp<kQuadXor1>(m));
-    return umax(m, dpp<kQuadXor2>(m));
-}
-__device__ inline uint32_t max16(uint32_t m)
-{
-    m = max4(m);
-    m = umax(m, dpp<kRowHalfMirror>(m));
-    return umax(m, dpp<kRowMirror>(m));
-}
-__device__ inline uint32_t max64(uint32_t m)
-{
-    m = max16(m);
-    m = umax(m, (uint32_t)__shfl_xor((int)m, 16));
-    return umax(m, (uint32_t)__shfl_xor((int)m, 32));
-}
-__device__ inline float fdpp_add(float s, uint32_t other) { return s + __builtin_bit_cast(float, other); }
-__device__ inline float sum64(float s)
-{
-    s = fdpp_add(s, dpp<kQuadXor1>(__builtin_bit_cast(uint32_t, s)));
-    s = fdpp_add(s, dpp<kQuadXor2>(__builtin_bit_cast(uint32_t, s)));
-    s = fdpp_add(s, dpp<kRowHalfMirror>(__builtin_bit_cast(uint32_t, s)));
-    s = fdpp_add(s, dpp<kRowMirror>(__builtin_bit_cast(uint32_t, s)));
-    s += __shfl_xor(s, 16);
-    return s + __shfl_xor(s, 32);
-}
-
-// ----------------------------------------------------------------- scales
-
-// fp32 scale of a block (NaN for a block that is not finite).
-__device__ inline float scale_f32(uint32_t amax)
-{
-    if (amax >= kInfBits)
-        return __builtin_bit_cast(float, 0x7FC00000u);
-    return __builtin_fmaxf(__builtin_bit_cast(float, amax) / kTop, 0x1p-126f);
-}
-
-// E8M0 byte of a block: 448 = 1.75 * 2^8, so a mantissa above 1.75 (bits
-// above 0x600000) carries into the exponent before 8 is taken off; 6 = 1.5 *
-// 2^2, floor(log2) is the exponent itself.
-template <int MODE>
-__device__ inline int scale_e8m0(uint32_t amax)
-{
-    if (amax >= kInfBits)
-        return 255;
-    const int e = MODE == kScaleMx32 ? (int)(amax >> 23) - 2 : (int)((amax + 0x1FFFFFu) >> 23) - 8;
-    return e > 0 ? e : 0;
-}
-
-// 2^(127 - e), what the block is multiplied by (e <= 253: a normal number);
-// NaN for e = 255.
-__device__ inline float e8m0_multiplier(int e)
-{
-    return __builtin_bit_cast(float, e == 255 ? 0x7FC00000u : (uint32_t)(254 - e) << 23);
-}
-
-// ------------------------------------------------------------------ codes
-
-// 4 values -> 4 e4m3 codes (round to nearest even).  SAT: values above 448
-// saturate (a NaN stays one); without it the caller's scale rules them out.
-template <bool SAT>
-__device__ inline uint32_t pack_e4m3(float a, float b, float c, float d)
-{
-    if constexpr (SAT) {
-        auto sat = [](float v) { v = v > kTop ? kTop : v; return v < -kTop ? -kTop : v; };
-        a = sat(a), b = sat(b), c = sat(c), d = sat(d);
-    }
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-}
-
-// 8 values -> 8 E2M1 codes, element 0 in the lowest nibble; |v| saturates
-// at 6 (round to nearest even).
-__device__ inline uint32_t pack_e2m1(const float *v)
-{
-    float c[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        c[i] = __builtin_amdgcn_fmed3f(v[i], -6.0f, 6.0f);
-    uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, c[0], c[1], 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c[2], c[3], 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c[4], c[5], 1.0f, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c[6], c[7], 1.0f, 3);
-}
-
-// Codes and scale of 8 elements y of a row whose block is the 16 (128
-// blocks) or 4 (32 blocks) consecutive lanes around this one; `idx` = the
-// element's index / 8 in the output.  tmul: the per-tensor multiplier 1/s.
-template <int MODE, bool SAT>
-__device__ inline void emit8(const float (&y)[8], int64_t idx, void *Q, void *S, float tmul)
-{
-    if constexpr (MODE == kScaleNone) {
-        store8<kDtypeBf16>(Q, idx * 8, y);
-    } else if constexpr (MODE == kScaleMx32) {
-        const uint32_t m = max4(amax_bits(y));
-        const int e = scale_e8m0<MODE>(m);
-        const float f = e8m0_multiplier(e);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = y[i] * f;
-        static_cast<uint32_t *>(Q)[idx] = e == 255 ? 0u : pack_e2m1(v);
-        if ((threadIdx.x & 3) == 0)
-            static_cast<uint8_t *>(S)[idx >> 2] = (uint8_t)e;
-    } else {
-        float f = tmul;
-        if constexpr (MODE == kScaleBlock) {
-            const float s = scale_f32(max16(amax_bits(y)));
-            f = 1.0f / s;
-            if ((threadIdx.x & 15) == 0)
-                static_cast<float *>(S)[idx >> 4] = s;
-        } else if constexpr (MODE == kScaleMx) {
-            const int e = scale_e8m0<MODE>(max16(amax_bits(y)));
-            f = e8m0_multiplier(e);
-            if ((threadIdx.x & 15) == 0)
-                static_cast<uint8_t *>(S)[idx >> 4] = (uint8_t)e;
-        }
-        u32x2 w;
-        w.x = pack_e4m3<SAT>(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
-        w.y = pack_e4m3<SAT>(y[4] * f, y[5] * f, y[6] * f, y[7] * f);
-        static_cast<u32x2 *>(Q)[idx] = w;
-    }
-}
 
 // silu(g) * u = g / (1 + exp(-g)) * u, for g >= -80: 1 + exp(-g) and its
 // reciprocal (which gives no subnormal numbers) stay in the normal range.
@@ -566,99 +352,6 @@ __global__ __launch_bounds__(MODE == kScaleBlock ? 512 : 256) void quantize_b_ke
     }
 }
 
-// ------------------------------------------------------------------- norm
-
-// y = h / sqrt(mean(h^2) + eps) * w with h = x (+ residual), the sum taken
-// and kept in fp32; the residual stream is written back in the input's type.
-// T threads own a row (256 / T rows per workgroup where T < 256), C pieces of
-// 8 elements each, kept in registers between the two uses.  C = 0: rows longer
-// than the registers hold are read again for the second use.  HBM-bound: each
-// input is read and each output written once (4096 x 8192 bf16 with residual,
-// e4m3 codes and fp32 block scales: 235 MB in 47 us, 5.0 TB/s, the rate of a
-// copy; one row of 7168 to mxfp8: 3.1 us, the latency of one workgroup).
-template <int XT, int MODE, int T, int C>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(const NormArgs a)
-{
-    constexpr int kThreads = T < 256 ? 256 : T;
-    constexpr int kWaves = T / 64;
-    const int t = threadIdx.x % T;
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / T) + threadIdx.x / T;
-    if (T < 256 && row >= a.M)       // whole waves; no barrier follows for T = 64
-        return;
-    const int k8 = (int)(a.K / 8);
-    auto load_h = [&](int c, float(&h)[8]) {
-        to_float8<XT>(load_raw8<XT>(a.X, row * a.ldx + c * 8), h);
-        if (a.R) {
-            float r[8];
-            to_float8<XT>(load_raw8<XT>(a.R, row * a.ldr + c * 8), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h[i] += r[i];
-        }
-    };
-    float h[C > 0 ? C : 1][8];
-    float ss = 0.0f;
-    if constexpr (C > 0) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (t + c * T < k8)
-                load_h(t + c * T, h[c]);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (t + c * T < k8) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    ss = __builtin_fmaf(h[c][i], h[c][i], ss);
-            }
-    } else {
-        for (int c = t; c < k8; c += T) {
-            load_h(c, h[0]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                ss = __builtin_fmaf(h[0][i], h[0][i], ss);
-        }
-    }
-    ss = sum64(ss);
-    if constexpr (kWaves > 1) {
-        __shared__ float red[kWaves];
-        if ((threadIdx.x & 63) == 0)
-            red[threadIdx.x >> 6] = ss;
-        __syncthreads();
-        ss = red[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w)
-            ss += red[w];
-    }
-    const float rstd = 1.0f / __builtin_sqrtf(ss / (float)a.K + a.eps);
-    float tmul = 1.0f;
-    if constexpr (MODE == kScaleTensor)
-        tmul = 1.0f / a.scale[0];
-    auto finish = [&](int c, float(&v)[8]) {
-        if (a.H)
-            store8<XT>(a.H, row * a.K + c * 8, v);
-        float w[8];
-        if (a.wt == kTypeF32)
-            to_float8<kTypeF32>(load_raw8<kTypeF32>(a.W, (int64_t)c * 8), w);
-        else
-            to_float8<XT>(load_raw8<XT>(a.W, (int64_t)c * 8), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = v[i] * rstd * w[i];
-        emit8<MODE, MODE == kScaleTensor>(v, row * (int64_t)k8 + c, a.Q, a.S, tmul);
-    };
-    if constexpr (C > 0) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (t + c * T < k8)
-                finish(t + c * T, h[c]);
-    } else {
-        for (int c = t; c < k8; c += T) {
-            load_h(c, h[0]);
-            finish(c, h[0]);
-        }
-    }
-}
-
 // --------------------------------------------------------------- launches
 
 template <int XT, int MODE, bool GATED>
@@ -771,82 +464,9 @@ hipError_t launch_quantize_b(const WeightQuantArgs &a, int x_type, int mode, hip
     }
 }
 
-template <int XT, int MODE, int T, int C>
-static void launch_norm_rows(const NormArgs &a, hipStream_t s)
-{
-    constexpr int kThreads = T < 256 ? 256 : T, kRows = kThreads / T;
-    constexpr int kIn = XT == kTypeF32 ? 4 : 2;
-    // Slabs of rows whose threads fit the 32 bits of a launch.
-    constexpr int64_t slab = (int64_t(1) << 31) / T;
-    const int64_t qrow = MODE == kScaleNone ? 2 * a.K : MODE == kScaleMx32 ? a.K / 2 : a.K;
-    const int64_t srow = MODE == kScaleBlock ? a.K / 128 * 4 : MODE == kScaleMx ? a.K / 128 : MODE == kScaleMx32 ? a.K / 32 : 0;
-    for (int64_t r = 0; r < a.M; r += slab) {
-        NormArgs b = a;
-        b.M = a.M - r < slab ? a.M - r : slab;
-        b.X = static_cast<const uint8_t *>(a.X) + r * a.ldx * kIn;
-        if (a.R)
-            b.R = static_cast<const uint8_t *>(a.R) + r * a.ldr * kIn;
-        if (a.H)
-            b.H = static_cast<uint8_t *>(a.H) + r * a.K * kIn;
-        b.Q = static_cast<uint8_t *>(a.Q) + r * qrow;
-        if (srow)
-            b.S = static_cast<uint8_t *>(a.S) + r * srow;
-        rmsnorm_kernel<XT, MODE, T, C><<<(unsigned)((b.M + kRows - 1) / kRows), kThreads, 0, s>>>(b);
-    }
-}
-
-// Threads per row and pieces per thread by the row's length: one or two pieces
-// each keep the row's latency short and leave registers for many workgroups
-// (us for rows of bf16 with a residual, fp32 block scales out; "a/b" = T/C):
-//   1024: 256/1 2.6 and 64/2 3.2 for one row, 61 and 54 for 39 062
-//   2048: 256/1 2.7, 14.2, 51 for 1, 4096, 19 531 rows (64/4: 16.3, 61 for the latter two)
-//   4096: 512/1 2.9, 25.0, 51 for 1, 4096, 9765 rows (1024/1: 2.9, 30, 66)
-//   7168: 1024/1 3.3, 5.2, 9.6 and 512/2 3.6, 5.6, 9.0 for 1, 256, 600 rows
-//   (4096 x 8192: 512/2 47.2, 256/4 52.8)
-// Just past a border up to half of the threads hold nothing (1237 x 2112 fp16 to
-// bf16, 264 pieces on 512 threads: 4.3 us where a copy's rate gives 2.1).  fp32
-// rows and other outputs take the same rule, which was not measured on them.
-template <int XT, int MODE>
-static void launch_norm(const NormArgs &a, hipStream_t s)
-{
-    const int64_t k8 = a.K / 8;
-    if (k8 <= 64)
-        launch_norm_rows<XT, MODE, 64, 1>(a, s);
-    else if (k8 <= 128 && a.M > 8192)
-        launch_norm_rows<XT, MODE, 64, 2>(a, s);
-    else if (k8 <= 256)
-        launch_norm_rows<XT, MODE, 256, 1>(a, s);
-    else if (k8 <= 512)
-        launch_norm_rows<XT, MODE, 512, 1>(a, s);
-    else if (k8 <= 1024 && a.M > 384)
-        launch_norm_rows<XT, MODE, 512, 2>(a, s);
-    else if (k8 <= 1024)
-        launch_norm_rows<XT, MODE, 1024, 1>(a, s);
-    else if (k8 <= 4096)
-        launch_norm_rows<XT, MODE, 1024, 4>(a, s);
-    else
-        launch_norm_rows<XT, MODE, 1024, 0>(a, s);
-}
-
 hipError_t launch_rmsnorm(const NormArgs &a, int x_type, int mode, hipStream_t s)
 {
-    auto typed = [&](auto xt) {
-        constexpr int XT = decltype(xt)::value;
-        switch (mode) {
-        case kScaleNone: launch_norm<XT, kScaleNone>(a, s); return hipGetLastError();
-        case kScaleTensor: launch_norm<XT, kScaleTensor>(a, s); return hipGetLastError();
-        case kScaleBlock: launch_norm<XT, kScaleBlock>(a, s); return hipGetLastError();
-        case kScaleMx: launch_norm<XT, kScaleMx>(a, s); return hipGetLastError();
-        case kScaleMx32: launch_norm<XT, kScaleMx32>(a, s); return hipGetLastError();
-        default: return hipErrorInvalidValue;
-        }
-    };
-    switch (x_type) {
-    case kDtypeBf16: return typed(std::integral_constant<int, kDtypeBf16>{});
-    case kTypeF16: return typed(std::integral_constant<int, kTypeF16>{});
-    case kTypeF32: return typed(std::integral_constant<int, kTypeF32>{});
-    default: return hipErrorInvalidValue;
-    }
+    return launch_norm_typed<false>(a, x_type, mode, s);
 }
 
 }  // namespace dgp

@@ -1,0 +1,119 @@
+// Gradient of the gated activation (dgp_swiglu_backward).  With s = 1 / (1 +
+// exp(-g)), y = g s u, so
+//
+//   dg = dy u s (1 + g (1 - s)),   du = dy g s.
+//
+// 1 - s is exp(-g) s, which keeps its digits where s is near 1.  All arithmetic
+// is fp32, rounded once to the gradients' type.
+#include "common.h"
+#include "launch.h"
+#include "operand.h"
+
+namespace dgp {
+
+namespace {
+
+// For g >= -80 (see kFar).  exp(-g) is infinite nowhere in that range.
+__device__ inline void grads(float dy, float g, float u, float &dg, float &du)
+{
+    const float e = __expf(-g), s = __builtin_amdgcn_rcpf(1.0f + e);
+    const float a = dy * s;
+    dg = a * u * __builtin_fmaf(g, e * s, 1.0f);
+    du = a * g;
+}
+
+// Gates below -80: there s is exp(g) and 1 - s is 1 to 2^-115; exp(g) goes in
+// as four factors exp(g / 4), so that no product leaves the normal range
+// before the results do.
+constexpr uint32_t kFar = 0xC2A00000u;     // -80.0f; more negative numbers have larger bits
+
+template <int XT, int MODE>
+__device__ inline void grads8(const float (&dy)[8], const float (&g)[8], const float (&u)[8], float (&dg)[8], float (&du)[8])
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        top = umax(top, __builtin_bit_cast(uint32_t, g[i]));
+        grads(dy[i], g[i], u[i], dg[i], du[i]);
+    }
+    if (top > kFar) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = __expf(0.25f * g[i]);
+            const bool far = g[i] < -80.0f;
+            dg[i] = far ? (1.0f + g[i]) * q * dy[i] * q * u[i] * q * q : dg[i];
+            du[i] = far ? g[i] * q * dy[i] * q * q * q : du[i];
+        }
+    }
+}
+
+}  // namespace
+
+// Thread = 8 consecutive elements of dy, gate and up.  HBM-bound: reads each
+// once, writes both gradients once.
+template <int XT, int MODE>
+__global__ __launch_bounds__(256) void swiglu_grad_kernel(const SwigluGradArgs a)
+{
+    const uint32_t k8 = (uint32_t)(a.K / 8);
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    if (i >= (uint32_t)(a.M * (int64_t)k8))    // the launcher keeps it below 2^31
+        return;
+    const uint32_t row = i / k8;
+    const int col = (int)((i - row * k8) * 8u);
+    const auto ry = load_raw8<XT>(a.Y, (int64_t)row * a.ldy + col);
+    const auto rg = load_kept8<XT, MODE>(a.G, a.SG, row, a.ldg, a.ldsg, col);
+    const auto ru = load_kept8<XT, MODE>(a.U, a.SU, row, a.ldu, a.ldsu, col);
+    float y[8], g[8], u[8], dg[8], du[8];
+    to_float8<XT>(ry, y);
+    kept_floats<XT, MODE>(rg, g);
+    kept_floats<XT, MODE>(ru, u);
+    grads8<XT, MODE>(y, g, u, dg, du);
+    const int64_t o = (int64_t)row * (2 * a.K) + col;
+    store8<XT>(a.D, o, dg);
+    store8<XT>(a.D, o + a.K, du);
+}
+
+template <int XT, int MODE>
+static hipError_t launch_typed(const SwigluGradArgs &a, hipStream_t s)
+{
+    // Slabs of rows whose piece count fits 31 bits (a slab is one launch).
+    const int64_t k8 = a.K / 8, slab = (int64_t(1) << 31) / k8 - 1;
+    constexpr int64_t kIn = XT == kTypeF32 ? 4 : 2, kKept = MODE == kScaleNone ? kIn : 1;
+    constexpr int64_t kScale = MODE == kScaleBlock ? 4 : MODE == kScaleMx ? 1 : 0;
+    auto at = [](const void *p, int64_t bytes) { return static_cast<const void *>(static_cast<const uint8_t *>(p) + bytes); };
+    for (int64_t r = 0; r < a.M; r += slab) {
+        SwigluGradArgs b = a;
+        b.M = a.M - r < slab ? a.M - r : slab;
+        b.Y = at(a.Y, r * a.ldy * kIn);
+        b.G = at(a.G, r * a.ldg * kKept), b.U = at(a.U, r * a.ldu * kKept);
+        if (kScale)
+            b.SG = at(a.SG, r * a.ldsg * kScale), b.SU = at(a.SU, r * a.ldsu * kScale);
+        b.D = static_cast<uint8_t *>(a.D) + r * 2 * a.K * kIn;
+        swiglu_grad_kernel<XT, MODE><<<(unsigned)((b.M * k8 + 255) / 256), 256, 0, s>>>(b);
+    }
+    return hipGetLastError();
+}
+
+template <int XT>
+static hipError_t launch_mode(const SwigluGradArgs &a, int mode, hipStream_t s)
+{
+    switch (mode) {
+    case kScaleNone: return launch_typed<XT, kScaleNone>(a, s);
+    case kScaleTensor: return launch_typed<XT, kScaleTensor>(a, s);
+    case kScaleBlock: return launch_typed<XT, kScaleBlock>(a, s);
+    case kScaleMx: return launch_typed<XT, kScaleMx>(a, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_swiglu_grad(const SwigluGradArgs &a, int type, int mode, hipStream_t s)
+{
+    switch (type) {
+    case kDtypeBf16: return launch_mode<kDtypeBf16>(a, mode, s);
+    case kTypeF16: return launch_mode<kTypeF16>(a, mode, s);
+    case kTypeF32: return launch_mode<kTypeF32>(a, mode, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace dgp

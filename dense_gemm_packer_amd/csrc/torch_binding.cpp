@@ -36,6 +36,13 @@ struct Abi {
     decltype(&dgp_swiglu_quantize) swiglu;
     decltype(&dgp_gemm_preshuffle_grouped) grouped;
     decltype(&dgp_gemm_preshuffle) gemm;
+    decltype(&dgp_layernorm_quantize) layernorm;
+    decltype(&dgp_norm_backward_workspace_bytes) norm_workspace_bytes;
+    decltype(&dgp_layernorm_backward) layernorm_grad;
+    decltype(&dgp_rmsnorm_backward) rmsnorm_grad;
+    decltype(&dgp_swiglu_backward) swiglu_grad;
+    decltype(&dgp_wgrad_workspace_bytes) wgrad_workspace_bytes;
+    decltype(&dgp_gemm_wgrad) wgrad;
 };
 Abi abi;
 PyObject *raise_status;     // raises DgpError for a status code
@@ -370,26 +377,44 @@ PyObject *quantize_b(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// rmsnorm_quantize(X, weight, mode, residual, eps, scale, out, scales, residual_out, stream)
-PyObject *rmsnorm_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
+// A norm's or a norm gradient's vector of K values, of X's type or fp32.
+void check_vector(const Tensor &W, const char *what, int64_t K, const Tensor &X)
 {
-    HANDLE_TH_ERRORS
-    arity(n, 10);
+    if (W.dim() != 1 || W.size(0) != K || (W.scalar_type() != X.scalar_type() && W.scalar_type() != ScalarType::Float))
+        bad_value(text(what, " must hold ", K, " values of ", X.scalar_type(), " or float32 (got ", W.sizes(), " ",
+                       W.scalar_type(), ")"));
+    if (!W.is_contiguous())
+        bad_value(text(what, " must be contiguous"));
+    same_device(W, what, X);
+}
+
+double number(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred())
+        throw python_error();
+    return v;
+}
+
+// The norms: X, weight, (layer) bias, then mode, residual, eps, scale, out, scales, residual_out, stream.
+PyObject *norm_quantize(PyObject *const *a, bool layer)
+{
     const Tensor &X = tensor(a[0], "X"), &W = tensor(a[1], "weight");
+    const Tensor B = layer ? maybe(a[2], "bias") : Tensor();
+    if (layer)
+        ++a;
     const int64_t ldx = row_stride(X, "X");
     const int mode = scale_mode(a[2], true), code = input_code(X);
     const int64_t M = X.size(0), K = X.size(1);
     const Tensor R = maybe(a[3], "residual");
-    const double eps = PyFloat_AsDouble(a[4]);
-    if (eps == -1.0 && PyErr_Occurred())
-        throw python_error();
+    const double eps = number(a[4]);
     const int64_t ldr = R.defined() ? row_stride_like(R, "residual", X) : 0;
-    if (W.dim() != 1 || W.size(0) != K || (W.scalar_type() != X.scalar_type() && W.scalar_type() != ScalarType::Float))
-        bad_value(text("weight must hold ", K, " values of ", X.scalar_type(), " or float32 (got ", W.sizes(), " ",
-                       W.scalar_type(), ")"));
-    if (!W.is_contiguous())
-        bad_value("weight must be contiguous");
-    same_device(W, "weight", X);
+    check_vector(W, "weight", K, X);
+    if (B.defined()) {
+        check_vector(B, "bias", K, X);
+        if (B.scalar_type() != W.scalar_type())
+            bad_value(text("bias is ", B.scalar_type(), ", weight ", W.scalar_type()));
+    }
     Operand o(X, M, K, mode, a[5], a[6], a[7]);
     Tensor H = maybe(a[8], "residual_out");
     if (H.defined()) {
@@ -402,14 +427,36 @@ PyObject *rmsnorm_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
     o.allocate(X, mode);
     if (R.defined() && !H.defined())
         H = empty(X.sizes(), X.scalar_type(), X);
-    call(abi.rmsnorm, (const void *)X.data_ptr(), ldx, (const void *)ptr(R), ldr, code, (const void *)W.data_ptr(),
-         input_code(W), (float)eps, o.Q.data_ptr(), ptr(o.S), (const float *)ptr(o.scale), ptr(H), M, K, mode,
-         place.handle());
+    if (layer)
+        call(abi.layernorm, (const void *)X.data_ptr(), ldx, (const void *)ptr(R), ldr, code, (const void *)W.data_ptr(),
+             (const void *)ptr(B), input_code(W), (float)eps, o.Q.data_ptr(), ptr(o.S), (const float *)ptr(o.scale), ptr(H), M,
+             K, mode, place.handle());
+    else
+        call(abi.rmsnorm, (const void *)X.data_ptr(), ldx, (const void *)ptr(R), ldr, code, (const void *)W.data_ptr(),
+             input_code(W), (float)eps, o.Q.data_ptr(), ptr(o.S), (const float *)ptr(o.scale), ptr(H), M, K, mode,
+             place.handle());
     if (!R.defined())
         return pair(o.Q, o.scales());
     const Tensor &S = o.scales();
     PyObject *s = S.defined() ? THPVariable_Wrap(S) : Py_NewRef(Py_None);
     return Py_BuildValue("(NNN)", THPVariable_Wrap(o.Q), s, THPVariable_Wrap(H));
+}
+
+// rmsnorm_quantize(X, weight, mode, residual, eps, scale, out, scales, residual_out, stream)
+PyObject *rmsnorm_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 10);
+    return norm_quantize(a, false);
+    END_HANDLE_TH_ERRORS
+}
+
+// layernorm_quantize(X, weight, bias, mode, residual, eps, scale, out, scales, residual_out, stream)
+PyObject *layernorm_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 11);
+    return norm_quantize(a, true);
     END_HANDLE_TH_ERRORS
 }
 
@@ -564,6 +611,216 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------- gradients
+
+// The scale mode of a kept activation, by the modes that gradients read.
+int kept_mode(PyObject *o)
+{
+    const int mode = scale_mode(o, true);
+    if (mode == DGP_SCALE_MX32) {
+        PyObject *r = PyObject_CallFunction(refuse_mode, "l", (long)mode);
+        Py_XDECREF(r);
+        throw python_error();
+    }
+    return mode;
+}
+
+// A kept activation of Y's rows: `shape` values of Y's type, or codes and their scales.
+struct Kept {
+    const Tensor &X;
+    Tensor S;
+    int64_t ld, lds = 0;
+
+    Kept(PyObject *x, PyObject *s, const char *what, const char *scales, int mode, const Tensor &Y, int64_t M, int64_t K)
+        : X(tensor(x, what)), S(maybe(s, scales))
+    {
+        const ScalarType want = mode == DGP_SCALE_NONE ? Y.scalar_type() : ScalarType::Float8_e4m3fn;
+        if (X.dim() != 2 || X.size(0) != M || X.size(1) != K || X.scalar_type() != want)
+            bad_value(text(what, " must be a [", M, ", ", K, "] ", want, " tensor for this scale mode (got ", X.sizes(), " ",
+                           X.scalar_type(), ")"));
+        ld = row_stride(X, what);
+        same_device(X, what, Y);
+        if (mode == DGP_SCALE_NONE) {
+            if (S.defined())
+                bad_value("SCALE_NONE has no scales");
+            return;
+        }
+        if (!S.defined())
+            bad_value(text(scales, " are needed for this scale mode"));
+        if (mode == DGP_SCALE_TENSOR) {
+            if (S.scalar_type() != ScalarType::Float || S.numel() != 1)
+                bad_value(text(scales, " must hold one float32 value (got ", S.sizes(), " ", S.scalar_type(), ")"));
+        } else {
+            if (S.dim() != 2 || S.size(0) != M || S.size(1) != K / 128 || S.scalar_type() != scale_type(mode))
+                bad_value(text(scales, " must be a [", M, ", ", K / 128, "] ", scale_type(mode), " tensor for this scale mode (got ",
+                               S.sizes(), " ", S.scalar_type(), ")"));
+            lds = row_stride(S, scales);
+        }
+        same_device(S, scales, Y);
+    }
+    const void *values() const { return X.data_ptr(); }
+    const void *scales() const { return ptr(S); }
+};
+
+Tensor float_workspace(size_t bytes, const Tensor &X)
+{
+    return bytes ? empty({(int64_t)((bytes + 3) / 4)}, ScalarType::Float, X) : Tensor();
+}
+
+// dY, X, weight, mode, scales, residual_grad, eps, dx, dweight, (layer) dbias, stream
+PyObject *norm_backward(PyObject *const *a, bool layer)
+{
+    const Tensor &Y = tensor(a[0], "dY");
+    const int64_t ldy = row_stride(Y, "dY");
+    const int code = input_code(Y), mode = kept_mode(a[3]);
+    const int64_t M = Y.size(0), K = Y.size(1);
+    const Kept X(a[1], a[4], "X", "scales", mode, Y, M, K);
+    if (X.S.defined() && !X.S.is_contiguous())
+        bad_value("scales must be contiguous");
+    const Tensor &W = tensor(a[2], "weight");
+    check_vector(W, "weight", K, Y);
+    const Tensor R = maybe(a[5], "residual_grad");
+    const int64_t ldr = R.defined() ? row_stride_like(R, "residual_grad", Y) : 0;
+    const double eps = number(a[6]);
+    Tensor dX = maybe(a[7], "dx"), dW = maybe(a[8], "dweight"), dB = layer ? maybe(a[9], "dbias") : Tensor();
+    if (dX.defined())
+        dense(dX, Y.scalar_type(), Y.sizes(), Y, "dx");
+    if (dW.defined())
+        dense(dW, ScalarType::Float, {K}, Y, "dweight");
+    if (dB.defined())
+        dense(dB, ScalarType::Float, {K}, Y, "dbias");
+    on_device(Y, "dY");
+    Place place(Y, a[layer ? 10 : 9]);
+    if (!dX.defined())
+        dX = empty(Y.sizes(), Y.scalar_type(), Y);
+    if (!dW.defined())
+        dW = empty({K}, ScalarType::Float, Y);
+    if (layer && !dB.defined())
+        dB = empty({K}, ScalarType::Float, Y);
+    const size_t bytes = abi.norm_workspace_bytes(M, K, layer);
+    const Tensor ws = float_workspace(bytes, Y);
+    if (layer)
+        call(abi.layernorm_grad, (const void *)Y.data_ptr(), ldy, code, X.values(), X.ld, X.scales(), mode,
+             (const void *)W.data_ptr(), input_code(W), (const void *)ptr(R), ldr, (float)eps, dX.data_ptr(),
+             (float *)dW.data_ptr(), (float *)dB.data_ptr(), M, K, (float *)ptr(ws), bytes, place.handle());
+    else
+        call(abi.rmsnorm_grad, (const void *)Y.data_ptr(), ldy, code, X.values(), X.ld, X.scales(), mode,
+             (const void *)W.data_ptr(), input_code(W), (const void *)ptr(R), ldr, (float)eps, dX.data_ptr(),
+             (float *)dW.data_ptr(), M, K, (float *)ptr(ws), bytes, place.handle());
+    if (!layer)
+        return Py_BuildValue("(NN)", THPVariable_Wrap(dX), THPVariable_Wrap(dW));
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(dX), THPVariable_Wrap(dW), THPVariable_Wrap(dB));
+}
+
+// layernorm_backward(dY, X, weight, mode, scales, residual_grad, eps, dx, dweight, dbias, stream)
+PyObject *layernorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 11);
+    return norm_backward(a, true);
+    END_HANDLE_TH_ERRORS
+}
+
+// rmsnorm_backward(dY, X, weight, mode, scales, residual_grad, eps, dx, dweight, stream)
+PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 10);
+    return norm_backward(a, false);
+    END_HANDLE_TH_ERRORS
+}
+
+// swiglu_backward(dY, gate, up, mode, gate_scales, up_scales, out, stream)
+PyObject *swiglu_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 8);
+    const Tensor &Y = tensor(a[0], "dY");
+    const int64_t ldy = row_stride(Y, "dY");
+    const int code = input_code(Y), mode = kept_mode(a[3]);
+    const int64_t M = Y.size(0), K = Y.size(1);
+    const Kept G(a[1], a[4], "gate", "gate_scales", mode, Y, M, K), U(a[2], a[5], "up", "up_scales", mode, Y, M, K);
+    Tensor D = maybe(a[6], "out");
+    const int64_t shape[2] = {M, 2 * K};
+    if (D.defined())
+        dense(D, Y.scalar_type(), shape, Y, "out");
+    on_device(Y, "dY");
+    Place place(Y, a[7]);
+    if (!D.defined())
+        D = empty(shape, Y.scalar_type(), Y);
+    call(abi.swiglu_grad, (const void *)Y.data_ptr(), ldy, code, G.values(), G.ld, U.values(), U.ld, G.scales(), G.lds,
+         U.scales(), U.lds, mode, D.data_ptr(), M, K, place.handle());
+    return THPVariable_Wrap(D);
+    END_HANDLE_TH_ERRORS
+}
+
+// wgrad(dC, X, S, mode, offsets, rows, out, out is bf16, accumulate, stream)
+PyObject *wgrad(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    arity(n, 10);
+    const Tensor &Y = tensor(a[0], "dC"), &X = tensor(a[1], "X");
+    const Tensor S = maybe(a[2], "sX"), off = maybe(a[4], "offsets"), rows = maybe(a[5], "rows");
+    const int mode = kept_mode(a[3]);
+    Tensor C = maybe(a[6], "out");
+    const int bf16 = PyObject_IsTrue(a[7]), accumulate = PyObject_IsTrue(a[8]);
+    if (bf16 < 0 || accumulate < 0)
+        throw python_error();
+    const int64_t ldc = row_stride(Y, "dC");
+    if (Y.scalar_type() != ScalarType::BFloat16)
+        bad_value(text("dC must be bfloat16 (got ", Y.scalar_type(), ")"));
+    const ScalarType want = mode == DGP_SCALE_NONE ? ScalarType::BFloat16 : ScalarType::Float8_e4m3fn;
+    if (X.dim() != 2 || X.scalar_type() != want)
+        bad_value(text("X must be a 2-D ", want, " tensor for this scale mode (got ", X.sizes(), " ", X.scalar_type(), ")"));
+    if (!X.is_contiguous())
+        bad_value("X must be contiguous");
+    same_device(X, "X", Y);
+    const int64_t M = Y.size(0), N = Y.size(1), K = X.size(1);
+    if (mode == DGP_SCALE_NONE) {
+        if (S.defined())
+            bad_value("SCALE_NONE has no scales");
+    } else if (mode == DGP_SCALE_TENSOR) {
+        check_scales(S, "sX", mode, 1, Y);
+    } else {
+        check_scales(S, "sX", mode, X.size(0) * (K / 128), Y);
+    }
+    int64_t E = 1;
+    if (off.defined()) {
+        if (off.scalar_type() != ScalarType::Int || off.dim() != 1 || off.size(0) < 1)
+            bad_value(text("offsets must be a 1-D int32 tensor (got ", off.sizes(), " ", off.scalar_type(), ")"));
+        dense(off, ScalarType::Int, off.sizes(), Y, "offsets");
+        E = off.size(0) - 1;
+    }
+    if (rows.defined()) {
+        if (!off.defined())
+            bad_value("rows needs offsets");
+        if (rows.scalar_type() != ScalarType::Int || rows.dim() != 1 || rows.size(0) != M)
+            bad_value(text("rows must be ", M, " int32 values (got ", rows.sizes(), " ", rows.scalar_type(), ")"));
+        dense(rows, ScalarType::Int, rows.sizes(), Y, "rows");
+    } else if (X.size(0) != M) {
+        bad_value(text("X has ", X.size(0), " rows, dC ", M));
+    }
+    const int64_t shape[3] = {E, N, K};
+    const at::IntArrayRef shape_c = off.defined() ? at::IntArrayRef(shape, 3) : at::IntArrayRef(shape + 1, 2);
+    const ScalarType type = bf16 ? ScalarType::BFloat16 : ScalarType::Float;
+    if (accumulate && !C.defined())
+        bad_value("accumulate needs out");
+    if (C.defined())
+        dense(C, type, shape_c, Y, "out");
+    on_device(Y, "dC");
+    Place place(Y, a[9]);
+    if (!C.defined())
+        C = empty(shape_c, type, Y);
+    const size_t bytes = abi.wgrad_workspace_bytes(M, N, K, E);
+    const Tensor ws = float_workspace(bytes, Y);
+    call(abi.wgrad, (const void *)Y.data_ptr(), ldc, (const void *)X.data_ptr(), X.size(0),
+         (int)(mode == DGP_SCALE_NONE ? DGP_BF16 : DGP_FP8_E4M3), (const void *)ptr(S), mode, C.data_ptr(),
+         (int)(bf16 ? DGP_BF16 : DGP_F32), accumulate, M, N, K, E, (const int32_t *)ptr(off), (const int32_t *)ptr(rows),
+         (float *)ptr(ws), bytes, place.handle());
+    return THPVariable_Wrap(C);
+    END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses, raise_status, refuse_mode, current_stream): addresses of the
 // entry points in Abi's order.
 PyObject *bind(PyObject *, PyObject *args)
@@ -587,7 +844,9 @@ PyObject *bind(PyObject *, PyObject *args)
     }
     abi = Abi{(decltype(Abi::workspace_bytes))p[0], (decltype(Abi::quantize))p[1], (decltype(Abi::quantize_b))p[2],
               (decltype(Abi::rmsnorm))p[3], (decltype(Abi::swiglu))p[4], (decltype(Abi::grouped))p[5],
-              (decltype(Abi::gemm))p[6]};
+              (decltype(Abi::gemm))p[6], (decltype(Abi::layernorm))p[7], (decltype(Abi::norm_workspace_bytes))p[8],
+              (decltype(Abi::layernorm_grad))p[9], (decltype(Abi::rmsnorm_grad))p[10], (decltype(Abi::swiglu_grad))p[11],
+              (decltype(Abi::wgrad_workspace_bytes))p[12], (decltype(Abi::wgrad))p[13]};
     Py_XSETREF(raise_status, Py_NewRef(rs));
     Py_XSETREF(refuse_mode, Py_NewRef(rm));
     Py_XSETREF(current_stream, Py_NewRef(cs));
@@ -596,6 +855,7 @@ PyObject *bind(PyObject *, PyObject *args)
 
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(quantize), FAST(quantize_b), FAST(rmsnorm_quantize), FAST(swiglu_quantize), FAST(grouped), FAST(gemm),
+                         FAST(layernorm_quantize), FAST(layernorm_backward), FAST(rmsnorm_backward), FAST(swiglu_backward), FAST(wgrad),
                          {"bind", bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

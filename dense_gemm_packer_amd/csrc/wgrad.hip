@@ -1,0 +1,566 @@
+// A weight's gradient (dgp_gemm_wgrad): for every group e of rows,
+//
+//   C[e][n][k] = sum over the rows m of e of Y[m][n] * x[rows ? rows[m] : m][k],
+//
+// Y the output's gradient in bf16 and x the forward product's operand A, bf16 or
+// e4m3 codes with their scales.
+//
+// Both operands have the summed index as their slow one, where a matrix-core
+// instruction wants it in a lane's consecutive elements.  The tile of each goes
+// to LDS in blocks of 4 rows x 16 columns (128 bytes, row by row), and the
+// transposing LDS read (ds_read_b64_tr_b16) hands lane i of 16 the four rows of
+// column i: two of them are one operand fragment of the 16x16x32 instruction.
+// The order of the rows inside a fragment is the same for both operands, so it
+// cancels out.  x's fragment is the first operand and Y's the second, so a lane
+// holds C[n = l % 16][k = 4 (l / 16) + r]: consecutive elements of one row of C.
+//
+// e4m3 codes become bf16 on their way into LDS.  An E8M0 scale times a code is
+// exact in bf16 (one converting instruction); a per-tensor scale multiplies the
+// sum at the end; a code times an fp32 block scale is rounded to bf16, which is
+// a sixteenth of the code's own step (bf16 C: as fine as C's own rounding), or
+// kept as a sum of two bf16 numbers, 2^-17 relative, and multiplied twice
+// (fp32 C).
+//
+// Pipeline, per step of 32 rows: the fragments of step s are in registers while
+// those of s + 1 are read from LDS, the codes of s + 2 are converted and the
+// copies of s + kD are sent off, all of it placed between the products by hand
+// (one wave per SIMD: nothing else hides a stall).  One barrier a step.
+#include "gemm_common.h"
+
+namespace dgp {
+
+namespace {
+
+constexpr int kStep = 32;                  // rows per step
+constexpr uint32_t kNowhere = 0xFFFFFFF0u; // an offset past every buffer's end: loads as zero
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+__device__ inline i32x4 transposed(const uint8_t *p, int second)
+{
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + second));
+    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+    return i32x4{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
+}
+
+// The async copies of gemm_common.h as inline assembly: behind the builtin the
+// compiler waits for every copy in flight before each transposing read (it
+// tells their LDS apart for ordinary reads only).  Each copy waits out what a
+// vector instruction's write to its scalar operands and the write to m0 need.
+// The waits for the copies themselves are counted below.
+template <int BYTES>
+__device__ inline void copy_lds(const i32x4 &rsrc, uint8_t *lds_dst, uint32_t voff)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_u8 *)lds_dst;
+    if constexpr (kLdsPoison) {
+        const int lane = (int)(threadIdx.x & 63);
+        if constexpr (BYTES == 16)
+            ((lds_i32x4 *)lds_dst)[lane] = i32x4{-1, -1, -1, -1};
+        else
+            ((lds_i32 *)lds_dst)[lane] = -1;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    if constexpr (BYTES == 16)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     :: "s"(at), "v"(voff), "s"(rsrc) : "memory");
+    else if constexpr (BYTES == 4)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                     :: "s"(at), "v"(voff), "s"(rsrc) : "memory");
+    else
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds"
+                     :: "s"(at), "v"(voff), "s"(rsrc) : "memory");
+}
+
+// A run of bytes that a copy's range is cut from: `left` bytes from `base` on
+// (none where it is not positive), moved on by one step at a time.
+struct Run {
+    uint64_t base;
+    int64_t left;
+    __device__ inline void next(int64_t bytes) { base += (uint64_t)bytes, left -= bytes; }
+    __device__ inline i32x4 rsrc() const
+    {
+        const uint32_t n = left <= 0 ? 0u : left >= 0xFFFFFFFFll ? 0xFFFFFFFFu : (uint32_t)left;
+        return i32x4{(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)n, 0x00020000};
+    }
+};
+
+// f(0), f(1), ... f(N - 1) with compile-time numbers.
+template <int... I, class Fn>
+__device__ inline void each_of(std::integer_sequence<int, I...>, Fn f)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class Fn>
+__device__ inline void each_of(Fn f)
+{
+    each_of(std::make_integer_sequence<int, N>{}, f);
+}
+
+// Accumulator in place in the AGPRs (F = 8: all 256 of them): the compiler
+// would move it between register files.  Its inputs come straight from LDS.
+template <bool AGPR>
+__device__ inline void multiply_add(f32x4 &acc, const i32x4 &x, const i32x4 &y)
+{
+    if constexpr (AGPR)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(x), "v"(y));
+    else
+        acc = mfma_op(x, y, acc);
+}
+
+// 16 codes -> 16 bf16 values.  `scale`: E8M0 byte or fp32 bits.  LOW: what the
+// rounding to bf16 left over, rounded to bf16 itself.
+template <int MODE, bool LOW>
+__device__ inline void widen(const i32x4 &codes, uint32_t scale, i32x4 (&out)[2])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[2];
+        if constexpr (MODE == kScaleBlock) {
+            const float s = __builtin_bit_cast(float, scale);
+            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i], false);
+            const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i], true);
+            const float v[4] = {a[0] * s, a[1] * s, b[0] * s, b[1] * s};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[h] = pack_bf16x2(v[2 * h], v[2 * h + 1]);
+                if constexpr (LOW)
+                    w[h] = pack_bf16x2(v[2 * h] - __builtin_bit_cast(float, w[h] << 16),
+                                       v[2 * h + 1] - __builtin_bit_cast(float, w[h] & 0xFFFF0000u));
+            }
+        } else {
+            // the instruction takes the exponent field of its fp32 scale: 2^(e - 127), NaN for e = 255
+            const float s = __builtin_bit_cast(float, MODE == kScaleMx ? scale << 23 : 0x3F800000u);
+            w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, false));
+            w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, true));
+        }
+        out[i / 2][i % 2 * 2] = (int)w[0];
+        out[i / 2][i % 2 * 2 + 1] = (int)w[1];
+    }
+}
+
+}  // namespace
+
+// F: fragments of a wave along n and along k (4 waves, 2 x 2: a tile of 32 F).
+template <int MODE, int TERMS, int F, bool GATHER, bool BF16>
+__global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k)
+{
+    constexpr bool kCodes = MODE != kScaleNone;
+    constexpr bool kScaled = MODE == kScaleBlock || MODE == kScaleMx;
+    constexpr int kCols = 32 * F;                        // tile
+    constexpr int H = F / 4;                             // 128-column halves
+    constexpr int kD = TERMS == 2 && F == 8 ? 3 : 4;     // steps that the copies run ahead
+    constexpr int kRow4 = kCols * 8;                     // bytes of 4 rows x kCols in LDS
+    constexpr int kTile = kStep * kCols * 2;             // bytes of a bf16 stage
+    constexpr int kXStages = kCodes ? 2 : kD;
+    // codes: H copies of 1 KiB a wave and step, their scales a dword a lane each
+    constexpr int kCodeStage = kCodes ? 4 * H * 1024 : 0, kScaleStage = kScaled ? 4 * H * 256 : 0;
+    constexpr int kIdx = kCodes ? H : 2;                 // row indices a lane and step
+    constexpr int kIdxStage = GATHER ? 4 * kIdx * 256 : 0;
+    constexpr int kOffX = kD * kTile, kOffCodes = kOffX + kXStages * TERMS * kTile;
+    constexpr int kOffScales = kOffCodes + kD * kCodeStage, kOffIdx = kOffScales + kD * kScaleStage;
+    constexpr int kIdxStages = 8;        // (a stage is read in the step after the one that its next copy sits in)
+    constexpr int kLds = kOffIdx + kIdxStages * kIdxStage;
+    static_assert(kLds <= 160 * 1024, "LDS");
+    constexpr int kGroup = 2 * H + (kCodes ? H : 2 * H) + (kScaled ? H : 0) + (GATHER ? kIdx : 0);   // copies a step
+    static_assert(kGroup * (kD - 1) < 64, "copies in flight");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+    if constexpr (kLdsPoison) {
+        lds_poison_fill(lds, kLds);
+        __syncthreads();
+    }
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const auto tc = tile_of_workgroup<int>((int)blockIdx.x, tiles_n, tiles_k, (int)a.E * a.splits, 1, 4);
+    const int n0 = tc.tm * kCols, k0 = tc.tn * kCols;
+    const int e = tc.s / a.splits, split = tc.s - e * a.splits;
+
+    // The rows of this workgroup.
+    int64_t lo = 0, hi = a.M;
+    if (a.offsets) {
+        lo = a.offsets[e], hi = a.offsets[e + 1];
+        lo = lo < 0 ? 0 : lo > a.M ? a.M : lo;
+        hi = hi < lo ? lo : hi > a.M ? a.M : hi;
+    }
+    if (a.splits > 1) {
+        const int64_t per = ((hi - lo + a.splits - 1) / a.splits + kStep - 1) / kStep * kStep;
+        lo += split * per;
+        hi = lo > hi ? lo : lo + per < hi ? lo + per : hi;
+    }
+    const int steps = __builtin_amdgcn_readfirstlane((int)((hi - lo + kStep - 1) / kStep));
+
+    // ---- copies.  A 1 KiB copy fills 16-byte pieces of LDS in order: 8 blocks
+    // of 4 rows x 16 columns.  Copy (rg, half) of a stage holds the rows 4 rg ..
+    // 4 rg + 3 and 128 columns: a lane's piece is row 4 rg + lane % 8 / 2, eight
+    // columns from 16 (lane / 8) + 8 (lane % 2).
+    const int krow = (lane & 7) >> 1, kcol = (lane >> 3) * 16 + (lane & 1) * 8;
+    const int64_t K = a.K;
+    const uint32_t x_size = kCodes ? 1 : 2;
+    // A lane's piece of codes: row crow of the copy's first row group, 16 columns.
+    const int crow = (lane & 3) + (F == 8 ? 0 : (lane >> 5) * 4), ccol = (F == 8 ? lane >> 2 : (lane >> 2) & 7) * 16;
+
+    // What a step's copies read, from its first row on: Y, x and x's scales (or,
+    // by row list, all of the rows of X), the row list.
+    const int64_t kb = K / 128, s_size = MODE == kScaleBlock ? 4 : 1, rows = hi - lo;
+    const int64_t ldy2 = a.ldy * 2, ldx = K * x_size, lds_ = kb * s_size;
+    const int64_t x_rows = GATHER ? a.x_rows : rows, x_first = GATHER ? 0 : lo;
+    Run ry{(uint64_t)a.Y + (uint64_t)(lo * ldy2 + n0 * 2), (rows - 1) * ldy2 + (a.N - n0) * 2};
+    Run rx{(uint64_t)a.X + (uint64_t)(x_first * ldx + k0 * x_size), x_rows * ldx - k0 * (int64_t)x_size};
+    Run rs{(uint64_t)a.S + (uint64_t)(x_first * lds_ + k0 / 128 * s_size), x_rows * lds_ - k0 / 128 * s_size};
+    Run ri{(uint64_t)a.rows + (uint64_t)(lo * 4), rows * 4};
+    int x_left = (int)(rows < INT32_MAX ? rows : INT32_MAX);    // (by row list) rows from this step on
+
+    // Rows (within the step) of the lane's pieces, and their offsets.
+    uint32_t row_of[kIdx];
+#pragma unroll
+    for (int j = 0; j < kIdx; ++j)
+        row_of[j] = kCodes ? (F == 8 ? 4 * (j * 4 + wave) : 8 * wave) + crow : 4 * (j * 4 + wave) + krow;
+    const uint32_t x_col = kCodes ? (uint32_t)ccol : (uint32_t)kcol * 2, s_col = (uint32_t)ccol / 128 * (uint32_t)s_size;
+    uint32_t y_off[2], x_off[kIdx], s_off[kIdx];
+    auto place_x = [&](const int (&idx)[kIdx]) {
+#pragma unroll
+        for (int j = 0; j < kIdx; ++j) {
+            const uint32_t r = GATHER ? (uint32_t)idx[j] : row_of[j];
+            x_off[j] = r * (uint32_t)ldx + x_col;
+            s_off[j] = r * (uint32_t)lds_ + s_col;
+            if (GATHER && ((int)row_of[j] >= x_left || r >= (uint32_t)a.x_rows))
+                x_off[j] = s_off[j] = kNowhere;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        y_off[j] = (uint32_t)(4 * (j * 4 + wave) + krow) * (uint32_t)ldy2 + (uint32_t)kcol * 2;
+
+    // Copies of one step, numbered 0 .. kGroup - 1; slot: the LDS stage of each kind.
+    i32x4 dy, dx, ds, di;      // ranges of Y, x, scales and row list
+    auto copy_y = [&](int j, int slot) {
+        const int rg = (j / H) * 4 + wave, half = j % H;
+        copy_lds<16>(dy, lds + slot * kTile + rg * kRow4 + half * 1024, y_off[j / H] + half * 256);
+    };
+    auto copy_x = [&](int j, int slot) {
+        if constexpr (kCodes) {
+            copy_lds<16>(dx, lds + kOffCodes + slot * kCodeStage + (j * 4 + wave) * 1024, x_off[j % kIdx]);
+        } else {
+            const int rg = (j / H) * 4 + wave, half = j % H;
+            const uint32_t off = x_off[j / H] + half * 256;
+            copy_lds<16>(dx, lds + kOffX + slot * kTile + rg * kRow4 + half * 1024, GATHER && x_off[j / H] == kNowhere ? kNowhere : off);
+        }
+    };
+    auto copy_s = [&](int j, int slot) {
+        copy_lds<MODE == kScaleBlock ? 4 : 1>(ds, lds + kOffScales + slot * kScaleStage + (j * 4 + wave) * 256, s_off[j % kIdx]);
+    };
+    auto copy_i = [&](int j, int slot) {
+        copy_lds<4>(di, lds + kOffIdx + slot * kIdxStage + (j * 4 + wave) * 256, row_of[j % kIdx] * 4);
+    };
+    constexpr int kXCopies = kCodes ? H : 2 * H, kSCopies = kScaled ? H : 0, kICopies = GATHER ? kIdx : 0;
+    static_assert(kGroup == 2 * H + kXCopies + kSCopies + kICopies, "");
+    auto copy = [&](auto cc, int slot_y, int slot_x, int slot_i) {
+        constexpr int c = decltype(cc)::value;
+        if constexpr (c < 2 * H)
+            copy_y(c, slot_y);
+        else if constexpr (c < 2 * H + kXCopies)
+            copy_x(c - 2 * H, slot_x);
+        else if constexpr (c < 2 * H + kXCopies + kSCopies)
+            copy_s(c - 2 * H - kXCopies, slot_x);
+        else
+            copy_i(c - 2 * H - kXCopies - kSCopies, slot_i);
+    };
+    // The next step's ranges.
+    auto next_y = [&] { dy = ry.rsrc(), ry.next(kStep * ldy2); };
+    auto next_x = [&] {
+        dx = rx.rsrc(), ds = rs.rsrc();
+        if constexpr (!GATHER)
+            rx.next(kStep * ldx), rs.next(kStep * lds_);
+    };
+    auto next_i = [&] { di = ri.rsrc(), ri.next(kStep * 4); };
+
+    // The wave's own codes of one step (copy j), as bf16 into an LDS stage of x.
+    auto convert = [&](int j, const i32x4 &c, uint32_t s, int x_slot) {
+        uint8_t *d = lds + kOffX + x_slot * (TERMS * kTile) + (row_of[j % kIdx] >> 2) * kRow4 + (ccol >> 4) * 128 + (crow & 3) * 32;
+        i32x4 v[2];
+        widen<MODE, false>(c, s, v);
+        reinterpret_cast<i32x4 *>(d)[0] = v[0];
+        reinterpret_cast<i32x4 *>(d)[1] = v[1];
+        if constexpr (TERMS == 2) {
+            widen<MODE, true>(c, s, v);
+            reinterpret_cast<i32x4 *>(d + kTile)[0] = v[0];
+            reinterpret_cast<i32x4 *>(d + kTile)[1] = v[1];
+        }
+    };
+    auto read_codes = [&](int j, int slot, i32x4 &c, uint32_t &s) {
+        c = *reinterpret_cast<const i32x4 *>(lds + kOffCodes + slot * kCodeStage + (j * 4 + wave) * 1024 + lane * 16);
+        s = 0;
+        if constexpr (kScaled)
+            s = reinterpret_cast<const uint32_t *>(lds + kOffScales + slot * kScaleStage + (j * 4 + wave) * 256)[lane];
+    };
+
+    // ---- fragments.  Wave (wn, wk) of 2 x 2 owns 16 F columns of each operand.
+    const int wn = wave >> 1, wk = wave & 1;
+    const int frag = (lane >> 4) * kRow4 + (lane & 15) * 8;     // row groups 0..3 by lane / 16, then 4..7
+    const uint8_t *const yfrag = lds + frag + wn * F * 128;
+    const uint8_t *const xfrag = lds + kOffX + frag + wk * F * 128;
+    i32x4 yf[2][F], xf[2][TERMS][F];
+    f32x4 acc[F][F];                                            // [k fragment][n fragment]
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto read_frag = [&](auto pc, auto fc, int y_slot, int x_slot) {
+        constexpr int P = decltype(pc)::value, f = decltype(fc)::value;
+        if constexpr (f < F)
+            yf[P][f] = transposed(yfrag + y_slot * kTile + f * 128, 4 * kRow4);
+        else
+            xf[P][(f - F) / F][f % F] = transposed(xfrag + x_slot * (TERMS * kTile) + (f - F) / F * kTile + f % F * 128, 4 * kRow4);
+    };
+
+    // Group g of copies (one per step, and before the first step those of -kD + 1 .. -1):
+    // Y of step g + kD, x of g + kD (codes: kD + 1), the row list for x of group g + kD + 1.
+    constexpr int kAhead = kCodes ? 1 : 0;
+    constexpr int kFrags = F * (1 + TERMS), kSlots = F * F * TERMS / 4;     // a slot: 4 products
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    int idx[kIdx];
+    // row indices of the steps before the list comes through LDS
+    auto first_idx = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < kIdx; ++j) {
+            idx[j] = 0;
+            const int64_t m = lo + (int64_t)t * kStep + row_of[j];
+            if (GATHER && m < hi)
+                idx[j] = a.rows[m];
+        }
+        place_x(idx);
+        x_left -= kStep;
+    };
+    next_y();
+    for (int c = 0; c < 2 * H; ++c)
+        copy_y(c, 0);
+#pragma unroll
+    for (int t = 0; t <= kAhead; ++t) {
+        first_idx(t);
+        next_x();
+        for (int c = 0; c < kXCopies; ++c)
+            copy_x(c, t);
+        for (int c = 0; c < kSCopies; ++c)
+            copy_s(c, t);
+    }
+    if constexpr (GATHER) {
+        ri.next((kD + kAhead + 1) * kStep * 4);
+        next_i();
+        for (int c = 0; c < kICopies; ++c)
+            copy_i(c, 1 % kIdxStages);
+    }
+    auto first_group = [&](int g) {
+        first_idx(g + kD + kAhead);
+        next_y(), next_x(), next_i();
+        each_of<kGroup>([&](auto c) { copy(c, (g + kD) % kD, (g + kD + kAhead) % kD, (g + kD + 1) % kIdxStages); });
+    };
+#pragma unroll
+    for (int g = 1 - kD; g < -1; ++g)
+        first_group(g);
+    if constexpr (kCodes) {
+        // (group -1 copies codes to where those of step 0 are)
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kD - 2) * kGroup) : "memory");
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                i32x4 c;
+                uint32_t s;
+                read_codes(j, t, c, s);
+                convert(j, c, s, t);
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    first_group(-1);
+    first_idx(kD + kAhead);      // (the offsets of step 0's copies; GATHER waits for every load here)
+    next_y(), next_x(), next_i();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kD - 1) * kGroup) : "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    each_of<kFrags>([&](auto f) { read_frag(I0{}, f, 0, 0); });
+    // s % kD; stages s + 1 and s + 2
+    int slot = 0;
+    auto step = [&](auto pc, int s) {
+        constexpr int P = decltype(pc)::value;
+        const int slot1 = slot + 1 < kD ? slot + 1 : 0, slot2 = slot1 + 1 < kD ? slot1 + 1 : 0;
+        // Y and x (codes: of the step after) of step s + 1 have landed, here and, behind
+        // the barrier, in every wave; every wave has read the fragments of step s.
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kD - 2) * kGroup) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        i32x4 codes[kCodes ? H : 1];
+        uint32_t scales[kCodes ? H : 1];
+        each_of<kSlots>([&](auto wc) {
+            constexpr int w = decltype(wc)::value;
+            constexpr int i = w * 4 / F % F, j0 = w * 4 % F, q = w * 4 / (F * F);
+            // fragments of the next step over the first three quarters
+            constexpr int f0 = w * 4 * kFrags / (3 * kSlots), f1 = (w + 1) * 4 * kFrags / (3 * kSlots);
+            each_of<(f0 < kFrags ? (f1 < kFrags ? f1 : kFrags) - f0 : 0)>([&](auto fc) {
+                read_frag(std::integral_constant<int, 1 - P>{}, std::integral_constant<int, f0 + decltype(fc)::value>{}, slot1,
+                          kCodes ? (s + 1) & 1 : slot1);
+            });
+            if constexpr (kCodes && w < H)
+                read_codes(w, slot2, codes[w], scales[w]);
+            if constexpr (GATHER && w == 0) {
+#pragma unroll
+                for (int j = 0; j < kIdx; ++j)
+                    idx[j] = reinterpret_cast<const int *>(lds + kOffIdx + (s + 1) % kIdxStages * kIdxStage + (j * 4 + wave) * 256)[lane];
+            }
+            // copies over the slots, the next step's ranges and offsets behind them
+            constexpr int kSpan = kSlots - 1;
+            constexpr int c0 = w * kGroup / kSpan, c1 = (w + 1) * kGroup / kSpan;
+            each_of<(w < kSpan ? c1 - c0 : 0)>([&](auto c) {
+                copy(std::integral_constant<int, c0 + decltype(c)::value>{}, slot, kCodes ? slot1 : slot, (s + kD + 1) % kIdxStages);
+            });
+            if constexpr (kCodes && w >= 2 && w < 2 + H)
+                convert(w - 2, codes[w - 2], scales[w - 2], s & 1);
+            if constexpr (w == kSlots - 1) {
+                next_y(), next_x(), next_i();
+                if constexpr (GATHER)
+                    place_x(idx), x_left -= kStep;
+            }
+#pragma unroll
+            for (int j = j0; j < j0 + 4; ++j)
+                multiply_add<F == 8>(acc[i][j], xf[P][q][i], yf[P][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        slot = slot1;
+    };
+    // (in pairs, one at least: the accumulators of a loop with two ends would be copied at one of them;
+    // a step past the last row multiplies zeros)
+    int s = 0;
+    do {
+        step(I0{}, s);
+        step(I1{}, s + 1);
+        s += 2;
+    } while (s < steps);
+    // (copies of steps that do not come; the last products, which the compiler does not see as such)
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- results
+    float scale = 1.0f;
+    if (MODE == kScaleTensor && rows > 0)
+        scale = static_cast<const float *>(a.S)[0];
+    const int64_t size = a.N * K;
+    int at_n = n0 + wn * (F * 16) + (lane & 15), at_k = k0 + wk * (F * 16) + (lane >> 4) * 4;
+    asm volatile("" : "+v"(at_n), "+v"(at_k));     // (addresses that are worked out here, not held through the loop)
+    auto each = [&](auto store) {
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int n = at_n + j * 16;
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const int k = at_k + i * 16;
+                if (n < a.N && k < K) {
+                    f32x4 v = acc[i][j];
+                    asm volatile("" : "+v"(v));     // (read here, not all 64 of them at the loop's end)
+                    if constexpr (MODE == kScaleTensor)
+                        v = v * scale;
+                    store((int64_t)n * K + k, v);
+                }
+            }
+        }
+    };
+    if (a.splits > 1) {
+        float *c = a.ws + ((int64_t)split * a.E + e) * size;
+        each([&](int64_t at, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c + at) = v; });
+    } else if constexpr (BF16) {
+        uint16_t *c = static_cast<uint16_t *>(a.C) + (int64_t)e * size;
+        each([&](int64_t at, const f32x4 &v) {
+            *reinterpret_cast<u32x2 *>(c + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        });
+    } else if (a.accumulate) {
+        float *c = static_cast<float *>(a.C) + (int64_t)e * size;
+        each([&](int64_t at, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c + at) += v; });
+    } else {
+        float *c = static_cast<float *>(a.C) + (int64_t)e * size;
+        each([&](int64_t at, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c + at) = v; });
+    }
+}
+
+// C (+)= the sum of `splits` partial results in order, rounded once.
+template <bool BF16>
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float *ws, void *C, int64_t quads, int splits, int accumulate)
+{
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(ws);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+        f32x4 v = p[i];
+        for (int s = 1; s < splits; ++s)
+            v += p[s * quads + i];
+        if constexpr (BF16) {
+            static_cast<u32x2 *>(C)[i] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        } else {
+            f32x4 *c = static_cast<f32x4 *>(C) + i;
+            *c = accumulate ? *c + v : v;
+        }
+    }
+}
+
+// --------------------------------------------------------------- launches
+
+WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K, int64_t E)
+{
+    auto tiles = [&](int64_t t) { return (N + t - 1) / t * ((K + t - 1) / t) * E; };
+    const int64_t rows = M / (E > 0 ? E : 1);
+    WgradPlan p{tiles(256) >= 192 ? 256 : 128, 1};
+    if (p.tile == 128) {
+        while (p.splits < 16 && tiles(128) * p.splits < 256 && rows / (p.splits * 2) >= 256)
+            p.splits *= 2;
+    }
+    return p;
+}
+
+namespace {
+
+template <int MODE, int TERMS, int F, bool BF16>
+void launch_tile(const WgradArgs &a, hipStream_t s)
+{
+    const int64_t tile = 32 * F, tn = (a.N + tile - 1) / tile, tk = (a.K + tile - 1) / tile;
+    const unsigned grid = (unsigned)(tn * tk * a.E * a.splits);
+    if (a.rows)
+        wgrad_kernel<MODE, TERMS, F, true, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk);
+    else
+        wgrad_kernel<MODE, TERMS, F, false, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk);
+}
+
+template <int F, bool BF16>
+hipError_t launch_mode(const WgradArgs &a, int mode, hipStream_t s)
+{
+    switch (mode) {
+    case kScaleNone: launch_tile<kScaleNone, 1, F, BF16>(a, s); break;
+    case kScaleTensor: launch_tile<kScaleTensor, 1, F, BF16>(a, s); break;
+    case kScaleBlock: launch_tile<kScaleBlock, BF16 ? 1 : 2, F, BF16>(a, s); break;
+    case kScaleMx: launch_tile<kScaleMx, 1, F, BF16>(a, s); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_wgrad(const WgradArgs &args, int mode, bool out_bf16, const WgradPlan &plan, hipStream_t s)
+{
+    WgradArgs a = args;
+    a.splits = plan.splits;
+    const hipError_t err = plan.tile == 256 ? (out_bf16 ? launch_mode<8, true>(a, mode, s) : launch_mode<8, false>(a, mode, s))
+                                            : (out_bf16 ? launch_mode<4, true>(a, mode, s) : launch_mode<4, false>(a, mode, s));
+    if (err != hipSuccess || plan.splits == 1)
+        return err;
+    const int64_t quads = a.E * a.N * a.K / 4;
+    const unsigned grid = (unsigned)(quads / 256 + 1 < 4096 ? quads / 256 + 1 : 4096);
+    if (out_bf16)
+        wgrad_join_kernel<true><<<grid, 256, 0, s>>>(a.ws, a.C, quads, plan.splits, 0);
+    else
+        wgrad_join_kernel<false><<<grid, 256, 0, s>>>(a.ws, a.C, quads, plan.splits, a.accumulate);
+    return hipGetLastError();
+}
+
+}  // namespace dgp

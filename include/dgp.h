@@ -395,6 +395,102 @@ dgp_status dgp_rmsnorm_quantize(const void *X, int64_t ldx, const void *R, int64
 dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_t ldu, int x_type, void *Q, void *S,
                                const float *scale, int64_t M, int64_t K, int scale_mode, void *stream);
 
+/* dgp_layernorm_quantize -- h = x + r (r as in dgp_rmsnorm_quantize), y = (h - mean)
+ * / sqrt(var + eps) * w + b over each row, var the mean of (h - mean)^2; Q, S
+ * and H as there.  w, and b where not NULL, have K values of w_type (x_type or
+ * DGP_F32).  Squares are summed in fp32, about the mean: for rows that spread
+ * over more than about 1e19 y is b, with eps = 0 a row of equal values is 0 / 0. */
+dgp_status dgp_layernorm_quantize(const void *X, int64_t ldx, const void *R, int64_t ldr, int x_type, const void *W,
+                                  const void *B, int w_type, float eps, void *Q, void *S, const float *scale, void *H,
+                                  int64_t M, int64_t K, int scale_mode, void *stream);
+
+/*
+ * Gradients
+ *
+ * The backward pass of the operators above, in fp32 with one rounding at the
+ * end.  Gradients of activations come and go in `type` (DGP_BF16, DGP_F16 or
+ * DGP_F32).  What the forward pass kept of an activation is read in one of the
+ * forms that a product's operand A has:
+ *   DGP_SCALE_NONE      the activation itself, in `type`; S unused.
+ *   DGP_SCALE_TENSOR    e4m3, S one fp32 scale.
+ *   DGP_SCALE_BLOCK128  e4m3, S fp32 [M][K/128].
+ *   DGP_SCALE_MX128     e4m3, S E8M0 [M][K/128].
+ * so what dgp_quantize writes serves as an 8-bit checkpoint, and the operand of
+ * the forward product as its own.  A gradient is that of the formula at the
+ * values which the checkpoint holds.
+ *
+ * Inputs are rows ld* elements apart (ld* >= K; e4m3: bytes), each 16-byte
+ * aligned, of K elements: K % 64 == 0, with e4m3 K % 128 == 0; at most 2^23
+ * bytes.  Outputs are dense, and apart from every input but for an update in
+ * place where one is named; else DGP_ERR_SHAPE.  M = 0 writes zeros to the
+ * sums over rows; K = 0 is a no-op.  Sums over rows have a fixed order: the same
+ * bits in every run.
+ */
+
+/* Bytes of workspace of dgp_layernorm_backward (layer = 1) and
+ * dgp_rmsnorm_backward (0).  Its contents need no clearing. */
+size_t dgp_norm_backward_workspace_bytes(int64_t M, int64_t K, int layer);
+
+/* dgp_layernorm_backward -- with xhat = (x - mean) / sqrt(var + eps) over each
+ * row of x and g = dy w:
+ *   dx = (g - mean(g) - xhat mean(g xhat)) / sqrt(var + eps) (+ r)
+ *   dw = sum over rows of dy xhat,  db = sum over rows of dy
+ * x: the forward norm's h (its input, or with a residual the stream's new value).  r, where R is
+ * not NULL: a gradient to add, that of the residual stream.  dx is `type` [M][K], dw and db
+ * (NULL: not wanted) fp32 [K].  w has K values of `type` or DGP_F32.  dx may be dy, R or
+ * (DGP_SCALE_NONE) X itself, with dense rows. */
+dgp_status dgp_layernorm_backward(const void *dY, int64_t ldy, int type, const void *X, int64_t ldx, const void *S,
+                                  int scale_mode, const void *W, int w_type, const void *R, int64_t ldr, float eps,
+                                  void *dX, float *dW, float *dB, int64_t M, int64_t K, float *ws, size_t ws_bytes,
+                                  void *stream);
+
+/* dgp_rmsnorm_backward -- as dgp_layernorm_backward without the means of x and
+ * of g: xhat = x / sqrt(mean(x^2) + eps), dx = (g - xhat mean(g xhat)) /
+ * sqrt(mean(x^2) + eps) (+ r), dw = sum over rows of dy xhat. */
+dgp_status dgp_rmsnorm_backward(const void *dY, int64_t ldy, int type, const void *X, int64_t ldx, const void *S,
+                                int scale_mode, const void *W, int w_type, const void *R, int64_t ldr, float eps,
+                                void *dX, float *dW, int64_t M, int64_t K, float *ws, size_t ws_bytes, void *stream);
+
+/* dgp_swiglu_backward -- with s = 1 / (1 + exp(-g)), elementwise:
+ *   dg = dy u s (1 + g (1 - s)),  du = dy g s
+ * D is `type` [M][2 K]: dg in columns 0 .. K-1 and du behind it, the gradient of one product's columns
+ * that held gate and up side by side.  SG and SU: the scales of gate and of up, rows ldsg and ldsu
+ * scales apart (DGP_SCALE_TENSOR: one value each, may be the same one); the halves of one
+ * checkpoint are G, U = G + K with ldg = ldu = 2 K and SG, SU = SG + K/128 with ldsg = ldsu = 2 K/128.
+ * D may be G itself with U = G + K and ldg = ldu = 2 K (DGP_SCALE_NONE). */
+dgp_status dgp_swiglu_backward(const void *dY, int64_t ldy, int type, const void *G, int64_t ldg, const void *U, int64_t ldu,
+                               const void *SG, int64_t ldsg, const void *SU, int64_t ldsu, int scale_mode, void *D,
+                               int64_t M, int64_t K, void *stream);
+
+/* Bytes of workspace of dgp_gemm_wgrad. */
+size_t dgp_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E);
+
+/*
+ * dgp_gemm_wgrad -- gradient of a product's weight (of E weights, grouped as in
+ * dgp_gemm_preshuffle_grouped):
+ *
+ *   dB[e][n][k] (+)= sum over m in [offsets[e], offsets[e+1]) of dC[m][n] x[rows ? rows[m] : m][k]
+ *
+ * dC is bf16 [M][N], rows ldc elements apart; x the product's operand A: X [x_rows][K] of `dtype`
+ * (DGP_BF16, or DGP_FP8_E4M3 with the scales S of DGP_SCALE_TENSOR, BLOCK128 or MX128),
+ * dense.  offsets and rows as there; offsets NULL: one weight (E = 1) and all M rows.  dB is [E][N][K]
+ * row-major (not preshuffled), fp32 or, out_type DGP_BF16, rounded once; a weight without
+ * rows gets zeros.  accumulate (fp32 only): added to what dB holds.
+ *
+ * Products are those of bf16 numbers, summed in fp32 (subnormal ones may count as zero).  bf16,
+ * per-tensor and E8M0 scales: exactly dC and x (a per-tensor scale multiplies the sum).  Block scales:
+ * x is rounded to bf16 for a bf16 dB, and taken to 2^-17 of its value for an fp32 one.
+ *
+ * Requires N % 16 == 0, K % 64 == 0 (e4m3: K % 128 == 0), every pointer 16-byte aligned (offsets, rows and fp32
+ * scales 4-byte; E8M0 any), ldc * 2 % 16 == 0, N, K <= 2^22, ldc <= 2^25, E <= 65535; x_rows >= M, or with a row list any
+ * (then X is at most 0xFF000000 bytes; a row that X does not have counts as zeros).  No
+ * output may overlap an input.  N = 0, K = 0 or E = 0 is a no-op.
+ */
+dgp_status dgp_gemm_wgrad(const void *dC, int64_t ldc, const void *X, int64_t x_rows, int dtype, const void *S,
+                          int scale_mode, void *dB, int out_type, int accumulate, int64_t M, int64_t N, int64_t K,
+                          int64_t E, const int32_t *offsets, const int32_t *rows, float *ws, size_t ws_bytes,
+                          void *stream);
+
 /* dgp_check_arch -- DGP_OK if `gcn_arch_name` (as reported by the HIP device
  * properties, e.g. "gfx950:sramecc+:xnack-") names gfx950, else DGP_ERR_ARCH.
  * Pure host function.  The async global->LDS copy the GEMM depends on exists
