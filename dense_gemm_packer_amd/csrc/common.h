@@ -116,11 +116,13 @@ __device__ inline i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t voff)
 
 // ------------------------------------------------------------- conversions
 
+// (as one vector: the compiler makes two conversions, a shift and an or of two scalars)
 __device__ inline uint32_t pack_bf16x2(float lo, float hi)
 {
-    __bf16 a = (__bf16)lo;   // v_cvt_pk_bf16_f32: round to nearest even
-    __bf16 b = (__bf16)hi;
-    return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    // v_cvt_pk_bf16_f32: round to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
 }  // namespace dgp
