@@ -25,6 +25,8 @@
 // those of s + 1 are read from LDS, the codes of s + 2 are converted and the
 // copies of s + kD are sent off, all of it placed between the products by hand
 // (one wave per SIMD: nothing else hides a stall).  One barrier a step.
+#include <algorithm>
+
 #include "gemm_common.h"
 
 namespace dgp {
@@ -110,42 +112,62 @@ __device__ inline void multiply_add(f32x4 &acc, const i32x4 &x, const i32x4 &y)
         acc = mfma_op(x, y, acc);
 }
 
-// 16 codes -> 16 bf16 values.  `scale`: E8M0 byte or fp32 bits.  LOW: what the
+// 4 codes -> 4 bf16 values.  `scale`: E8M0 byte or fp32 bits.  LOW: what the
 // rounding to bf16 left over, rounded to bf16 itself.
 template <int MODE, bool LOW>
-__device__ inline void widen(const i32x4 &codes, uint32_t scale, i32x4 (&out)[2])
+__device__ inline void widen(int codes, uint32_t scale, int &lo, int &hi)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    if constexpr (MODE == kScaleBlock) {
+        const float s = __builtin_bit_cast(float, scale);
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(codes, false);
+        const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(codes, true);
+        const float v[4] = {a[0] * s, a[1] * s, b[0] * s, b[1] * s};
         uint32_t w[2];
-        if constexpr (MODE == kScaleBlock) {
-            const float s = __builtin_bit_cast(float, scale);
-            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i], false);
-            const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i], true);
-            const float v[4] = {a[0] * s, a[1] * s, b[0] * s, b[1] * s};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                w[h] = pack_bf16x2(v[2 * h], v[2 * h + 1]);
-                if constexpr (LOW)
-                    w[h] = pack_bf16x2(v[2 * h] - __builtin_bit_cast(float, w[h] << 16),
-                                       v[2 * h + 1] - __builtin_bit_cast(float, w[h] & 0xFFFF0000u));
-            }
-        } else {
-            // the instruction takes the exponent field of its fp32 scale: 2^(e - 127), NaN for e = 255
-            const float s = __builtin_bit_cast(float, MODE == kScaleMx ? scale << 23 : 0x3F800000u);
-            w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, false));
-            w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[i], s, true));
+        for (int h = 0; h < 2; ++h) {
+            w[h] = pack_bf16x2(v[2 * h], v[2 * h + 1]);
+            if constexpr (LOW)
+                w[h] = pack_bf16x2(v[2 * h] - __builtin_bit_cast(float, w[h] << 16),
+                                   v[2 * h + 1] - __builtin_bit_cast(float, w[h] & 0xFFFF0000u));
         }
-        out[i / 2][i % 2 * 2] = (int)w[0];
-        out[i / 2][i % 2 * 2 + 1] = (int)w[1];
+        lo = (int)w[0], hi = (int)w[1];
+    } else {
+        // the instruction takes the exponent field of its fp32 scale: 2^(e - 127), NaN for e = 255
+        const float s = __builtin_bit_cast(float, MODE == kScaleMx ? scale << 23 : 0x3F800000u);
+        lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, false));
+        hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true));
     }
 }
 
 }  // namespace
 
+// Tile `wg` of the grid in the order of the groups, in each a raster over 4 tile
+// rows.  Workgroups go to the XCDs in turn (wg % 8) whatever they take, so an XCD
+// gets every eighth run of `chunk` neighbouring tiles: neighbours share their
+// operands' panels in its L2, and each XCD has its part of every group, which
+// groups of unequal size need (32 groups of 585 to 2933 rows, N 4096, K 2048,
+// block scales by row list: 997 us with four whole groups an XCD, 790 where all
+// have 1024).  Tiles behind the last whole round keep their number.
+struct Tile {
+    int n, k, s;
+};
+__device__ inline Tile tile_at(int wg, int tiles_n, int tiles_k, int groups, int chunk)
+{
+    const int per = tiles_n * tiles_k, round = kNumXcd * chunk;
+    int t = wg;
+    if (wg < per * groups / round * round) {
+        const int i = wg / kNumXcd;
+        t = (i / chunk * kNumXcd + wg % kNumXcd) * chunk + i % chunk;
+    }
+    Tile r;
+    r.s = t / per;
+    raster_tile<int>(t - r.s * per, tiles_n, tiles_k, 4, r.n, r.k);
+    return r;
+}
+
 // F: fragments of a wave along n and along k (4 waves, 2 x 2: a tile of 32 F).
 template <int MODE, int TERMS, int F, bool GATHER, bool BF16>
-__global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k)
+__global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k, const int chunk)
 {
     constexpr bool kCodes = MODE != kScaleNone;
     constexpr bool kScaled = MODE == kScaleBlock || MODE == kScaleMx;
@@ -174,9 +196,9 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const auto tc = tile_of_workgroup<int>((int)blockIdx.x, tiles_n, tiles_k, (int)a.E * a.splits, 1, 4);
-    const int n0 = tc.tm * kCols, k0 = tc.tn * kCols;
-    const int e = tc.s / a.splits, split = tc.s - e * a.splits;
+    const Tile tile = tile_at((int)blockIdx.x, tiles_n, tiles_k, (int)a.E * a.splits, chunk);
+    const int n0 = tile.n * kCols, k0 = tile.k * kCols;
+    const int e = tile.s / a.splits, split = tile.s - e * a.splits;
 
     // The rows of this workgroup.
     int64_t lo = 0, hi = a.M;
@@ -277,17 +299,22 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
     };
     auto next_i = [&] { di = ri.rsrc(), ri.next(kStep * 4); };
 
-    // The wave's own codes of one step (copy j), as bf16 into an LDS stage of x.
-    auto convert = [&](int j, const i32x4 &c, uint32_t s, int x_slot) {
+    // Codes 4 i .. 4 i + 3 of the wave's own piece (copy j) of one step, as bf16; with every
+    // second one eight values go to an LDS stage of x.
+    i32x4 wide[TERMS];
+    auto convert = [&](int j, int i, const i32x4 &c, uint32_t s, int x_slot) {
         uint8_t *d = lds + kOffX + x_slot * (TERMS * kTile) + (row_of[j % kIdx] >> 2) * kRow4 + (ccol >> 4) * 128 + (crow & 3) * 32;
-        i32x4 v[2];
-        widen<MODE, false>(c, s, v);
-        reinterpret_cast<i32x4 *>(d)[0] = v[0];
-        reinterpret_cast<i32x4 *>(d)[1] = v[1];
+        int lo, hi;
+        widen<MODE, false>(c[i], s, lo, hi);
+        wide[0][i % 2 * 2] = lo, wide[0][i % 2 * 2 + 1] = hi;
         if constexpr (TERMS == 2) {
-            widen<MODE, true>(c, s, v);
-            reinterpret_cast<i32x4 *>(d + kTile)[0] = v[0];
-            reinterpret_cast<i32x4 *>(d + kTile)[1] = v[1];
+            widen<MODE, true>(c[i], s, lo, hi);
+            wide[1][i % 2 * 2] = lo, wide[1][i % 2 * 2 + 1] = hi;
+        }
+        if (i % 2 == 1) {
+#pragma unroll
+            for (int q = 0; q < TERMS; ++q)
+                reinterpret_cast<i32x4 *>(d + q * kTile)[i / 2] = wide[q];
         }
     };
     auto read_codes = [&](int j, int slot, i32x4 &c, uint32_t &s) {
@@ -324,16 +351,17 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     int idx[kIdx];
-    // row indices of the steps before the list comes through LDS
-    auto first_idx = [&](int t) {
+    // row indices of the steps before the list comes through LDS: all loads first
+    int head[kD + kAhead + 1][kIdx];
+#pragma unroll
+    for (int t = 0; t <= kD + kAhead; ++t)
 #pragma unroll
         for (int j = 0; j < kIdx; ++j) {
-            idx[j] = 0;
             const int64_t m = lo + (int64_t)t * kStep + row_of[j];
-            if (GATHER && m < hi)
-                idx[j] = a.rows[m];
+            head[t][j] = GATHER && m < hi ? a.rows[m] : 0;
         }
-        place_x(idx);
+    auto first_idx = [&](int t) {
+        place_x(head[t]);
         x_left -= kStep;
     };
     next_y();
@@ -373,7 +401,9 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
                 i32x4 c;
                 uint32_t s;
                 read_codes(j, t, c, s);
-                convert(j, c, s, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    convert(j, i, c, s, t);
             }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -418,8 +448,14 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
             each_of<(w < kSpan ? c1 - c0 : 0)>([&](auto c) {
                 copy(std::integral_constant<int, c0 + decltype(c)::value>{}, slot, kCodes ? slot1 : slot, (s + kD + 1) % kIdxStages);
             });
-            if constexpr (kCodes && w >= 2 && w < 2 + H)
-                convert(w - 2, codes[w - 2], scales[w - 2], s & 1);
+            // the codes' conversion over two thirds of the slots, from the third on
+            constexpr int kOver = kSlots * 2 / 3 < kSlots - 2 ? kSlots * 2 / 3 : kSlots - 2;
+            constexpr int v0 = (w - 2) * 4 * H / kOver, v1 = (w - 1) * 4 * H / kOver;
+            if constexpr (kCodes && w >= 2) {
+#pragma unroll
+                for (int v = v0; v < v1 && v < 4 * H; ++v)
+                    convert(v / 4, v % 4, codes[v / 4], scales[v / 4], s & 1);
+            }
             if constexpr (w == kSlots - 1) {
                 next_y(), next_x(), next_i();
                 if constexpr (GATHER)
@@ -525,10 +561,13 @@ void launch_tile(const WgradArgs &a, hipStream_t s)
 {
     const int64_t tile = 32 * F, tn = (a.N + tile - 1) / tile, tk = (a.K + tile - 1) / tile;
     const unsigned grid = (unsigned)(tn * tk * a.E * a.splits);
+    // one group: an eighth of its tiles each; several: an eighth of one's, 4 to 32 tiles
+    const int64_t per = tn * tk, groups = a.E * a.splits;
+    const int chunk = (int)(groups == 1 ? std::max<int64_t>(per / kNumXcd, 1) : std::clamp<int64_t>(per / kNumXcd, 4, 32));
     if (a.rows)
-        wgrad_kernel<MODE, TERMS, F, true, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk);
+        wgrad_kernel<MODE, TERMS, F, true, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk, chunk);
     else
-        wgrad_kernel<MODE, TERMS, F, false, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk);
+        wgrad_kernel<MODE, TERMS, F, false, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk, chunk);
 }
 
 template <int F, bool BF16>
