@@ -40,19 +40,18 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-__device__ inline i32x4 transposed(const uint8_t *p, int second)
+// Four rows of the 16 columns that start at p (in LDS, 32 bytes a row), a column a lane.
+__device__ inline u32x2 transposed(const uint8_t *p)
 {
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + second));
-    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
-    return i32x4{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
 }
 
 // The async copies of gemm_common.h as inline assembly: behind the builtin the
 // compiler waits for every copy in flight before each transposing read (it
-// tells their LDS apart for ordinary reads only).  Each copy waits out what a
-// vector instruction's write to its scalar operands and the write to m0 need.
-// The waits for the copies themselves are counted below.
+// tells their LDS apart for ordinary reads only).  A copy waits out the write to
+// m0; its scalar operands are made by scalar instructions, or by vector ones well
+// before (5 wait states, which a test of the assembly counts).  The waits for
+// the copies themselves are counted below.
 template <int BYTES>
 __device__ inline void copy_lds(const i32x4 &rsrc, uint8_t *lds_dst, uint32_t voff)
 {
@@ -66,13 +65,13 @@ __device__ inline void copy_lds(const i32x4 &rsrc, uint8_t *lds_dst, uint32_t vo
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     if constexpr (BYTES == 16)
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                      :: "s"(at), "v"(voff), "s"(rsrc) : "memory");
     else if constexpr (BYTES == 4)
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                      :: "s"(at), "v"(voff), "s"(rsrc) : "memory");
     else
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds"
                      :: "s"(at), "v"(voff), "s"(rsrc) : "memory");
 }
 
@@ -112,30 +111,24 @@ __device__ inline void multiply_add(f32x4 &acc, const i32x4 &x, const i32x4 &y)
         acc = mfma_op(x, y, acc);
 }
 
-// 4 codes -> 4 bf16 values.  `scale`: E8M0 byte or fp32 bits.  LOW: what the
-// rounding to bf16 left over, rounded to bf16 itself.
-template <int MODE, bool LOW>
-__device__ inline void widen(int codes, uint32_t scale, int &lo, int &hi)
+// Two codes (the low or the HIGH half of four) -> two bf16 values.  `scale`: E8M0
+// byte or fp32 bits.  `low` (block scales): what the rounding to bf16 left over,
+// rounded to bf16 itself.
+template <int MODE, bool HIGH, bool LOW>
+__device__ inline uint32_t widen(int codes, uint32_t scale, uint32_t &low)
 {
     if constexpr (MODE == kScaleBlock) {
         const float s = __builtin_bit_cast(float, scale);
-        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(codes, false);
-        const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(codes, true);
-        const float v[4] = {a[0] * s, a[1] * s, b[0] * s, b[1] * s};
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            w[h] = pack_bf16x2(v[2 * h], v[2 * h + 1]);
-            if constexpr (LOW)
-                w[h] = pack_bf16x2(v[2 * h] - __builtin_bit_cast(float, w[h] << 16),
-                                   v[2 * h + 1] - __builtin_bit_cast(float, w[h] & 0xFFFF0000u));
-        }
-        lo = (int)w[0], hi = (int)w[1];
+        const auto c = __builtin_amdgcn_cvt_pk_f32_fp8(codes, HIGH);
+        const float v[2] = {c[0] * s, c[1] * s};
+        const uint32_t w = pack_bf16x2(v[0], v[1]);
+        if constexpr (LOW)
+            low = pack_bf16x2(v[0] - __builtin_bit_cast(float, w << 16), v[1] - __builtin_bit_cast(float, w & 0xFFFF0000u));
+        return w;
     } else {
         // the instruction takes the exponent field of its fp32 scale: 2^(e - 127), NaN for e = 255
         const float s = __builtin_bit_cast(float, MODE == kScaleMx ? scale << 23 : 0x3F800000u);
-        lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, false));
-        hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, true));
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, s, HIGH));
     }
 }
 
@@ -143,7 +136,7 @@ __device__ inline void widen(int codes, uint32_t scale, int &lo, int &hi)
 
 // Tile `wg` of the grid in the order of the groups, in each a raster over 4 tile
 // rows.  Workgroups go to the XCDs in turn (wg % 8) whatever they take, so an XCD
-// gets every eighth run of `chunk` neighbouring tiles: neighbours share their
+// gets every eighth run of 2^chunk_log2 neighbouring tiles (one group: one run): neighbours share their
 // operands' panels in its L2, and each XCD has its part of every group, which
 // groups of unequal size need (32 groups of 585 to 2933 rows, N 4096, K 2048,
 // block scales by row list: 997 us with four whole groups an XCD, 790 where all
@@ -151,23 +144,33 @@ __device__ inline void widen(int codes, uint32_t scale, int &lo, int &hi)
 struct Tile {
     int n, k, s;
 };
-__device__ inline Tile tile_at(int wg, int tiles_n, int tiles_k, int groups, int chunk)
+__device__ inline Tile tile_at(uint32_t wg, uint32_t tiles_n, uint32_t tiles_k, uint32_t groups, uint32_t chunk_log2)
 {
-    const int per = tiles_n * tiles_k, round = kNumXcd * chunk;
-    int t = wg;
-    if (wg < per * groups / round * round) {
-        const int i = wg / kNumXcd;
-        t = (i / chunk * kNumXcd + wg % kNumXcd) * chunk + i % chunk;
+    constexpr uint32_t kLog = 3;
+    static_assert(kNumXcd == 1 << kLog, "");
+    const uint32_t per = tiles_n * tiles_k, x = wg & (kNumXcd - 1), i = wg >> kLog;
+    uint32_t t = wg;
+    Tile r{0, 0, 0};
+    if (groups == 1) {       // one run an XCD
+        if (i < per >> kLog)
+            t = x * (per >> kLog) + i;
+    } else {
+        if (wg < (per * groups >> (kLog + chunk_log2)) << (kLog + chunk_log2))
+            t = (((i >> chunk_log2) << kLog | x) << chunk_log2) + (i & ((1u << chunk_log2) - 1));
+        r.s = (int)(t / per);
+        t -= (uint32_t)r.s * per;
     }
-    Tile r;
-    r.s = t / per;
-    raster_tile<int>(t - r.s * per, tiles_n, tiles_k, 4, r.n, r.k);
+    const uint32_t strip = t / (4 * tiles_k), rows = tiles_n - 4 * strip, in = t - strip * 4 * tiles_k;
+    if (rows >= 4)
+        r.n = (int)(4 * strip + (in & 3)), r.k = (int)(in >> 2);
+    else
+        r.n = (int)(4 * strip + in % rows), r.k = (int)(in / rows);
     return r;
 }
 
 // F: fragments of a wave along n and along k (4 waves, 2 x 2: a tile of 32 F).
 template <int MODE, int TERMS, int F, bool GATHER, bool BF16>
-__global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k, const int chunk)
+__global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k, const int chunk_log2)
 {
     constexpr bool kCodes = MODE != kScaleNone;
     constexpr bool kScaled = MODE == kScaleBlock || MODE == kScaleMx;
@@ -196,9 +199,9 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Tile tile = tile_at((int)blockIdx.x, tiles_n, tiles_k, (int)a.E * a.splits, chunk);
+    const Tile tile = tile_at(blockIdx.x, tiles_n, tiles_k, (uint32_t)a.E * a.splits, chunk_log2);
     const int n0 = tile.n * kCols, k0 = tile.k * kCols;
-    const int e = tile.s / a.splits, split = tile.s - e * a.splits;
+    const int e = a.splits == 1 ? tile.s : tile.s / a.splits, split = tile.s - e * a.splits;
 
     // The rows of this workgroup.
     int64_t lo = 0, hi = a.M;
@@ -299,22 +302,21 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
     };
     auto next_i = [&] { di = ri.rsrc(), ri.next(kStep * 4); };
 
-    // Codes 4 i .. 4 i + 3 of the wave's own piece (copy j) of one step, as bf16; with every
-    // second one eight values go to an LDS stage of x.
+    // Pair v of 8 of the wave's own codes (copy j) of one step, as bf16; with every fourth one
+    // eight values go to an LDS stage of x.
+    constexpr int kPairs = kCodes ? 8 * H : 0;
     i32x4 wide[TERMS];
-    auto convert = [&](int j, int i, const i32x4 &c, uint32_t s, int x_slot) {
-        uint8_t *d = lds + kOffX + x_slot * (TERMS * kTile) + (row_of[j % kIdx] >> 2) * kRow4 + (ccol >> 4) * 128 + (crow & 3) * 32;
-        int lo, hi;
-        widen<MODE, false>(c[i], s, lo, hi);
-        wide[0][i % 2 * 2] = lo, wide[0][i % 2 * 2 + 1] = hi;
-        if constexpr (TERMS == 2) {
-            widen<MODE, true>(c[i], s, lo, hi);
-            wide[1][i % 2 * 2] = lo, wide[1][i % 2 * 2 + 1] = hi;
-        }
-        if (i % 2 == 1) {
+    auto convert = [&](auto vc, const i32x4 &c, uint32_t s, int x_slot) {
+        constexpr int j = decltype(vc)::value / 8, v = decltype(vc)::value % 8;
+        uint32_t low = 0;
+        wide[0][v % 4] = (int)widen<MODE, v % 2 == 1, TERMS == 2>(c[v / 2], s, low);
+        if constexpr (TERMS == 2)
+            wide[1][v % 4] = (int)low;
+        if constexpr (v % 4 == 3) {
+            uint8_t *d = lds + kOffX + x_slot * (TERMS * kTile) + (row_of[j % kIdx] >> 2) * kRow4 + (ccol >> 4) * 128 + (crow & 3) * 32;
 #pragma unroll
             for (int q = 0; q < TERMS; ++q)
-                reinterpret_cast<i32x4 *>(d + q * kTile)[i / 2] = wide[q];
+                reinterpret_cast<i32x4 *>(d + q * kTile)[v / 4] = wide[q];
         }
     };
     auto read_codes = [&](int j, int slot, i32x4 &c, uint32_t &s) {
@@ -336,18 +338,19 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
 #pragma unroll
         for (int j = 0; j < F; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto read_frag = [&](auto pc, auto fc, int y_slot, int x_slot) {
-        constexpr int P = decltype(pc)::value, f = decltype(fc)::value;
-        if constexpr (f < F)
-            yf[P][f] = transposed(yfrag + y_slot * kTile + f * 128, 4 * kRow4);
-        else
-            xf[P][(f - F) / F][f % F] = transposed(xfrag + x_slot * (TERMS * kTile) + (f - F) / F * kTile + f % F * 128, 4 * kRow4);
+    // Half h (four of a lane's eight rows) of fragment f: F of Y's, then x's.
+    auto read_half = [&](auto pc, auto rc, int y_slot, int x_slot) {
+        constexpr int P = decltype(pc)::value, f = decltype(rc)::value / 2, h = decltype(rc)::value % 2;
+        i32x4 &d = f < F ? yf[P][f % F] : xf[P][f < F ? 0 : (f - F) / F][f % F];
+        const u32x2 v = transposed((f < F ? yfrag + y_slot * kTile : xfrag + x_slot * (TERMS * kTile) + (f - F) / F * kTile) +
+                                   f % F * 128 + h * 4 * kRow4);
+        d[2 * h] = (int)v.x, d[2 * h + 1] = (int)v.y;
     };
 
     // Group g of copies (one per step, and before the first step those of -kD + 1 .. -1):
     // Y of step g + kD, x of g + kD (codes: kD + 1), the row list for x of group g + kD + 1.
     constexpr int kAhead = kCodes ? 1 : 0;
-    constexpr int kFrags = F * (1 + TERMS), kSlots = F * F * TERMS / 4;     // a slot: 4 products
+    constexpr int kReads = 2 * F * (1 + TERMS), kProducts = F * F * TERMS;
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     int idx[kIdx];
@@ -395,16 +398,14 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kD - 2) * kGroup) : "memory");
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
+            i32x4 c[H];
+            uint32_t s[H];
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                i32x4 c;
-                uint32_t s;
-                read_codes(j, t, c, s);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    convert(j, i, c, s, t);
-            }
+            for (int j = 0; j < H; ++j)
+                read_codes(j, t, c[j], s[j]);
+            each_of<kPairs>([&](auto v) { convert(v, c[decltype(v)::value / 8], s[decltype(v)::value / 8], t); });
+        }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     first_group(-1);
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kD - 1) * kGroup) : "memory");
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    each_of<kFrags>([&](auto f) { read_frag(I0{}, f, 0, 0); });
+    each_of<kReads>([&](auto r) { read_half(I0{}, r, 0, 0); });
     // s % kD; stages s + 1 and s + 2
     int slot = 0;
     auto step = [&](auto pc, int s) {
@@ -426,44 +427,43 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
         __builtin_amdgcn_sched_barrier(0);
         i32x4 codes[kCodes ? H : 1];
         uint32_t scales[kCodes ? H : 1];
-        each_of<kSlots>([&](auto wc) {
-            constexpr int w = decltype(wc)::value;
-            constexpr int i = w * 4 / F % F, j0 = w * 4 % F, q = w * 4 / (F * F);
-            // fragments of the next step over the first three quarters
-            constexpr int f0 = w * 4 * kFrags / (3 * kSlots), f1 = (w + 1) * 4 * kFrags / (3 * kSlots);
-            each_of<(f0 < kFrags ? (f1 < kFrags ? f1 : kFrags) - f0 : 0)>([&](auto fc) {
-                read_frag(std::integral_constant<int, 1 - P>{}, std::integral_constant<int, f0 + decltype(fc)::value>{}, slot1,
+        // Behind each product no more than the matrix unit's 16 cycles let through.  Counted in
+        // products: the reads of codes and row indices first, the next step's fragments over the
+        // first three quarters, the copies over all but the last four, the conversion of the codes
+        // from an eighth on over five eighths, the next copies' ranges and offsets at the end.
+        each_of<kProducts>([&](auto mc) {
+            constexpr int m = decltype(mc)::value, q = m / (F * F), i = m / F % F, j = m % F;
+            multiply_add<F == 8>(acc[i][j], xf[P][q][i], yf[P][j]);
+            if constexpr (kCodes && m < H)
+                read_codes(m, slot2, codes[m], scales[m]);
+            if constexpr (GATHER && m == 2) {
+#pragma unroll
+                for (int t = 0; t < kIdx; ++t)
+                    idx[t] = reinterpret_cast<const int *>(lds + kOffIdx + (s + 1) % kIdxStages * kIdxStage + (t * 4 + wave) * 256)[lane];
+            }
+            constexpr auto part = [](int x, int first, int over, int all) {      // items before product x
+                return x <= first ? 0 : x >= first + over ? all : (x - first) * all / over;
+            };
+            constexpr int r0 = part(m, 0, kProducts * 3 / 4, kReads), r1 = part(m + 1, 0, kProducts * 3 / 4, kReads);
+            each_of<r1 - r0>([&](auto r) {
+                read_half(std::integral_constant<int, 1 - P>{}, std::integral_constant<int, r0 + decltype(r)::value>{}, slot1,
                           kCodes ? (s + 1) & 1 : slot1);
             });
-            if constexpr (kCodes && w < H)
-                read_codes(w, slot2, codes[w], scales[w]);
-            if constexpr (GATHER && w == 0) {
-#pragma unroll
-                for (int j = 0; j < kIdx; ++j)
-                    idx[j] = reinterpret_cast<const int *>(lds + kOffIdx + (s + 1) % kIdxStages * kIdxStage + (j * 4 + wave) * 256)[lane];
-            }
-            // copies over the slots, the next step's ranges and offsets behind them
-            constexpr int kSpan = kSlots - 1;
-            constexpr int c0 = w * kGroup / kSpan, c1 = (w + 1) * kGroup / kSpan;
-            each_of<(w < kSpan ? c1 - c0 : 0)>([&](auto c) {
+            constexpr int c0 = part(m, 0, kProducts - 4, kGroup), c1 = part(m + 1, 0, kProducts - 4, kGroup);
+            each_of<c1 - c0>([&](auto c) {
                 copy(std::integral_constant<int, c0 + decltype(c)::value>{}, slot, kCodes ? slot1 : slot, (s + kD + 1) % kIdxStages);
             });
-            // the codes' conversion over two thirds of the slots, from the third on
-            constexpr int kOver = kSlots * 2 / 3 < kSlots - 2 ? kSlots * 2 / 3 : kSlots - 2;
-            constexpr int v0 = (w - 2) * 4 * H / kOver, v1 = (w - 1) * 4 * H / kOver;
-            if constexpr (kCodes && w >= 2) {
-#pragma unroll
-                for (int v = v0; v < v1 && v < 4 * H; ++v)
-                    convert(v / 4, v % 4, codes[v / 4], scales[v / 4], s & 1);
-            }
-            if constexpr (w == kSlots - 1) {
-                next_y(), next_x(), next_i();
-                if constexpr (GATHER)
-                    place_x(idx), x_left -= kStep;
-            }
-#pragma unroll
-            for (int j = j0; j < j0 + 4; ++j)
-                multiply_add<F == 8>(acc[i][j], xf[P][q][i], yf[P][j]);
+            constexpr int v0 = part(m, kProducts / 8, kProducts * 5 / 8, kPairs), v1 = part(m + 1, kProducts / 8, kProducts * 5 / 8, kPairs);
+            each_of<v1 - v0>([&](auto v) {
+                constexpr int at = v0 + decltype(v)::value;
+                convert(std::integral_constant<int, at>{}, codes[at / 8], scales[at / 8], s & 1);
+            });
+            if constexpr (m == kProducts - 3)
+                next_y();
+            if constexpr (m == kProducts - 2)
+                next_x();
+            if constexpr (GATHER && m == kProducts - 1)
+                next_i(), place_x(idx), x_left -= kStep;
             __builtin_amdgcn_sched_barrier(0);
         });
         slot = slot1;
@@ -485,40 +485,49 @@ __global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kerne
     float scale = 1.0f;
     if (MODE == kScaleTensor && rows > 0)
         scale = static_cast<const float *>(a.S)[0];
-    const int64_t size = a.N * K;
-    int at_n = n0 + wn * (F * 16) + (lane & 15), at_k = k0 + wk * (F * 16) + (lane >> 4) * 4;
-    asm volatile("" : "+v"(at_n), "+v"(at_k));     // (addresses that are worked out here, not held through the loop)
-    auto each = [&](auto store) {
+    // N and K are multiples of 16, so a fragment is inside or outside as a whole.
+    const int nf = n0 + wn * (F * 16), kf = k0 + wk * (F * 16);
+    int l = lane;
+    asm volatile("" : "+v"(l));     // (addresses that are worked out here, not held through the loop)
+    const int64_t at = (int64_t)(nf + (l & 15)) * K + kf + (l >> 4) * 4, row16 = 16 * K;
+    auto each = [&](auto *c, auto store) {
+        c += at;
+        auto all = [&](auto full) {
+            auto *p = c;
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const int n = at_n + j * 16;
+            for (int j = 0; j < F; ++j, p += row16) {
+                if (!full && nf + j * 16 >= a.N)
+                    break;
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                const int k = at_k + i * 16;
-                if (n < a.N && k < K) {
-                    f32x4 v = acc[i][j];
-                    asm volatile("" : "+v"(v));     // (read here, not all 64 of them at the loop's end)
-                    if constexpr (MODE == kScaleTensor)
-                        v = v * scale;
-                    store((int64_t)n * K + k, v);
-                }
+                for (int i = 0; i < F; ++i)
+                    if (full || kf + i * 16 < K) {
+                        f32x4 v = acc[i][j];
+                        // (read here, not all 64 of them at the loop's end)
+                        asm volatile("" : "+v"(v));
+                        if constexpr (MODE == kScaleTensor)
+                            v = v * scale;
+                        store(p + i * 16, v);
+                    }
             }
-        }
+        };
+        if (n0 + kCols <= a.N && k0 + kCols <= K)
+            all(std::true_type{});
+        else
+            all(std::false_type{});
     };
-    if (a.splits > 1) {
-        float *c = a.ws + ((int64_t)split * a.E + e) * size;
-        each([&](int64_t at, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c + at) = v; });
-    } else if constexpr (BF16) {
-        uint16_t *c = static_cast<uint16_t *>(a.C) + (int64_t)e * size;
-        each([&](int64_t at, const f32x4 &v) {
-            *reinterpret_cast<u32x2 *>(c + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        });
-    } else if (a.accumulate) {
-        float *c = static_cast<float *>(a.C) + (int64_t)e * size;
-        each([&](int64_t at, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c + at) += v; });
+    const int64_t group = ((int64_t)split * a.E + e) * a.N * K;
+    auto write = [](float *c, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c) = v; };
+    if constexpr (BF16) {
+        if (a.splits > 1)
+            each(a.ws + group, write);
+        else
+            each(static_cast<uint16_t *>(a.C) + group, [](uint16_t *c, const f32x4 &v) {
+                *reinterpret_cast<u32x2 *>(c) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            });
+    } else if (a.accumulate && a.splits == 1) {
+        each(static_cast<float *>(a.C) + group, [](float *c, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c) += v; });
     } else {
-        float *c = static_cast<float *>(a.C) + (int64_t)e * size;
-        each([&](int64_t at, const f32x4 &v) { *reinterpret_cast<f32x4 *>(c + at) = v; });
+        each((a.splits > 1 ? a.ws : static_cast<float *>(a.C)) + group, write);
     }
 }
 
@@ -561,9 +570,10 @@ void launch_tile(const WgradArgs &a, hipStream_t s)
 {
     const int64_t tile = 32 * F, tn = (a.N + tile - 1) / tile, tk = (a.K + tile - 1) / tile;
     const unsigned grid = (unsigned)(tn * tk * a.E * a.splits);
-    // one group: an eighth of its tiles each; several: an eighth of one's, 4 to 32 tiles
-    const int64_t per = tn * tk, groups = a.E * a.splits;
-    const int chunk = (int)(groups == 1 ? std::max<int64_t>(per / kNumXcd, 1) : std::clamp<int64_t>(per / kNumXcd, 4, 32));
+    // several groups: runs of an eighth of one's tiles, 4 to 32
+    int chunk = 2;
+    while (chunk < 5 && tn * tk >= (int64_t)kNumXcd << (chunk + 1))
+        ++chunk;
     if (a.rows)
         wgrad_kernel<MODE, TERMS, F, true, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk, chunk);
     else
