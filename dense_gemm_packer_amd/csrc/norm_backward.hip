@@ -24,31 +24,39 @@ namespace dgp {
 
 namespace {
 
-// Sums of N values over the T threads of a row, in every thread.  The W / T
-// rows of the workgroup do this at the same time; `red` (N x W / 64 values) is
-// not written again before the second barrier from here.
-template <int T, int W, int N>
-__device__ inline void sums(float (&v)[N], float (*red)[W / 64])
+// Sums of N values over the threads of a row, in every thread: up to WAVES waves
+// (1, 4, 8 or 16), whose sums stand from `first` on in `red`; t: the thread of
+// the row.  `red` holds zeros for waves that are not there, and is not written
+// again before the second barrier from here.
+template <int WAVES, int N>
+__device__ inline void sums(float (&v)[N], f32x4 (*red)[WAVES == 16 ? 4 : 2], int first, int t)
 {
 #pragma unroll
     for (int n = 0; n < N; ++n)
-        v[n] = sum64(v[n]);
-    if constexpr (T > 64) {
-        if ((threadIdx.x & 63) == 0) {
+        v[n] = total64(v[n]);
+    if constexpr (WAVES > 1) {
+        if ((t & 63) == 0) {
 #pragma unroll
             for (int n = 0; n < N; ++n)
-                red[n][threadIdx.x >> 6] = v[n];
+                reinterpret_cast<float *>(red[n])[first + (t >> 6)] = v[n];
         }
         __syncthreads();
-        const int first = (int)(threadIdx.x / T) * (T / 64);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            v[n] = red[n][first];
+            f32x4 s = red[n][first / 4];
 #pragma unroll
-            for (int w = 1; w < T / 64; ++w)
-                v[n] += red[n][first + w];
+            for (int q = 1; q < WAVES / 4; ++q)
+                s += red[n][first / 4 + q];
+            v[n] = (s[0] + s[1]) + (s[2] + s[3]);
         }
     }
+}
+
+// Zeros in all of an array of `red`, before its first use (a barrier follows).
+__device__ inline void clear(f32x4 *red, int n)
+{
+    if ((int)threadIdx.x < n)
+        red[threadIdx.x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
 template <int XT>
@@ -62,86 +70,107 @@ __device__ inline void load_weight(const NormGradArgs &a, int c, float (&w)[8])
 
 }  // namespace
 
-// T threads own a row (W / T rows of a workgroup at once), C pieces of 8
-// elements each; the next row's loads are in flight while this one's sums go
-// through the lanes.
-template <int XT, int MODE, int T, int W, int C, bool LN>
-__global__ __launch_bounds__(W) void norm_grad_kernel(const NormGradArgs a)
+// A row's pieces of 8 elements go to T = blockDim.x / R threads, C each; R rows
+// of a workgroup at once (WAVE: a wave a row, no barriers).  The next row's loads
+// are in flight while this one's sums go through the lanes.  To leave registers
+// for two workgroups a CU the weight waits in LDS and dy as it was loaded.
+template <int XT, int MODE, int C, int R, bool WAVE, int THREADS, bool LN>
+__global__ __launch_bounds__(THREADS, C == 1 ? 4 : XT == kTypeF32 ? 2 : WAVE ? 3 : 4) void norm_grad_kernel(const NormGradArgs a)
 {
-    constexpr int R = W / T;
-    const int t = threadIdx.x % T, sub = threadIdx.x / T;
-    const int k8 = (int)(a.K / 8);
+    const int T = WAVE ? 64 : (int)blockDim.x / R;
+    const int rows_at_once = WAVE ? (int)blockDim.x / 64 : R;
+    const int sub = WAVE || R > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
+    const int t = (int)threadIdx.x - sub * T;
+    constexpr int kWaves = WAVE ? 1 : 8 / R;       // of a row, at most
+    const int k8 = (int)(a.K / 8), first_wave = WAVE ? 0 : sub * kWaves;
     const float invk = 1.0f / (float)a.K;
-    const int64_t stride = (int64_t)gridDim.x * R;
-    __shared__ float red1[2][2][W / 64];
-    [[maybe_unused]] __shared__ float red2[3][W / 64];
+    const int64_t stride = (int64_t)gridDim.x * rows_at_once;
+    constexpr int kPieces = WAVE ? 64 * C : THREADS / R * C;
+    __shared__ f32x4 weight[2][kPieces];       // halves of pieces
+    __shared__ f32x4 red1[2][2][2];
+    [[maybe_unused]] __shared__ f32x4 red2[3][2];
 
-    Raw8<XT> ry[C], rr[C];
+    Raw8<XT> ry[C];
     Kept8<XT, MODE> rx[C];
     auto load = [&](int64_t row) {
+        if (row < a.M) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int p = t + c * T;
-            if (p < k8 && row < a.M) {
-                ry[c] = load_raw8<XT>(a.Y, row * a.ldy + p * 8);
-                rx[c] = load_kept8<XT, MODE>(a.X, a.S, row, a.ldx, a.K / 128, p * 8);
+            for (int c = 0; c < C; ++c) {
+                const int p = t + c * T;
+                if (p < k8) {
+                    ry[c] = load_raw8<XT>(a.Y, row * a.ldy + p * 8);
+                    rx[c] = load_kept8<XT, MODE>(a.X, a.S, row, a.ldx, a.K / 128, p * 8);
+                }
             }
         }
     };
-    auto load_r = [&](int64_t row) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (t + c * T < k8 && row < a.M)
-                rr[c] = load_raw8<XT>(a.R, row * a.ldr + (t + c * T) * 8);
-    };
-
-    float w[C][8], dw[C][8];
+    float dw[C][8];
     [[maybe_unused]] float db[LN ? C : 1][8];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        if (t + c * T < k8)
-            load_weight<XT>(a, t + c * T, w[c]);
+    for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             dw[c][i] = 0.0f;
             if constexpr (LN)
                 db[c][i] = 0.0f;
         }
-    }
-    const int64_t row0 = (int64_t)blockIdx.x * R;
+    const int64_t row0 = (int64_t)blockIdx.x * rows_at_once;
     load(row0 + sub);
+    for (int p = (int)threadIdx.x; p < k8; p += (int)blockDim.x) {
+        float w[8];
+        load_weight<XT>(a, p, w);
+        weight[0][p] = f32x4{w[0], w[1], w[2], w[3]};
+        weight[1][p] = f32x4{w[4], w[5], w[6], w[7]};
+    }
+    if constexpr (!WAVE) {
+        clear(red1[0][0], 8);
+        clear(red2[0], 6);
+    }
+    __syncthreads();
     int turn = 0;
     for (int64_t base = row0; base < a.M; base += stride, turn ^= 1) {   // (the same count in every thread)
         const int64_t row = base + sub;
         const bool live = row < a.M;
-        if (a.R)
-            load_r(row);
-        float x[C][8], y[C][8];
+        Raw8<XT> rr[C], y[C];
+        float x[C][8], g[C][8];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (live && t + c * T < k8) {
-                to_float8<XT>(ry[c], y[c]);
+                if (a.R)
+                    rr[c] = load_raw8<XT>(a.R, row * a.ldr + (t + c * T) * 8);
+                y[c] = ry[c];
                 kept_floats<XT, MODE>(rx[c], x[c]);
             } else {
+                y[c] = Raw8<XT>{};
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    x[c][i] = y[c][i] = 0.0f;
+                    x[c][i] = 0.0f;
             }
         }
         load(row + stride);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float v[8];
+            to_float8<XT>(y[c], v);
+            const int p = t + c * T < k8 ? t + c * T : 0;
+            const f32x4 w0 = weight[0][p], w1 = weight[1][p];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g[c][i] = v[i] * w0[i];
+                g[c][i + 4] = v[i + 4] * w1[i];
+            }
+        }
         float rstd, mg = 0.0f, c2;
         if constexpr (LN) {
             float s1[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                if (t + c * T < k8) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        s1[0] += x[c][i];
-                        s1[1] = __builtin_fmaf(y[c][i], w[c][i], s1[1]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    s1[0] += x[c][i];
+                    s1[1] += g[c][i];
                 }
-            sums<T, W>(s1, red1[turn]);
+            sums<kWaves>(s1, red1[turn], first_wave, t);
             const float mean = s1[0] * invk;
             mg = s1[1] * invk;
             float s2[3] = {0.0f, 0.0f, 0.0f};
@@ -151,12 +180,13 @@ __global__ __launch_bounds__(W) void norm_grad_kernel(const NormGradArgs a)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         x[c][i] -= mean;
+                        g[c][i] -= mg;
                         s2[0] += x[c][i];
                         s2[1] = __builtin_fmaf(x[c][i], x[c][i], s2[1]);
-                        s2[2] = __builtin_fmaf(y[c][i] * w[c][i] - mg, x[c][i], s2[2]);
+                        s2[2] = __builtin_fmaf(g[c][i], x[c][i], s2[2]);
                     }
                 }
-            sums<T, W>(s2, red2);
+            sums<kWaves>(s2, red2, first_wave, t);
             const float rest = s2[0] * invk;       // what the fp32 mean is off by
             const float var = s2[1] * invk - rest * rest;
             rstd = 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
@@ -170,14 +200,12 @@ __global__ __launch_bounds__(W) void norm_grad_kernel(const NormGradArgs a)
             float s1[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                if (t + c * T < k8) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        s1[0] = __builtin_fmaf(x[c][i], x[c][i], s1[0]);
-                        s1[1] = __builtin_fmaf(y[c][i] * w[c][i], x[c][i], s1[1]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    s1[0] = __builtin_fmaf(x[c][i], x[c][i], s1[0]);
+                    s1[1] = __builtin_fmaf(g[c][i], x[c][i], s1[1]);
                 }
-            sums<T, W>(s1, red1[turn]);
+            sums<kWaves>(s1, red1[turn], first_wave, t);
             rstd = 1.0f / __builtin_sqrtf(s1[0] * invk + a.eps);
             c2 = s1[1] * invk * rstd;
         }
@@ -185,21 +213,21 @@ __global__ __launch_bounds__(W) void norm_grad_kernel(const NormGradArgs a)
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 if (t + c * T < k8) {
-                    float d[8], r[8];
-                    if (a.R)
-                        to_float8<XT>(rr[c], r);
+                    float d[8], v[8];
+                    to_float8<XT>(y[c], v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float xh = x[c][i] * rstd;
-                        dw[c][i] = __builtin_fmaf(y[c][i], xh, dw[c][i]);
+                        dw[c][i] = __builtin_fmaf(v[i], xh, dw[c][i]);
                         if constexpr (LN)
-                            db[c][i] += y[c][i];
-                        float g = y[c][i] * w[c][i];
-                        if constexpr (LN)
-                            g -= mg;
-                        d[i] = rstd * (g - xh * c2);
-                        if (a.R)
-                            d[i] += r[i];
+                            db[c][i] += v[i];
+                        d[i] = rstd * __builtin_fmaf(-xh, c2, g[c][i]);
+                    }
+                    if (a.R) {
+                        to_float8<XT>(rr[c], v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            d[i] += v[i];
                     }
                     store8<XT>(a.D, row * a.K + (t + c * T) * 8, d);
                 }
@@ -207,9 +235,9 @@ __global__ __launch_bounds__(W) void norm_grad_kernel(const NormGradArgs a)
     }
 
     // The rows of the workgroup join their sums, one after the other.
-    if constexpr (R > 1) {
-        __shared__ float join[LN ? 2 : 1][T * C * 8];
-        for (int r = 1; r < R; ++r) {
+    if constexpr (WAVE || R > 1) {
+        __shared__ float join[LN ? 2 : 1][kPieces * 8];
+        for (int r = 1; r < rows_at_once; ++r) {
             __syncthreads();
             if (sub == r) {
 #pragma unroll
@@ -283,7 +311,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_grad_long_kernel(const Norm
     constexpr int T = kLongThreads;
     const int t = threadIdx.x, k8 = (int)(a.K / 8);
     const float invk = 1.0f / (float)a.K;
-    __shared__ float red1[2][2][T / 64], red2[3][T / 64];
+    __shared__ f32x4 red1[2][2][4], red2[3][4];
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
         float x[8], y[8], w[8];
@@ -302,7 +330,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_grad_long_kernel(const Norm
                 s1[1] = __builtin_fmaf(y[i] * w[i], LN ? 1.0f : x[i], s1[1]);
             }
         }
-        sums<T, T>(s1, red1[turn]);
+        sums<16>(s1, red1[turn], 0, t);
         if constexpr (LN) {
             mean = s1[0] * invk, mg = s1[1] * invk;
             float s2[3] = {0.0f, 0.0f, 0.0f};
@@ -316,7 +344,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_grad_long_kernel(const Norm
                     s2[2] = __builtin_fmaf(y[i] * w[i] - mg, d, s2[2]);
                 }
             }
-            sums<T, T>(s2, red2);
+            sums<16>(s2, red2, 0, t);
             rest = s2[0] * invk;
             const float var = s2[1] * invk - rest * rest;
             rstd = 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
@@ -393,29 +421,25 @@ namespace {
 
 constexpr int64_t kLongRow = 8192;     // elements; longer rows take the two kernels above
 
-// Workgroups of the row kernel: R rows of a workgroup at once.
+// Threads of the row kernel's workgroups, and rows of each at once.
 struct Shape {
-    int T, W, C;
+    int threads, rows;
 };
 Shape shape_of(int64_t K)
 {
-    const int64_t k8 = K / 8;
-    if (k8 <= 64)
-        return {64, 512, 1};
+    const int k8 = (int)(K / 8);
     if (k8 <= 128)
-        return {64, 512, 2};
+        return {512, 8};                                 // a wave a row
     if (k8 <= 256)
-        return {256, 512, 1};
-    if (k8 <= 512)
-        return {512, 512, 1};
-    return {512, 512, 2};
+        return {(k8 + 63) / 64 * 128, 2};
+    const int each = k8 <= 512 ? 1 : 2;                  // pieces a thread
+    return {((k8 + each - 1) / each + 63) / 64 * 64, 1};
 }
 
 int64_t row_groups(int64_t M, int64_t K)
 {
     const Shape p = shape_of(K);
-    const int64_t rows = p.W / p.T, all = (M + rows - 1) / rows;
-    return std::min<int64_t>(all, 512);
+    return std::min<int64_t>((M + p.rows - 1) / p.rows, 512);
 }
 
 int64_t long_slabs(int64_t M) { return std::clamp<int64_t>(M / 32, 1, 64); }
@@ -437,17 +461,18 @@ hipError_t launch_grad(const NormGradArgs &a, hipStream_t s)
     } else {
         count = row_groups(a.M, a.K);
         const unsigned grid = (unsigned)count;
-        const Shape p = shape_of(a.K);
-        if (p.T == 64 && p.C == 1)
-            norm_grad_kernel<XT, MODE, 64, 512, 1, LN><<<grid, 512, 0, s>>>(a);
-        else if (p.T == 64)
-            norm_grad_kernel<XT, MODE, 64, 512, 2, LN><<<grid, 512, 0, s>>>(a);
-        else if (p.T == 256)
-            norm_grad_kernel<XT, MODE, 256, 512, 1, LN><<<grid, 512, 0, s>>>(a);
-        else if (p.T == 512 && p.C == 1)
-            norm_grad_kernel<XT, MODE, 512, 512, 1, LN><<<grid, 512, 0, s>>>(a);
+        const int threads = shape_of(a.K).threads;
+        const int64_t k8 = a.K / 8;
+        if (k8 <= 64)
+            norm_grad_kernel<XT, MODE, 1, 1, true, 512, LN><<<grid, threads, 0, s>>>(a);
+        else if (k8 <= 128)
+            norm_grad_kernel<XT, MODE, 2, 1, true, 512, LN><<<grid, threads, 0, s>>>(a);
+        else if (k8 <= 256)
+            norm_grad_kernel<XT, MODE, 1, 2, false, 512, LN><<<grid, threads, 0, s>>>(a);
+        else if (k8 <= 512)
+            norm_grad_kernel<XT, MODE, 1, 1, false, 512, LN><<<grid, threads, 0, s>>>(a);
         else
-            norm_grad_kernel<XT, MODE, 512, 512, 2, LN><<<grid, 512, 0, s>>>(a);
+            norm_grad_kernel<XT, MODE, 2, 1, false, 512, LN><<<grid, threads, 0, s>>>(a);
         if (count == 1)
             return hipGetLastError();
     }

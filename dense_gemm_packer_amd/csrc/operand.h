@@ -125,6 +125,19 @@ __device__ inline float sum64(float s)
     return s + __shfl_xor(s, 32);
 }
 
+// The sum over the wave as a scalar, without a trip through LDS: rows of 16
+// lanes, then rows 0 and 2 onto 1 and 3, then 1 onto 2 and 3; lane 63 has it.
+__device__ inline float total64(float s)
+{
+    s = fdpp_add(s, dpp<kQuadXor1>(__builtin_bit_cast(uint32_t, s)));
+    s = fdpp_add(s, dpp<kQuadXor2>(__builtin_bit_cast(uint32_t, s)));
+    s = fdpp_add(s, dpp<kRowHalfMirror>(__builtin_bit_cast(uint32_t, s)));
+    s = fdpp_add(s, dpp<kRowMirror>(__builtin_bit_cast(uint32_t, s)));
+    s = fdpp_add(s, (uint32_t)__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x142, 0xA, 0xF, false));   // row_bcast 15
+    s = fdpp_add(s, (uint32_t)__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x143, 0xC, 0xF, false));   // row_bcast 31
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s), 63));
+}
+
 // ----------------------------------------------------------------- scales
 
 // fp32 scale of a block (NaN for a block that is not finite).
