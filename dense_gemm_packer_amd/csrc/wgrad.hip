@@ -26,6 +26,7 @@
 // copies of s + kD are sent off, all of it placed between the products by hand
 // (one wave per SIMD: nothing else hides a stall).  One barrier a step.
 #include <algorithm>
+#include <cmath>
 
 #include "gemm_common.h"
 
@@ -170,13 +171,13 @@ __device__ inline Tile tile_at(uint32_t wg, uint32_t tiles_n, uint32_t tiles_k, 
 
 // F: fragments of a wave along n and along k (4 waves, 2 x 2: a tile of 32 F).
 template <int MODE, int TERMS, int F, bool GATHER, bool BF16>
-__global__ __launch_bounds__(256, F == 8 || TERMS == 2 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k, const int chunk_log2)
+__global__ __launch_bounds__(256, F == 8 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k, const int chunk_log2)
 {
     constexpr bool kCodes = MODE != kScaleNone;
     constexpr bool kScaled = MODE == kScaleBlock || MODE == kScaleMx;
     constexpr int kCols = 32 * F;                        // tile
     constexpr int H = F / 4;                             // 128-column halves
-    constexpr int kD = TERMS == 2 && F == 8 ? 3 : 4;     // steps that the copies run ahead
+    constexpr int kD = 3;                                // steps that the copies run ahead (4 and 5: the same times)
     constexpr int kRow4 = kCols * 8;                     // bytes of 4 rows x kCols in LDS
     constexpr int kTile = kStep * kCols * 2;             // bytes of a bf16 stage
     constexpr int kXStages = kCodes ? 2 : kD;
@@ -551,16 +552,41 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float *ws, void *
 
 // --------------------------------------------------------------- launches
 
+// Tile and parts of a group's rows, by estimated time (us): with W workgroups of
+// `steps` steps and out MB of results (fp32 partial ones where there are parts),
+//
+//   256: 5.5 + ceil(W / 256) (7.1 + steps (0.59 + 0.11 min(1, W / 256))) + out / 12.8
+//   128: 4.7 + ceil(W / 256) (2.1 + 0.29 steps) + (0.075 steps, a workgroup a CU at most) + out / 12.8
+//   parts: 3.6 + out / 6.4 for adding them up
+//
+// fitted to graph timings of 58 shapes (64 to 20000 rows, 256 x 256 to 8192 x 8192,
+// 1 to 64 groups, up to 14 choices each): the choice is on average 0.6 % slower
+// than the fastest (at worst 14 %: 2048 rows, 512 x 1024).  The 128 tile reads twice
+// the bytes for a product, 14 TB/s out of the L2s with four workgroups a CU (1.2 us
+// for a step of theirs, where the 256 tile takes 0.7 for the same products); it is
+// there for weights with too few large tiles, as parts are (8192 rows, 2048 x 2048:
+// 128 tile 80 us, 256 tile in one part 155, in four 74).
 WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K, int64_t E)
 {
-    auto tiles = [&](int64_t t) { return (N + t - 1) / t * ((K + t - 1) / t) * E; };
-    const int64_t rows = M / (E > 0 ? E : 1);
-    WgradPlan p{tiles(256) >= 192 ? 256 : 128, 1};
-    if (p.tile == 128) {
-        while (p.splits < 16 && tiles(128) * p.splits < 256 && rows / (p.splits * 2) >= 256)
-            p.splits *= 2;
-    }
-    return p;
+    const int64_t rows = (M + E - 1) / E;
+    WgradPlan best{128, 1};
+    double least = 0;
+    for (const int tile : {128, 256})
+        for (const int parts : {1, 2, 3, 4, 6, 8, 16}) {
+            if (parts > 1 && rows < parts * 96)
+                break;
+            const double w = (double)((N + tile - 1) / tile) * (double)((K + tile - 1) / tile) * (double)E * parts;
+            const double rounds = std::ceil(w / kNumCu), steps = (double)((rows + parts * 64 - 1) / (parts * 64) * 2);
+            const double out = (double)E * (double)N * (double)K * 4e-6 * parts;
+            double us = out / 12.8 + (parts > 1 ? 3.6 + out / 6.4 : 0.0);
+            if (tile == 256)
+                us += 5.5 + rounds * (7.1 + steps * (0.59 + 0.11 * std::min(1.0, w / kNumCu)));
+            else
+                us += 4.7 + rounds * (2.1 + 0.29 * steps) + (w <= kNumCu ? 0.075 * steps : 0.0);
+            if (least == 0 || us < least)
+                best = {tile, parts}, least = us;
+        }
+    return best;
 }
 
 namespace {

@@ -55,9 +55,9 @@ def test_exact(mode, out, m, n, k):
 
 @pytest.mark.parametrize("mode", list(GRAD_MODES))
 @pytest.mark.parametrize("out", list(OUTS))
-@pytest.mark.parametrize("m,n,k", [(1, 4096, 3968), (97, 4112, 4096), (320, 3600, 4480)])
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 3968), (97, 4112, 4096), (320, 3600, 4480), (4101, 2112, 2048), (9000, 1040, 1152)])
 def test_exact_large_tiles(mode, out, m, n, k):
-    """Enough 256 x 256 tiles for the whole GPU."""
+    """Enough 256 x 256 tiles for the whole GPU, or made enough by parts of the rows."""
     X, S, xv = whole(mode, m, k, m)
     dY, d = grads(m, n, 5)
     want = (d.float().to(DEV).t() @ xv.float().to(DEV)).cpu().double()     # (whole numbers of eighths: exact in any order)
