@@ -110,26 +110,25 @@ __device__ inline void load_weight(const NormGradArgs &a, int c, float (&w)[8])
 
 }  // namespace
 
-// A row's pieces of 8 elements go to T = blockDim.x / R threads, one each; R rows
-// of a workgroup side by side (WAVE: a wave a row, no barriers).  The next row's
-// loads are in flight while this one's sums go through the lanes; to leave registers for four waves a SIMD the weight waits in
-// LDS (4096 x 8192 bf16 with a residual, layer norm: 60 us, in registers 67) and
-// dy as it was loaded.
-template <int XT, int MODE, int R, bool WAVE, bool LN>
-__global__ __launch_bounds__(1024, 4) void norm_grad_kernel(const NormGradArgs a)
+// A row's pieces of 8 elements go to T threads (whole waves), one each; `side` =
+// blockDim.x / T rows of a workgroup side by side.  WAVES: 1 (a wave a row, no
+// barriers), 4, 8 or 16, room for the sums of a row's waves.  The next row's loads
+// are in flight while this one's sums go through the lanes; to leave registers for
+// four waves a SIMD the weight waits in LDS (4096 x 8192 bf16 with a residual,
+// layer norm: 60 us, in registers 67) and dy as it was loaded.
+template <int XT, int MODE, int WAVES, bool LN>
+__global__ __launch_bounds__(1024, 4) void norm_grad_kernel(const NormGradArgs a, const int rows_side, const int T)
 {
-    constexpr int kThreads = 1024;                            // at most
-    constexpr int kWaves = WAVE ? 1 : kThreads / 64 / R;      // of a row, at most
-    constexpr int kRed = kThreads / 256;
-    const int T = WAVE ? 64 : (int)blockDim.x / R;
-    const int side = WAVE ? (int)blockDim.x / 64 : R;         // rows side by side
-    const int sub = WAVE || R > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
+    constexpr bool kSide = WAVES < 16;                        // several rows
+    const int side = kSide ? rows_side : 1;
+    constexpr int kRed = WAVES == 4 ? 8 : WAVES == 8 ? 6 : 4; // 8 rows of 4, 3 of 8, 1 of 16
+    const int sub = kSide ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
     const int t = (int)threadIdx.x - sub * T;                 // the piece
     const bool mine = t < (int)(a.K / 8);
-    const int first_wave = WAVE ? 0 : sub * kWaves;
+    const int first_wave = sub * WAVES;
     const float invk = 1.0f / (float)a.K;
     const int64_t stride = (int64_t)gridDim.x * side;
-    constexpr int kPieces = WAVE ? 64 : kThreads / R;
+    constexpr int kPieces = WAVES * 64;
     __shared__ f32x4 weight[2][kPieces];                      // halves of pieces
     __shared__ f32x4 red1[2][2][kRed];
     [[maybe_unused]] __shared__ f32x4 red2[3][kRed];
@@ -166,7 +165,7 @@ __global__ __launch_bounds__(1024, 4) void norm_grad_kernel(const NormGradArgs a
         weight[0][t] = f32x4{w[0], w[1], w[2], w[3]};
         weight[1][t] = f32x4{w[4], w[5], w[6], w[7]};
     }
-    if constexpr (!WAVE) {
+    if constexpr (WAVES > 1) {
         clear(red1[0][0], 4 * kRed);
         clear(red2[0], 3 * kRed);
     }
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(1024, 4) void norm_grad_kernel(const NormGradArgs a
                 s1[0] += x[i];
                 s1[1] += g[i];
             }
-            sums<kWaves>(s1, red1[P], first_wave, t);
+            sums<WAVES>(s1, red1[P], first_wave, t);
             const float mean = mine ? s1[0] * invk : 0.0f, mg = mine ? s1[1] * invk : 0.0f;
             float s2[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -204,7 +203,7 @@ __global__ __launch_bounds__(1024, 4) void norm_grad_kernel(const NormGradArgs a
                 s2[1] = __builtin_fmaf(x[i], x[i], s2[1]);
                 s2[2] = __builtin_fmaf(g[i], x[i], s2[2]);
             }
-            sums<kWaves>(s2, red2, first_wave, t);
+            sums<WAVES>(s2, red2, first_wave, t);
             const float rest = s2[0] * invk;       // what the fp32 mean is off by
             const float var = s2[1] * invk - rest * rest;
             rstd = 1.0f / __builtin_sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
@@ -219,7 +218,7 @@ __global__ __launch_bounds__(1024, 4) void norm_grad_kernel(const NormGradArgs a
                 s1[0] = __builtin_fmaf(x[i], x[i], s1[0]);
                 s1[1] = __builtin_fmaf(g[i], x[i], s1[1]);
             }
-            sums<kWaves>(s1, red1[P], first_wave, t);
+            sums<WAVES>(s1, red1[P], first_wave, t);
             rstd = 1.0f / __builtin_sqrtf(s1[0] * invk + a.eps);
             c2 = s1[1] * invk * rstd;
         }
@@ -247,38 +246,38 @@ __global__ __launch_bounds__(1024, 4) void norm_grad_kernel(const NormGradArgs a
             step(std::integral_constant<int, 1>{}, base + stride + sub);
     }
 
-    // The rows side by side join their sums, one after the other.
-    if constexpr (WAVE || R > 1) {
-        __shared__ float join[LN ? 2 : 1][kPieces * 8];
-        for (int r = 1; r < side; ++r) {
-            __syncthreads();
-            if (sub == r) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    join[0][i * T + t] = dw[i];
-                    if constexpr (LN)
-                        join[1][i * T + t] = db[i];
-                }
-            }
-            __syncthreads();
-            if (sub == 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dw[i] += join[0][i * T + t];
-                    if constexpr (LN)
-                        db[i] += join[1][i * T + t];
-                }
-            }
-        }
-    }
-    if (sub != 0 || !mine)
-        return;
     const bool alone = gridDim.x == 1;
     float *pw = alone ? a.dW : a.ws + (int64_t)blockIdx.x * (LN ? 2 : 1) * a.K;
     float *pb = alone ? a.dB : pw + a.K;
-    store8<kTypeF32>(pw, t * 8, dw);
-    if (LN && pb)
-        store8<kTypeF32>(pb, t * 8, db);
+    if constexpr (!kSide) {
+        if (!mine)
+            return;
+        store8<kTypeF32>(pw, t * 8, dw);
+        if (LN && pb)
+            store8<kTypeF32>(pb, t * 8, db);
+    } else {
+        // The rows side by side put their sums into LDS, and every thread adds up those
+        // of a quad of columns, in order (16 391 x 512 bf16, sixteen rows: 17.3 us; row
+        // after row, two barriers each, 19.5).
+        constexpr int kQuads = LN ? 4 : 2;                    // dw, db: halves of pieces
+        __shared__ f32x4 join[kQuads * 1024];
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+            const float *v = (q < 2 ? dw : db) + q % 2 * 4;
+            join[(q * side + sub) * T + t] = f32x4{v[0], v[1], v[2], v[3]};
+        }
+        __syncthreads();
+        // (every wave is in one quad's range: T is whole waves)
+        for (int c = (int)threadIdx.x; c < kQuads * T; c += (int)blockDim.x) {
+            const int q = c / T, piece = c - q * T;
+            float *p = q < 2 ? pw : pb;
+            f32x4 sum = join[q * side * T + piece];
+            for (int r = 1; r < side; ++r)
+                sum += join[(q * side + r) * T + piece];
+            if (p && piece < (int)(a.K / 8))
+                *reinterpret_cast<f32x4 *>(p + piece * 8 + q % 2 * 4) = sum;
+        }
+    }
 }
 
 // Partial sums [parts][len] (len = one or two times K) -> dW, dB.  A workgroup
@@ -427,25 +426,28 @@ namespace {
 
 constexpr int64_t kLongRow = 8192;     // elements; longer rows take the two kernels above
 
-// The row kernel: rows side by side in a workgroup of up to 16 waves, by the row's
-// length.  One workgroup a CU writes the fewest partial sums, and side by side the
-// short rows share its barriers: 16 391 x 2048 mxfp8, root-mean-square norm, four
-// rows in 16 waves 43.7 us, two in 8 (two workgroups a CU) 46.4; 4096 x 4096 bf16,
-// layer norm, two in 16 waves 30.7, one in 8 33.2.
+// The row kernel: as many rows side by side as make up 16 waves.  One workgroup a
+// CU writes the fewest partial sums, and side by side the short rows share its
+// barriers: 16 391 x 2304 bf16, layer norm, three rows 65 us, two 71; 4096 x 4096
+// two rows 30.7, one 33.2; 16 391 x 2048 mxfp8, root-mean-square norm, four rows
+// 43.7, two in 8 waves (two workgroups a CU) 46.4.  With few rows the waves of one
+// workgroup wait for each other to no end: 128 workgroups then (256 x 512 bf16 6.6
+// us, sixteen rows in each of 16 workgroups 9.4; 256 workgroups, whose partial sums
+// are more to add up, 7.5).
 struct Shape {
-    int side, threads;
+    int side, waves;       // rows, waves of a row
+    int threads() const { return side * waves * 64; }
 };
-Shape shape_of(int64_t K)
+Shape shape_of(int64_t M, int64_t K)
 {
     const int waves = (int)((K / 8 + 63) / 64);
-    const int side = waves == 1 ? 16 : waves <= 4 ? 4 : waves <= 8 ? 2 : 1;
-    return {side, side * waves * 64};
+    return {(int)std::min<int64_t>(16 / waves, (M + 127) / 128), waves};
 }
 
 int64_t row_groups(int64_t M, int64_t K)
 {
-    const Shape p = shape_of(K);
-    return std::min<int64_t>((M + p.side - 1) / p.side, 256 * (1024 / p.threads));
+    const Shape p = shape_of(M, K);
+    return std::min<int64_t>((M + p.side - 1) / p.side, 256);
 }
 
 int64_t long_slabs(int64_t M) { return std::clamp<int64_t>(M / 32, 1, 64); }
@@ -467,15 +469,16 @@ hipError_t launch_grad(const NormGradArgs &a, hipStream_t s)
     } else {
         count = row_groups(a.M, a.K);
         const unsigned grid = (unsigned)count;
-        const Shape p = shape_of(a.K);
-        if (p.side == 16)
-            norm_grad_kernel<XT, MODE, 1, true, LN><<<grid, p.threads, 0, s>>>(a);
-        else if (p.side == 4)
-            norm_grad_kernel<XT, MODE, 4, false, LN><<<grid, p.threads, 0, s>>>(a);
-        else if (p.side == 2)
-            norm_grad_kernel<XT, MODE, 2, false, LN><<<grid, p.threads, 0, s>>>(a);
+        const Shape p = shape_of(a.M, a.K);
+        const int T = p.waves * 64;
+        if (p.waves == 1)
+            norm_grad_kernel<XT, MODE, 1, LN><<<grid, p.threads(), 0, s>>>(a, p.side, T);
+        else if (p.waves <= 4)
+            norm_grad_kernel<XT, MODE, 4, LN><<<grid, p.threads(), 0, s>>>(a, p.side, T);
+        else if (p.waves <= 8)
+            norm_grad_kernel<XT, MODE, 8, LN><<<grid, p.threads(), 0, s>>>(a, p.side, T);
         else
-            norm_grad_kernel<XT, MODE, 1, false, LN><<<grid, p.threads, 0, s>>>(a);
+            norm_grad_kernel<XT, MODE, 16, LN><<<grid, p.threads(), 0, s>>>(a, p.side, T);
         if (count == 1)
             return hipGetLastError();
     }
