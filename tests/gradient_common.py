@@ -21,8 +21,8 @@ def chain(k):
 
 
 def rows_chain(m):
-    """Roundings of a term in a sum over m rows: a workgroup's own rows, the
-    rows of a workgroup (8), the parts' 32, their 16 slices."""
+    """Roundings of a term in a sum over m rows: a workgroup's own rows (of
+    256), the rows side by side (at most 16), every 32nd part (8), the 32 sums of these."""
     return m / 64 + 64
 
 
