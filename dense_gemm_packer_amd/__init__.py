@@ -1,7 +1,7 @@
 """Python binding of the gfx950 preshuffled-B GEMM library (libdgp.so).
 
 Argument marshalling only, through ctypes; the one-pass products and the
-operators that write their operands go through a small native module
+operators that write their operands, and the gradients, go through a small native module
 (csrc/torch_binding.cpp, _binding.so), whose calls cost less on the host.
 Every computation runs in the HIP kernels behind the C ABI declared in
 include/dgp.h.  torch supplies device memory (outputs are allocated as torch
@@ -34,7 +34,7 @@ BINDING_PATH = os.path.join(_HERE, "_binding.so")
 BF16 = 0
 FP8_E4M3 = 1
 FP4_E2M1 = 2
-F16 = 3      # inputs of the quantising operators only
+F16 = 3      # inputs of the quantising operators and the gradients only
 F32 = 4
 SCALE_NONE = 0
 SCALE_TENSOR = 1

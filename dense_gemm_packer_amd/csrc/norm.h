@@ -11,7 +11,7 @@ namespace dgp {
 // Sums of N values over the T threads of a row (64: one wave), in every thread.
 // `red` holds N x T / 64 partial sums in LDS; a second call takes another array.
 // (TOTAL: without LDS inside a wave, in another order; one row of 7168 to mxfp8
-// with two such sums 4.6 us.)
+// with two such sums 3.3 us.)
 template <int T, bool TOTAL, int N>
 __device__ inline void row_sums(float (&v)[N], float (*red)[T / 64])
 {

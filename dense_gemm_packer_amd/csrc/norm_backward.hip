@@ -13,7 +13,10 @@
 // The sums over rows: a workgroup owns every G-th row and keeps its sums in
 // registers (a thread has the same columns of every row), writes them once, and
 // a second kernel adds the G partial sums in order: no atomics, the same bits in
-// every run.
+// every run.  HBM-bound where rows are many (4096 x 8192 bf16 with a residual, x an
+// 8-bit checkpoint with block scales: 236 MB in 44 us, 5.4 TB/s, and 5 us for the
+// partial sums; 16 391 x 2048 mxfp8 without means 235 MB in 35 and 4), latency where
+// they are few (128 x 7168: 6 and 2 to 3 us).
 #include <algorithm>
 
 #include "common.h"

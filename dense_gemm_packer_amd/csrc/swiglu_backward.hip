@@ -50,7 +50,8 @@ __device__ inline void grads8(const float (&dy)[8], const float (&g)[8], const f
 }  // namespace
 
 // Thread = 8 consecutive elements of dy, gate and up.  HBM-bound: reads each
-// once, writes both gradients once.
+// once, writes both gradients once (16 391 x 2048 bf16, gate and up an mxfp8
+// checkpoint: 269 MB in 40 us, 6.7 TB/s; 128 x 2048 in 2.9 us, a launch).
 template <int XT, int MODE>
 __global__ __launch_bounds__(256) void swiglu_grad_kernel(const SwigluGradArgs a)
 {

