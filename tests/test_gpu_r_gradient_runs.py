@@ -159,6 +159,59 @@ def test_micro_batches_add_up():
     assert equal(out, d.t() @ xv)
 
 
+# --------------------------------------------------- places and sizes
+
+@pytest.mark.parametrize("k", [256, 8192, 8256, 40960])
+@pytest.mark.parametrize("m", [1, 5, 300])
+def test_layernorm_onto_its_input(m, k):
+    """Q (bf16) in X's own rows and in the residual's, the new stream in the other: also rows read more than once."""
+    x, r = (activations(m, k, torch.bfloat16, s, mean=3.0).to(DEV) for s in (81, 82))
+    w = torch.full((k,), 0.75, dtype=torch.bfloat16, device=DEV)
+    want, _, h = dgp.layernorm_quantize(x, w, w, dgp.SCALE_NONE, residual=r)
+    for swap in (False, True):
+        x1, r1 = x.clone(), r.clone()
+        out, stream = (r1, x1) if swap else (x1, r1)
+        Q, _, H = dgp.layernorm_quantize(x1, w, w, dgp.SCALE_NONE, residual=r1, out=out, residual_out=stream)
+        assert same(Q, want) and same(H, h) and Q is out and H is stream
+
+
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("k", [64, 512, 1280, 8192, 8256, 16448])
+@pytest.mark.parametrize("m", [1, 300])
+def test_norm_gradient_onto_its_inputs(layer, k, m):
+    """dX in the residual gradient's place; where rows are read once, in dY's and in X's."""
+    x, dy, r = (activations(m, k, torch.bfloat16, s).to(DEV) for s in (83, 84, 85))
+    w = torch.full((k,), 0.75, dtype=torch.bfloat16, device=DEV)
+    f = dgp.layernorm_backward if layer else dgp.rmsnorm_backward
+    want = f(dy, x, w, residual_grad=r)
+    for place in "ryx":
+        t = dict(x=x.clone(), y=dy.clone(), r=r.clone())
+        call = lambda: f(t["y"], t["x"], w, residual_grad=t["r"], dx=t[place])  # noqa: E731, B023
+        if place != "r" and k > 8192:
+            with pytest.raises(dgp.DgpError, match="overlap"):
+                call()
+            continue
+        got = call()
+        assert got[0] is t[place] and all(same(a, b) for a, b in zip(got, want))
+    both = f(dy, x, w, residual_grad=dy)
+    t = dy.clone()
+    if k <= 8192:                      # one tensor as three
+        assert all(same(a, b) for a, b in zip(f(t, x, w, residual_grad=t, dx=t), both))
+
+
+def test_nothing_to_do():
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    assert tuple(dgp.swiglu_backward(z(0, 256), z(0, 256), z(0, 256)).shape) == (0, 512)
+    assert tuple(dgp.swiglu_backward(z(4, 0), z(4, 0), z(4, 0)).shape) == (4, 0)
+    assert tuple(dgp.layernorm_quantize(z(0, 256), z(256), None, dgp.SCALE_MX128)[0].shape) == (0, 256)
+    for f in (dgp.layernorm_backward, dgp.rmsnorm_backward):
+        assert tuple(f(z(4, 0), z(4, 0), z(0))[0].shape) == (4, 0)
+    one = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert tuple(dgp.gemm_wgrad(z(4, 32), z(4, 64), offsets=one).shape) == (0, 32, 64)
+    assert tuple(dgp.gemm_wgrad(z(4, 0), z(4, 64)).shape) == (0, 64)
+    assert tuple(dgp.gemm_wgrad(z(4, 32), z(4, 0)).shape) == (32, 0)
+
+
 # -------------------------------------------- threads, streams and graphs
 
 def results(o):
