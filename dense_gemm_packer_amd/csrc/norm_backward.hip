@@ -450,7 +450,7 @@ struct Shape {
 };
 Shape shape_of(int64_t M, int64_t K)
 {
-    const int waves = (int)((K / 8 + 63) / 64);
+    const int waves = (int)((K + 511) / 512);
     return {(int)std::min<int64_t>(16 / waves, (M + 127) / 128), waves};
 }
 

@@ -96,6 +96,14 @@ def test_norm_backward_workspace(L, layer):
 
 
 @both
+def test_norm_backward_workspace_of_any_size(L, layer):
+    """The query takes what the operator would refuse: lengths that are no multiple of 64, down to one element."""
+    for k in (1, 7, 8, 9, 63, 65, 511, 513, 8191, 8193):
+        for m in (1, 2, 127, 1 << 30):
+            assert 0 <= L.dgp_norm_backward_workspace_bytes(m, k, layer) <= (256 * 2 * k + 4 * m) * 4
+
+
+@both
 @pytest.mark.parametrize("kw", [
     # dX over a shifted or strided dY, R or X, over codes, the weight or the scales
     dict(D=Y + 512), dict(D=Y, ldy=512), dict(D=X + 512), dict(D=X, ldx=512), dict(D=R + 16, R=R, ldr=256), dict(D=R, R=R, ldr=512),
