@@ -16,18 +16,19 @@
 //
 // e4m3 codes become bf16 on their way into LDS.  An E8M0 scale times a code is
 // exact in bf16 (one converting instruction); a per-tensor scale multiplies the
-// sum at the end; a code times an fp32 block scale is rounded to bf16, which is
-// a sixteenth of the code's own step (bf16 C: as fine as C's own rounding), or
-// kept as a sum of two bf16 numbers, 2^-17 relative, and multiplied twice
-// (fp32 C).
+// sum at the end; a code times an fp32 block scale is kept as a sum of two bf16
+// numbers, 2^-17 relative, and multiplied twice, whatever C's type: one of them
+// would put 2^-9 more into every product, as much as a bf16 C's own rounding
+// (32 experts of 585 to 2933 rows: 1.98e-3 from 64 bits, where exact operands
+// give 1.66e-3).
 //
 // Pipeline, per step of 32 rows: the fragments of step s are in registers while
 // those of s + 1 are read from LDS, the codes of s + 2 are converted and the
 // copies of s + kD are sent off, all of it placed between the products by hand
 // (one wave per SIMD: nothing else hides a stall).  One barrier a step.
 // Bound by the matrix pipes and the chip's power: 8192 rows, 8192 x 4096, bf16
-// 393-418 us by card (1.32-1.40 PFLOP/s), mxfp8 to fp32 425-456, block scales to
-// bf16 450-476, to fp32 with two products 830; 32 experts of 585 to 2933 rows, 4096 x 2048, 640-665.
+// 393-418 us by card (1.32-1.40 PFLOP/s), mxfp8 to fp32 425-456, block scales,
+// with two products, 800-830; 32 experts of 585 to 2933 rows, 4096 x 2048, block scales to bf16, 994.
 #include <algorithm>
 #include <cmath>
 
@@ -118,7 +119,7 @@ __device__ inline void multiply_add(f32x4 &acc, const i32x4 &x, const i32x4 &y)
 // Two codes (the low or the HIGH half of four) -> two bf16 values.  `scale`: E8M0
 // byte or fp32 bits.  `low` (block scales): what the rounding to bf16 left over,
 // rounded to bf16 itself.
-template <int MODE, bool HIGH, bool LOW>
+template <int MODE, bool HIGH>
 __device__ inline uint32_t widen(int codes, uint32_t scale, uint32_t &low)
 {
     if constexpr (MODE == kScaleBlock) {
@@ -126,8 +127,7 @@ __device__ inline uint32_t widen(int codes, uint32_t scale, uint32_t &low)
         const auto c = __builtin_amdgcn_cvt_pk_f32_fp8(codes, HIGH);
         const float v[2] = {c[0] * s, c[1] * s};
         const uint32_t w = pack_bf16x2(v[0], v[1]);
-        if constexpr (LOW)
-            low = pack_bf16x2(v[0] - __builtin_bit_cast(float, w << 16), v[1] - __builtin_bit_cast(float, w & 0xFFFF0000u));
+        low = pack_bf16x2(v[0] - __builtin_bit_cast(float, w << 16), v[1] - __builtin_bit_cast(float, w & 0xFFFF0000u));
         return w;
     } else {
         // the instruction takes the exponent field of its fp32 scale: 2^(e - 127), NaN for e = 255
@@ -143,8 +143,8 @@ __device__ inline uint32_t widen(int codes, uint32_t scale, uint32_t &low)
 // gets every eighth run of 2^chunk_log2 neighbouring tiles (one group: one run): neighbours share their
 // operands' panels in its L2, and each XCD has its part of every group, which
 // groups of unequal size need (32 groups of 585 to 2933 rows, N 4096, K 2048,
-// block scales by row list: 997 us with four whole groups an XCD, 790 where all
-// have 1024).  Tiles behind the last whole round keep their number.
+// block scales by row list, one product: 997 us with four whole groups an XCD, 790
+// where all have 1024).  Tiles behind the last whole round keep their number.
 struct Tile {
     int n, k, s;
 };
@@ -173,10 +173,11 @@ __device__ inline Tile tile_at(uint32_t wg, uint32_t tiles_n, uint32_t tiles_k, 
 }
 
 // F: fragments of a wave along n and along k (4 waves, 2 x 2: a tile of 32 F).
-template <int MODE, int TERMS, int F, bool GATHER, bool BF16>
+template <int MODE, int F, bool GATHER, bool BF16>
 __global__ __launch_bounds__(256, F == 8 ? 1 : 2) void wgrad_kernel(const WgradArgs a, const int tiles_n, const int tiles_k, const int chunk_log2)
 {
     constexpr bool kCodes = MODE != kScaleNone;
+    constexpr int TERMS = MODE == kScaleBlock ? 2 : 1;   // bf16 numbers that make up a value of x
     constexpr bool kScaled = MODE == kScaleBlock || MODE == kScaleMx;
     constexpr int kCols = 32 * F;                        // tile
     constexpr int H = F / 4;                             // 128-column halves
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(256, F == 8 ? 1 : 2) void wgrad_kernel(const WgradA
     auto convert = [&](auto vc, const i32x4 &c, uint32_t s, int x_slot) {
         constexpr int j = decltype(vc)::value / 8, v = decltype(vc)::value % 8;
         uint32_t low = 0;
-        wide[0][v % 4] = (int)widen<MODE, v % 2 == 1, TERMS == 2>(c[v / 2], s, low);
+        wide[0][v % 4] = (int)widen<MODE, v % 2 == 1>(c[v / 2], s, low);
         if constexpr (TERMS == 2)
             wide[1][v % 4] = (int)low;
         if constexpr (v % 4 == 3) {
@@ -594,7 +595,7 @@ WgradPlan wgrad_plan(int64_t M, int64_t N, int64_t K, int64_t E)
 
 namespace {
 
-template <int MODE, int TERMS, int F, bool BF16>
+template <int MODE, int F, bool BF16>
 void launch_tile(const WgradArgs &a, hipStream_t s)
 {
     const int64_t tile = 32 * F, tn = (a.N + tile - 1) / tile, tk = (a.K + tile - 1) / tile;
@@ -604,19 +605,19 @@ void launch_tile(const WgradArgs &a, hipStream_t s)
     while (chunk < 5 && tn * tk >= (int64_t)kNumXcd << (chunk + 1))
         ++chunk;
     if (a.rows)
-        wgrad_kernel<MODE, TERMS, F, true, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk, chunk);
+        wgrad_kernel<MODE, F, true, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk, chunk);
     else
-        wgrad_kernel<MODE, TERMS, F, false, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk, chunk);
+        wgrad_kernel<MODE, F, false, BF16><<<grid, 256, 0, s>>>(a, (int)tn, (int)tk, chunk);
 }
 
 template <int F, bool BF16>
 hipError_t launch_mode(const WgradArgs &a, int mode, hipStream_t s)
 {
     switch (mode) {
-    case kScaleNone: launch_tile<kScaleNone, 1, F, BF16>(a, s); break;
-    case kScaleTensor: launch_tile<kScaleTensor, 1, F, BF16>(a, s); break;
-    case kScaleBlock: launch_tile<kScaleBlock, BF16 ? 1 : 2, F, BF16>(a, s); break;
-    case kScaleMx: launch_tile<kScaleMx, 1, F, BF16>(a, s); break;
+    case kScaleNone: launch_tile<kScaleNone, F, BF16>(a, s); break;
+    case kScaleTensor: launch_tile<kScaleTensor, F, BF16>(a, s); break;
+    case kScaleBlock: launch_tile<kScaleBlock, F, BF16>(a, s); break;
+    case kScaleMx: launch_tile<kScaleMx, F, BF16>(a, s); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();

@@ -479,7 +479,7 @@ size_t dgp_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E);
  *
  * Products are those of bf16 numbers, summed in fp32 (subnormal ones may count as zero).  bf16,
  * per-tensor and E8M0 scales: exactly dC and x (a per-tensor scale multiplies the sum).  Block scales:
- * x is rounded to bf16 for a bf16 dB, and taken to 2^-17 of its value for an fp32 one.
+ * x is taken to 2^-17 of its value, as a sum of two bf16 numbers (beyond bf16's largest, 3.39e38: NaN).
  *
  * Requires N % 16 == 0, K % 64 == 0 (e4m3: K % 128 == 0), every pointer 16-byte aligned (offsets, rows and fp32
  * scales 4-byte; E8M0 any), ldc * 2 % 16 == 0, N, K <= 2^22, ldc <= 2^25, E <= 65535; x_rows >= M, or with a row list any
