@@ -1374,7 +1374,9 @@ dgp_status dgp_gemm_wgrad(const void *dC, int64_t ldc, const void *X, int64_t x_
     WgradArgs a{};
     a.Y = dC, a.X = X, a.S = S, a.C = dB, a.ws = ws;
     a.offsets = offsets, a.rows = M > 0 ? rows : nullptr;
-    a.ldy = ldc, a.M = M, a.N = N, a.K = K, a.E = E, a.x_rows = x_rows;
+    // (the kernel's range of dC's last row on ends before it begins where there are no rows, with strides from N on)
+    a.ldy = M > 0 ? ldc : N;
+    a.M = M, a.N = N, a.K = K, a.E = E, a.x_rows = x_rows;
     a.accumulate = accumulate;
     return hip_status(launch_wgrad(a, scale_mode, out_type == DGP_BF16, plan, (hipStream_t)stream), "weight gradient launch");
 }

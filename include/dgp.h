@@ -475,7 +475,8 @@ size_t dgp_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E);
  * (DGP_BF16, or DGP_FP8_E4M3 with the scales S of DGP_SCALE_TENSOR, BLOCK128 or MX128),
  * dense.  offsets and rows as there; offsets NULL: one weight (E = 1) and all M rows.  dB is [E][N][K]
  * row-major (not preshuffled), fp32 or, out_type DGP_BF16, rounded once; a weight without
- * rows gets zeros.  accumulate (fp32 only): added to what dB holds.
+ * rows gets zeros (M = 0: all of them; dC, X, S and rows may be NULL and ldc is not looked at).  accumulate
+ * (fp32 only): added to what dB holds.
  *
  * Products are those of bf16 numbers, summed in fp32 (subnormal ones may count as zero).  bf16,
  * per-tensor and E8M0 scales: exactly dC and x (a per-tensor scale multiplies the sum).  Block scales:
