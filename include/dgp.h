@@ -453,6 +453,7 @@ dgp_status dgp_rmsnorm_backward(const void *dY, int64_t ldy, int type, const voi
 
 /* dgp_swiglu_backward -- with s = 1 / (1 + exp(-g)), elementwise:
  *   dg = dy u s (1 + g (1 - s)),  du = dy g s
+ * to 20 half steps of fp32 (dg: of dy u s |g (1 - s)| where its terms cancel) before the rounding to `type`.
  * D is `type` [M][2 K]: dg in columns 0 .. K-1 and du behind it, the gradient of one product's columns
  * that held gate and up side by side.  SG and SU: the scales of gate and of up, rows ldsg and ldsu
  * scales apart (DGP_SCALE_TENSOR: one value each, may be the same one); the halves of one
