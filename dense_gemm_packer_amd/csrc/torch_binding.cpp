@@ -286,6 +286,9 @@ struct Operand {
         }
     }
 
+    // Whether allocate() has nothing to do.
+    bool given(int mode) const { return Q.defined() && (S.defined() || scale.defined() || mode == DGP_SCALE_NONE); }
+
     void allocate(const Tensor &X, int mode)
     {
         if (!Q.defined())
@@ -423,7 +426,7 @@ PyObject *norm_quantize(PyObject *const *a, bool layer)
         dense(H, X.scalar_type(), X.sizes(), X, "residual_out");
     }
     on_device(X, "X");
-    Place place(X, a[9]);
+    Place place(X, a[9], !o.given(mode) || (R.defined() && !H.defined()));
     o.allocate(X, mode);
     if (R.defined() && !H.defined())
         H = empty(X.sizes(), X.scalar_type(), X);
@@ -745,7 +748,7 @@ PyObject *swiglu_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (D.defined())
         dense(D, Y.scalar_type(), shape, Y, "out");
     on_device(Y, "dY");
-    Place place(Y, a[7]);
+    Place place(Y, a[7], !D.defined());
     if (!D.defined())
         D = empty(shape, Y.scalar_type(), Y);
     call(abi.swiglu_grad, (const void *)Y.data_ptr(), ldy, code, G.values(), G.ld, U.values(), U.ld, G.scales(), G.lds,
