@@ -17,7 +17,8 @@ namespace {
 
 // exp(x) = 2^t (1 + r ln 2) with t the fp32 product x log2(e) and r what t is off
 // by: 2^t alone is off by |x| half steps (16 391 x 2048 from mxfp8 41.3 us with r and
-// 40.3 without, bf16 52.8 and 53.2, 8195 x 2048 fp32 58.8 and 57.9).  x from where exp(x) is 0 on up to where it is infinite.
+// 40.3 without, bf16 52.8 and 53.2, 8195 x 2048 fp32 58.8 and 57.9).  For finite x
+// below where exp(x) is infinite.
 __device__ inline float exponential(float x)
 {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f;   // log2(e) to 2^-50
@@ -38,8 +39,8 @@ __device__ inline void grads(float dy, float g, float u, float &dg, float &du)
 }
 
 // Gates below -80: there s is exp(g) and 1 - s is 1 to 2^-115; exp(g) goes in
-// as four factors exp(g / 4), so that no product leaves the normal range
-// before the results do.
+// as four factors exp(g / 4), between dy and u, so that with those of ordinary
+// size no product leaves the normal range before the results do.
 constexpr uint32_t kFar = 0xC2A00000u;     // -80.0f; more negative numbers have larger bits
 
 template <int XT, int MODE>

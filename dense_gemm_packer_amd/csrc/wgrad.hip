@@ -26,9 +26,13 @@
 // those of s + 1 are read from LDS, the codes of s + 2 are converted and the
 // copies of s + kD are sent off, all of it placed between the products by hand
 // (one wave per SIMD: nothing else hides a stall).  One barrier a step.
-// Bound by the matrix pipes and the chip's power: 8192 rows, 8192 x 4096, bf16
-// 393-418 us by card (1.32-1.40 PFLOP/s), mxfp8 to fp32 425-456, block scales,
-// with two products, 800-830; 32 experts of 585 to 2933 rows, 4096 x 2048, block scales to bf16, 994.
+// bf16 is bound by the matrix pipes (72 % busy) and the chip's power: 8192 rows,
+// 8192 x 4096, 393-418 us by card (1.32-1.40 PFLOP/s).  mxfp8 to fp32 418-456 us
+// (478 under a profiler): the conversion, which every workgroup along n does again,
+// puts 375 cycles on the 1427 of a step (pipes 57 % busy; on zeros, where power
+// does not bind, 396 us and bf16 314).  Block scales, with two products, 800-836;
+// 32 experts of 585 to 2933 rows, 4096 x 2048, block scales to bf16, 994-1018
+// (1109 under a profiler).
 #include <algorithm>
 #include <cmath>
 
@@ -564,8 +568,12 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float *ws, void *
 //   parts: 3.6 + out / 6.4 for adding them up
 //
 // fitted to graph timings of 58 shapes (64 to 20000 rows, 256 x 256 to 8192 x 8192,
-// 1 to 64 groups, up to 14 choices each): the choice is on average 0.6 % slower
-// than the fastest (at worst 14 %: 2048 rows, 512 x 1024).  The 128 tile reads twice
+// 1 to 64 groups, up to 14 choices each): the choice is on average 0.5 % slower
+// than the fastest (at worst 14 %: 2048 rows, 512 x 1024).  Groups count as even,
+// as those of the fit were: the host does not know their rows, and a group that
+// has most of them gets no more parts than the others (16 384 rows of 64 experts of
+// 1024 x 1024, nearly all of one: 16 workgroups walk them, about 370 us by the
+// formula above where that weight alone in 16 parts is at 54).  The 128 tile reads twice
 // the bytes for a product, 14 TB/s out of the L2s with four workgroups a CU (1.2 us
 // for a step of theirs, where the 256 tile takes 0.7 for the same products); it is
 // there for weights with too few large tiles, as parts are (8192 rows, 2048 x 2048:

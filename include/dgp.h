@@ -399,7 +399,8 @@ dgp_status dgp_swiglu_quantize(const void *G, int64_t ldg, const void *U, int64_
  * / sqrt(var + eps) * w + b over each row, var the mean of (h - mean)^2; Q, S
  * and H as there.  w, and b where not NULL, have K values of w_type (x_type or
  * DGP_F32).  Squares are summed in fp32, about the mean: for rows that spread
- * over more than about 1e19 y is b, with eps = 0 a row of equal values is 0 / 0. */
+ * over more than about 1e19 y is b, with eps = 0 a row of equal values is 0 / 0;
+ * a row whose sum passes 3.4e38 is NaN. */
 dgp_status dgp_layernorm_quantize(const void *X, int64_t ldx, const void *R, int64_t ldr, int x_type, const void *W,
                                   const void *B, int w_type, float eps, void *Q, void *S, const float *scale, void *H,
                                   int64_t M, int64_t K, int scale_mode, void *stream);
@@ -417,7 +418,10 @@ dgp_status dgp_layernorm_quantize(const void *X, int64_t ldx, const void *R, int
  *   DGP_SCALE_MX128     e4m3, S E8M0 [M][K/128].
  * so what dgp_quantize writes serves as an 8-bit checkpoint, and the operand of
  * the forward product as its own.  A gradient is that of the formula at the
- * values which the checkpoint holds.
+ * values which the checkpoint holds.  The norms' sums over a row are fp32, as
+ * forward: a row whose squares (layer norm: about the mean) pass 3.4e38 has xhat
+ * 0 and no gradient of its own; where its sum (layer norm) or that of its
+ * products with g passes that, dx of the row and the sums over rows are NaN.
  *
  * Inputs are rows ld* elements apart (ld* >= K; e4m3: bytes), each 16-byte
  * aligned, of K elements: K % 64 == 0, with e4m3 K % 128 == 0; at most 2^23
@@ -438,7 +442,8 @@ size_t dgp_norm_backward_workspace_bytes(int64_t M, int64_t K, int layer);
  * x: the forward norm's h (its input, or with a residual the stream's new value).  r, where R is
  * not NULL: a gradient to add, that of the residual stream.  dx is `type` [M][K], dw and db
  * (NULL: not wanted) fp32 [K].  w has K values of `type` or DGP_F32.  With dense
- * rows dx may be R itself, and where K <= 8192 (longer rows are read twice) dy or (DGP_SCALE_NONE) X. */
+ * rows dx may be R itself, and where K <= 8192 dy or (DGP_SCALE_NONE) X (of longer rows dy and x are read
+ * four times, without the means three times). */
 dgp_status dgp_layernorm_backward(const void *dY, int64_t ldy, int type, const void *X, int64_t ldx, const void *S,
                                   int scale_mode, const void *W, int w_type, const void *R, int64_t ldr, float eps,
                                   void *dX, float *dW, float *dB, int64_t M, int64_t K, float *ws, size_t ws_bytes,
@@ -453,7 +458,8 @@ dgp_status dgp_rmsnorm_backward(const void *dY, int64_t ldy, int type, const voi
 
 /* dgp_swiglu_backward -- with s = 1 / (1 + exp(-g)), elementwise:
  *   dg = dy u s (1 + g (1 - s)),  du = dy g s
- * to 20 half steps of fp32 (dg: of dy u s |g (1 - s)| where its terms cancel) before the rounding to `type`.
+ * to 20 half steps of fp32 (dg: of dy u s |g (1 - s)| where its terms cancel) before the rounding to `type`,
+ * as long as dy s and the products that follow are normal numbers.
  * D is `type` [M][2 K]: dg in columns 0 .. K-1 and du behind it, the gradient of one product's columns
  * that held gate and up side by side.  SG and SU: the scales of gate and of up, rows ldsg and ldsu
  * scales apart (DGP_SCALE_TENSOR: one value each, may be the same one); the halves of one
